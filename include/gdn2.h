@@ -29,7 +29,7 @@
 extern "C" {
 #endif
 
-#define GDN2_ABI_VERSION 5
+#define GDN2_ABI_VERSION 6
 
 /* Element types a tensor descriptor may carry. */
 typedef enum gdn2_dtype {
@@ -64,7 +64,8 @@ enum {
     GDN2_ERR_UNSUPPORTED = -5, /* K or V not 64 or 128 (the backward: K != V), or an option out of range */
     GDN2_ERR_LAYOUT = -6,      /* a tensor's strides or alignment are not accepted */
     GDN2_ERR_ALIAS = -7,       /* an output overlaps an input */
-    GDN2_ERR_HIP = -8          /* the HIP runtime reported an error */
+    GDN2_ERR_HIP = -8,         /* the HIP runtime reported an error */
+    GDN2_ERR_WORKSPACE = -9    /* a caller's workspace is missing, too small or not aligned */
 };
 
 /*
@@ -411,6 +412,223 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
                          const gdn2_tensor *dv, const gdn2_tensor *dg,
                          const gdn2_tensor *dbeta, const gdn2_tensor *dw,
                          const gdn2_tensor *d_initial_state);
+
+/* ------------------------------------------------ scalar-gated delta rule --
+ *
+ * The gated delta rule with one decay and one gate per token and head, the
+ * case g constant over the channels and w = beta = one scalar of the rule
+ * above (FlashInfer chunk_gated_delta_rule2 docs: the reduction to the
+ * scalar rule): per sequence and value head, with a K x V float32 state S,
+ *
+ *     S_t  = exp(g_t) S_{t-1}
+ *     u_t  = beta_t (v_t - S_t^T k_t)
+ *     S_t += k_t u_t^T
+ *     o_t  = scale * q_t^T S_t
+ *
+ * gdn2_delta_chunk_fwd evaluates it in 64-token chunks (prefill, training),
+ * gdn2_delta_recurrent_fwd token by token (decode and short spans), and
+ * gdn2_delta_chunk_bwd computes the gradients. Tensors as in gdn2_chunk_fwd
+ * but for the gates:
+ *   q, k  [T, H, K], v, out [T, HV, V]   bf16 or float16, one io type
+ *   g     [T, HV]   float32, bf16 or float16; natural log of the decay, <= 0
+ *                   and finite (precondition, not checked); NULL: 0
+ *   beta  [T, HV]   io type, taken as given; NULL: 1
+ *   initial_state, final_state [N, HV, K, V] float32 or bf16 (or V-major by
+ *                   option), cu_seqlens [N + 1] int32 or int64
+ * with the same defaults for NULL arguments and scale, the same sizes (K and
+ * V each 64 or 128, HV a multiple of H), the same preconditions on cu_seqlens
+ * and conditioning, and the same layouts; g and beta may have any
+ * non-negative strides (elements) and need only their element's alignment.
+ * opts: state_layout and qk_l2norm as for gdn2_chunk_fwd_opts (NULL:
+ * defaults); the chunked entry runs whole sequences and refuses
+ * seq_split_chunks > 0 (GDN2_ERR_UNSUPPORTED), the recurrent one ignores it.
+ * N * HV and (T / 64 + N) * HV may reach 8388607 (GDN2_ERR_SHAPE beyond).
+ *
+ * Accuracy: every product runs on bf16 MFMA with float32 accumulation and
+ * float32 operands taken in two bf16 parts (16 significant bits), the state
+ * and all sums in float32. Float32 results (final_state, dg,
+ * d_initial_state) are within about 1e-5 of a float64 evaluation, relative
+ * in the 2-norm, on unit-norm keys; 16-bit results are rounded once.
+ *
+ * Workspace: these entries allocate nothing and keep nothing between calls.
+ * The caller passes device memory of at least the number of bytes that the
+ * entry's _workspace function gives (0: NULL is accepted), 256-byte aligned
+ * and apart from every tensor (GDN2_ERR_WORKSPACE, GDN2_ERR_ALIAS). Its
+ * contents before the call do not matter and are undefined after it; it may
+ * be reused once the call's work on the stream is done. Calls that can
+ * overlap in time need workspaces of their own. Every entry may be captured
+ * into a graph; a graph's workspace belongs to that graph's replays.
+ *
+ * Asynchronous, deterministic (no atomics), reentrant. Errors as
+ * gdn2_chunk_fwd. Each _check function is the host-side validation alone,
+ * without the workspace: no HIP call, no device memory.
+ */
+
+/* Bytes of workspace of gdn2_delta_chunk_fwd: (T / 64 + N) * HV * 26368. */
+int64_t gdn2_delta_chunk_fwd_workspace(int64_t T, int32_t N, int32_t HV);
+
+/* The chunked forward. final_state may not alias initial_state. */
+int gdn2_delta_chunk_fwd(const gdn2_tensor *q, const gdn2_tensor *k,
+                         const gdn2_tensor *v, const gdn2_tensor *g,
+                         const gdn2_tensor *beta, float scale,
+                         const gdn2_tensor *initial_state,
+                         const gdn2_tensor *cu_seqlens, const gdn2_tensor *out,
+                         const gdn2_tensor *final_state,
+                         const gdn2_fwd_options *opts, void *workspace,
+                         int64_t workspace_bytes, hipStream_t stream);
+int gdn2_delta_chunk_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
+                               const gdn2_tensor *v, const gdn2_tensor *g,
+                               const gdn2_tensor *beta, float scale,
+                               const gdn2_tensor *initial_state,
+                               const gdn2_tensor *cu_seqlens,
+                               const gdn2_tensor *out,
+                               const gdn2_tensor *final_state,
+                               const gdn2_fwd_options *opts);
+
+/* Token by token, without a workspace: every state is read and written once
+ * per call. final_state may be initial_state's own buffer (same pointer and
+ * type) to update the state in place. */
+int gdn2_delta_recurrent_fwd(const gdn2_tensor *q, const gdn2_tensor *k,
+                             const gdn2_tensor *v, const gdn2_tensor *g,
+                             const gdn2_tensor *beta, float scale,
+                             const gdn2_tensor *initial_state,
+                             const gdn2_tensor *cu_seqlens,
+                             const gdn2_tensor *out,
+                             const gdn2_tensor *final_state,
+                             const gdn2_fwd_options *opts, hipStream_t stream);
+int gdn2_delta_recurrent_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
+                                   const gdn2_tensor *v, const gdn2_tensor *g,
+                                   const gdn2_tensor *beta, float scale,
+                                   const gdn2_tensor *initial_state,
+                                   const gdn2_tensor *cu_seqlens,
+                                   const gdn2_tensor *out,
+                                   const gdn2_tensor *final_state,
+                                   const gdn2_fwd_options *opts);
+
+/*
+ * The backward of gdn2_delta_chunk_fwd (without qk_l2norm; see
+ * gdn2_qk_norm_rope_bwd for the norm's gradient). Every tensor dense and
+ * 16-byte aligned; q, k, v, g, beta, d_out required; (K, V) = (64, 64) or
+ * (128, 128); states K-major float32 (initial_state and d_final_state NULL:
+ * zero; d_initial_state NULL: not written). dq, dk (summed over the value
+ * heads that read each q/k head), dv and dbeta have q's type, dg g's.
+ * Workspace: per (chunk, value head) 26368 + 8 K V + 528 V bytes, plus
+ * 8 T HV K with grouped heads (HV > H), each part rounded up to 256 bytes.
+ */
+int64_t gdn2_delta_chunk_bwd_workspace(int64_t T, int32_t N, int32_t H,
+                                       int32_t HV, int32_t K, int32_t V);
+int gdn2_delta_chunk_bwd(const gdn2_tensor *q, const gdn2_tensor *k,
+                         const gdn2_tensor *v, const gdn2_tensor *g,
+                         const gdn2_tensor *beta, float scale,
+                         const gdn2_tensor *initial_state,
+                         const gdn2_tensor *cu_seqlens,
+                         const gdn2_tensor *d_out,
+                         const gdn2_tensor *d_final_state,
+                         const gdn2_tensor *dq, const gdn2_tensor *dk,
+                         const gdn2_tensor *dv, const gdn2_tensor *dg,
+                         const gdn2_tensor *dbeta,
+                         const gdn2_tensor *d_initial_state, void *workspace,
+                         int64_t workspace_bytes, hipStream_t stream);
+int gdn2_delta_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
+                               const gdn2_tensor *v, const gdn2_tensor *g,
+                               const gdn2_tensor *beta, float scale,
+                               const gdn2_tensor *initial_state,
+                               const gdn2_tensor *cu_seqlens,
+                               const gdn2_tensor *d_out,
+                               const gdn2_tensor *d_final_state,
+                               const gdn2_tensor *dq, const gdn2_tensor *dk,
+                               const gdn2_tensor *dv, const gdn2_tensor *dg,
+                               const gdn2_tensor *dbeta,
+                               const gdn2_tensor *d_initial_state);
+
+/* ---------------------------------------- norms and rotation of q and k --
+ *
+ * What a model does to q and k before the rule, both in one launch: every
+ * (token, head) row x of K elements becomes
+ *
+ *     z = x * r * weight,   r = 1 / max(|x|, eps)           (L2, the default)
+ *                           r = 1 / sqrt(mean(x^2) + eps)   (RMS)
+ *                           r = 1                           (NONE)
+ *     y = z with its first rot elements turned by the token's position: each
+ *         pair (a, b) becomes (a cos - b sin, a sin + b cos)
+ *
+ * in float32, rounded once. L2 with eps 1e-12 and no weight is what
+ * qk_l2norm does in the forward entries; here it has a backward. A rotation
+ * keeps a row's norm, so the rule's conditioning is that of the norm alone.
+ *
+ *   q [T, H, K], k [T, HK, K]   bf16 or float16 (one io type), K 64 or 128
+ *   q_weight, k_weight [K]      float32 or the io type; NULL: 1
+ *   rope [P, rot]               float32: rot / 2 cosines, then rot / 2 sines
+ *                               of each position's angles (any frequencies and
+ *                               scaling); NULL: no rotation. rot a multiple of
+ *                               16, or of 2 with interleaved, at most K
+ *   positions [T]               int32 or int64, in [0, P) (precondition, not
+ *                               checked on the device: others read the
+ *                               table's first or last row); with rope only
+ *   q_out, k_out                q's and k's shapes and type
+ * Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved. Rows as in
+ * gdn2_chunk_fwd (token and head strides free, 16-byte multiples); weights,
+ * table and positions dense and 16-byte aligned. Outputs may not overlap an
+ * input or each other (their spans, also of interleaved views).
+ */
+enum {
+    GDN2_QK_NORM_NONE = 0,
+    GDN2_QK_NORM_L2 = 1,
+    GDN2_QK_NORM_RMS = 2
+};
+
+/* struct_size: sizeof(gdn2_qk_options). NULL options: L2, 1e-12, halves. */
+typedef struct gdn2_qk_options {
+    int32_t struct_size;
+    int32_t norm;        /* GDN2_QK_NORM_* */
+    int32_t interleaved; /* 0 or 1 */
+    float eps;           /* 0: 1e-12 (L2) or 1e-6 (RMS) */
+} gdn2_qk_options;
+
+int gdn2_qk_norm_rope_fwd(const gdn2_tensor *q, const gdn2_tensor *k,
+                          const gdn2_tensor *q_weight,
+                          const gdn2_tensor *k_weight, const gdn2_tensor *rope,
+                          const gdn2_tensor *positions,
+                          const gdn2_tensor *q_out, const gdn2_tensor *k_out,
+                          const gdn2_qk_options *opts, hipStream_t stream);
+int gdn2_qk_norm_rope_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
+                                const gdn2_tensor *q_weight,
+                                const gdn2_tensor *k_weight,
+                                const gdn2_tensor *rope,
+                                const gdn2_tensor *positions,
+                                const gdn2_tensor *q_out,
+                                const gdn2_tensor *k_out,
+                                const gdn2_qk_options *opts);
+
+/*
+ * Its backward: dq, dk from the inputs q, k and the gradients dq_out, dk_out
+ * of the outputs (all of q's and k's shapes and type, rows as above), and,
+ * where given, dq_weight and dk_weight [K] in the weight's type, summed over
+ * all tokens and heads in float32 in a fixed order. The sums need a workspace
+ * (as above; 0 bytes when neither is given).
+ */
+int64_t gdn2_qk_norm_rope_bwd_workspace(int64_t T, int32_t H, int32_t HK,
+                                        int32_t K);
+int gdn2_qk_norm_rope_bwd(const gdn2_tensor *q, const gdn2_tensor *k,
+                          const gdn2_tensor *dq_out, const gdn2_tensor *dk_out,
+                          const gdn2_tensor *q_weight,
+                          const gdn2_tensor *k_weight, const gdn2_tensor *rope,
+                          const gdn2_tensor *positions, const gdn2_tensor *dq,
+                          const gdn2_tensor *dk, const gdn2_tensor *dq_weight,
+                          const gdn2_tensor *dk_weight,
+                          const gdn2_qk_options *opts, void *workspace,
+                          int64_t workspace_bytes, hipStream_t stream);
+int gdn2_qk_norm_rope_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
+                                const gdn2_tensor *dq_out,
+                                const gdn2_tensor *dk_out,
+                                const gdn2_tensor *q_weight,
+                                const gdn2_tensor *k_weight,
+                                const gdn2_tensor *rope,
+                                const gdn2_tensor *positions,
+                                const gdn2_tensor *dq, const gdn2_tensor *dk,
+                                const gdn2_tensor *dq_weight,
+                                const gdn2_tensor *dk_weight,
+                                const gdn2_qk_options *opts);
 
 /* Message describing the last failure on the calling thread ("" if none).
  * The string stays valid until the next call on the same thread. */

@@ -14,7 +14,10 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgdn2.so")
 SOURCES = [os.path.join(HERE, "csrc", "gdn2_api.cpp"), os.path.join(HERE, "csrc", "gdn2_fwd.hip"),
            os.path.join(HERE, "csrc", "gdn2_fwd_mixed.hip"), os.path.join(HERE, "csrc", "gdn2_recurrent.hip"),
-           os.path.join(HERE, "csrc", "gdn2_bwd.hip")]
+           os.path.join(HERE, "csrc", "gdn2_bwd.hip"), os.path.join(HERE, "csrc", "gdn2_check.cpp"),
+           os.path.join(HERE, "csrc", "gdn2_delta_api.cpp"), os.path.join(HERE, "csrc", "gdn2_delta_fwd.hip"),
+           os.path.join(HERE, "csrc", "gdn2_delta_bwd.hip"), os.path.join(HERE, "csrc", "gdn2_delta_step.hip"),
+           os.path.join(HERE, "csrc", "gdn2_qk.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -1,0 +1,105 @@
+// Internal interface between the C-ABI layer (gdn2_delta_api.cpp) and the
+// gfx950 kernels of the scalar-gated delta rule and of the q/k preparation.
+// Not installed, not part of the ABI.
+#pragma once
+
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "gdn2_internal.h"
+
+namespace gdn2 {
+
+// Validated arguments of one call of the scalar-gated delta rule. Pointers
+// are device pointers; optional ones are nullptr when omitted.
+struct DeltaParams {
+    const uint16_t *q, *k;  // [T, H, K] io
+    const uint16_t *v;      // [T, HV, V] io
+    const void *g;          // [T, HV] g type, or nullptr (= 0)
+    const uint16_t *beta;   // [T, HV] io, or nullptr (= 1)
+    const float *h0;        // [N, HV, K, V] (or [N, HV, V, K]) float32 or bf16, or nullptr (= 0)
+    const void *cu;         // [N + 1] int32 or int64, or nullptr (one sequence of T tokens)
+    uint16_t *out;          // [T, HV, V] io
+    float *ht;              // as h0, or nullptr (not written)
+    int64_t T;
+    int32_t N, H, HV, K, V;
+    float scale;            // resolved (never 0)
+    int32_t io, gtype;      // IO_*, G_*
+    int32_t cu64;
+    int32_t h0_bf16, ht_bf16;
+    // element strides of the token and head dimensions
+    int64_t sq, sk, sv, so, sg, sb;
+    int64_t hsq, hsk, hsv, hso, hsg, hsb;
+    int32_t state_vmajor;
+    int32_t qk_l2norm;
+    int32_t nslots;         // slot_count(T, N)
+    // workspace (chunked calls): every chunk's record, DeltaRecord::bytes per (slot, value head)
+    char *rec;
+    // backward only. The checkpoints are in accumulator order: per (slot,
+    // value head, 16 value columns) the float32 fragments f32x4[tile][lane]
+    // of a wave, tiles of 16 rows (DeltaFrag).
+    const uint16_t *dout;   // [T, HV, V] io
+    const float *dht;       // [N, HV, K, V] or nullptr (zero)
+    float *dh0;             // [N, HV, K, V] or nullptr (not written)
+    uint16_t *dq, *dk;      // [T, H, K] io
+    uint16_t *dv;           // [T, HV, V] io
+    void *dg;               // [T, HV] gtype
+    uint16_t *dbeta;        // [T, HV] io
+    float *s_ck, *ds_ck;    // state entering / gradient of the state leaving each chunk: K x V per item
+    float *u_ck, *y_ck;     // U and dY of each chunk: 64 x V per item
+    float *yv;              // [item][V / 16][64]: partial sums of dY . v over 16 columns
+    float *dq_ws, *dk_ws;   // [T, HV, K] per value head (grouped heads only)
+};
+
+// One chunk's record, K-independent: the lower triangles of T and P as bf16
+// planes (high and low part: T = Th + Tl to 2^-17), then float32 vectors over
+// the chunk's 64 tokens. A plane holds rows 0..31 with 32 columns and rows
+// 32..63 with 64 columns (whatever lies above the diagonal in them is zero):
+// the columns that 32-wide products over the earlier tokens read.
+struct DeltaRecord {
+    static constexpr int PLANE = 32 * 64 + 32 * 128;  // bytes
+    static constexpr int TH = 0, TL = PLANE, PH = 2 * PLANE, PL = 3 * PLANE;
+    static constexpr int VEC = 4 * PLANE;
+    // vectors: e^G rk, scale e^G rq, e^(G_C - G) rk, beta, G log2(e) in two parts
+    // (rk, rq: the reciprocal norms with in-kernel normalisation, else 1)
+    enum { EG = 0, EQ = 1, ED = 2, BT = 3, GH = 4, GL = 5, NVEC = 6 };
+    static constexpr int GAMMA = VEC + NVEC * 256;  // e^(G_C), one float
+    static constexpr int BYTES = GAMMA + 256;
+};
+
+// Arguments of the q/k preparation (forward and backward).
+struct QkParams {
+    const uint16_t *x[2];        // q, k: [T, H or HK, K] io
+    uint16_t *y[2];              // outputs (forward: rows; backward: dq, dk)
+    const uint16_t *dy[2];       // backward: gradients of the outputs
+    const void *w[2];            // weights [K] float32 or io, or nullptr
+    void *dw[2];                 // gradients of the weights, the weights' type, or nullptr
+    int32_t w_f32[2];
+    const float *rope;           // [P, rot]: cos then sin, or nullptr
+    const void *pos;             // [T] int32 or int64
+    int32_t pos64;
+    int64_t P;                   // rows of the table
+    int64_t T;
+    int32_t heads[2];
+    int32_t K, rot;
+    int32_t norm, interleaved, io;
+    float eps;
+    int64_t sx[2], hsx[2], sy[2], hsy[2], sdy[2], hsdy[2];
+    float *part;                 // backward with weights: [groups][2][K] partial sums
+    int32_t groups;
+};
+
+hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream);
+hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream);
+hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream);
+hipError_t launch_delta_bwd_grad(const DeltaParams &p, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaParams &p, int ncu, hipStream_t stream);
+hipError_t launch_qk_fwd(const QkParams &p, hipStream_t stream);
+hipError_t launch_qk_bwd(const QkParams &p, hipStream_t stream);
+// Workgroups of the q/k backward (each leaves one row of partial weight gradients).
+int qk_bwd_groups(int64_t T, int32_t heads_q, int32_t heads_k, int32_t K);
+
+__host__ __device__ inline SeqRange seq_of(const DeltaParams &p, int64_t n) { return seq_range(p.cu, p.cu64, p.T, n); }
+
+}  // namespace gdn2

@@ -1,0 +1,392 @@
+"""GPU tests of the scalar-gated delta rule (chunked, token by token, its
+gradients) against float64 (see tests/delta_ref.py for the tolerances)."""
+
+import os
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from tests.delta_ref import DG_REL, F32_REL, backward64, close, forward64, make
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+RAGGED = [70, 0, 1, 64, 63, 129, 65, 0, 200]
+INPUTS = ("q", "k", "v", "g", "beta", "initial_state", "cu_seqlens")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from linear_attention_rnn_gdn2_amd import gdn2
+    from oracle.build import LIB, build_c_oracle
+    gdn2.load_library()
+    if not os.path.exists(LIB):
+        build_c_oracle()
+    return gdn2
+
+
+def on_gpu(d):
+    return {n: None if d.get(n) is None else d[n].cuda() for n in INPUTS}
+
+
+def fwd(lib, d, recurrent=False, **kw):
+    call = lib.delta_recurrent_fwd if recurrent else lib.delta_chunk_fwd
+    out = call(**on_gpu(d), **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_fwd(tag, got, ref):
+    close(tag + " out", got[0], ref[0], F32_REL)
+    close(tag + " state", got[1], ref[1], F32_REL)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("K,V,H,HV,io,gtype", [
+    (64, 64, 1, 1, BF16, F32), (128, 128, 2, 2, BF16, F32), (128, 64, 1, 3, F16, BF16), (64, 128, 2, 4, BF16, F16),
+    (128, 128, 1, 4, F16, F32), (64, 64, 3, 6, F16, F16)])
+def test_forward(lib, recurrent, K, V, H, HV, io, gtype):
+    """Ragged batches with empty sequences and chunk borders, both evaluations, every type."""
+    d = make(RAGGED, H, HV, K, V, seed=K + V + HV, io=io, gtype=gtype)
+    check_fwd(f"K={K} V={V}", fwd(lib, d, recurrent), forward64(d))
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("drop", [("g",), ("beta",), ("initial_state",), ("g", "beta", "initial_state")])
+def test_defaults(lib, recurrent, drop):
+    d = make([90, 7], 2, 2, 64, 64, seed=3, beta_max=1.0)
+    for n in drop:
+        d[n] = None
+    check_fwd(str(drop), fwd(lib, d, recurrent), forward64(d))
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_one_sequence_without_cu_and_scale(lib, recurrent):
+    d = make([150], 1, 2, 128, 64, seed=4)
+    a = on_gpu(d)
+    a["cu_seqlens"] = None
+    call = lib.delta_recurrent_fwd if recurrent else lib.delta_chunk_fwd
+    got = call(**a, scale=0.7)
+    check_fwd("scale", got, forward64(d, scale=0.7))
+    got = call(**a, output_final_state=False)
+    assert got[1] is None
+    close("no state", got[0], forward64(d)[0], F32_REL)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64)])
+def test_state_types_and_layouts(lib, recurrent, K, V):
+    """V-major states equal K-major ones bit for bit; bf16 states are widened and rounded once."""
+    d = make([70, 0, 5], 1, 2, K, V, seed=5)
+    base = fwd(lib, d, recurrent)
+    vk = dict(d, initial_state=d["initial_state"].transpose(2, 3).contiguous())
+    got = fwd(lib, vk, recurrent, state_layout="vk")
+    assert torch.equal(got[0], base[0]) and torch.equal(got[1].transpose(2, 3), base[1])
+    for layout in ("kv", "vk"):
+        b = dict(d, initial_state=d["initial_state"].to(BF16))
+        ref = forward64(dict(b, initial_state=b["initial_state"].float()))
+        if layout == "vk":
+            b["initial_state"] = b["initial_state"].transpose(2, 3).contiguous()
+        fin = torch.empty_like(b["initial_state"], device="cuda")
+        out, fin = fwd(lib, b, recurrent, final_state=fin, state_layout=layout)
+        close("bf16 out", out, ref[0], F32_REL)
+        close("bf16 state", fin.transpose(2, 3) if layout == "vk" else fin, ref[1], F32_REL)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("io", [BF16, F16])
+def test_l2norm(lib, recurrent, io):
+    """In-kernel norms of rows of any size, a zero row among them."""
+    d = make([100, 3], 2, 4, 64, 64, seed=6, io=io)
+    d["q"] = (d["q"].float() * 5.0).to(io)
+    d["k"] = (d["k"].float() * torch.linspace(0.1, 9.0, 103)[:, None, None]).to(io)
+    d["k"][17, 1] = 0
+    d["q"][101] = 0
+    check_fwd("l2norm", fwd(lib, d, recurrent, qk_l2norm=True), forward64(d, qk_l2norm=True))
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_strong_decay(lib, recurrent):
+    """Single tokens that decay the state by e^-30, next to slow ones: chunk sums of g in the hundreds."""
+    d = make([200, 64], 1, 2, 128, 128, seed=7, strong=True)
+    check_fwd("strong", fwd(lib, d, recurrent), forward64(d))
+    d["g"][:] = -2000.0
+    check_fwd("everything forgotten", fwd(lib, d, recurrent), forward64(d))
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_strided_views(lib, recurrent):
+    """q, k, v as views of one projection, gates as views of another, odd offsets, int64 cu_seqlens."""
+    T, H, K = 133, 2, 64
+    d = make([68, 65], H, H, K, K, seed=8)
+    a = on_gpu(d)
+    base = (lib.delta_recurrent_fwd if recurrent else lib.delta_chunk_fwd)(**a)
+    fused = torch.stack([a["q"], a["k"], a["v"]], 1).contiguous()
+    gates = torch.full((T, 3 * H + 1), float("nan"), device="cuda")
+    gates[:, 1:1 + H] = a["g"]
+    b16 = torch.full((H, T + 3), float("nan"), device="cuda", dtype=BF16)
+    b16[:, 3:] = a["beta"].T
+    room = torch.full((T, H + 1, K), 7.0, device="cuda", dtype=BF16)
+    s = dict(a, q=fused[:, 0], k=fused[:, 1], v=fused[:, 2], g=gates[:, 1:1 + H], beta=b16[:, 3:].T,
+             cu_seqlens=a["cu_seqlens"].long(), out=room[:, :H])
+    got = (lib.delta_recurrent_fwd if recurrent else lib.delta_chunk_fwd)(**s)
+    assert torch.equal(got[0], base[0]) and torch.equal(got[1], base[1])
+    assert (room[:, H] == 7.0).all(), "elements next to the output were written"
+
+
+def test_neighbours_do_not_leak(lib):
+    """A sequence's NaN and infinity reach no other sequence's chunk or head."""
+    d = make([70, 30, 100], 2, 2, 64, 64, seed=9)
+    clean = fwd(lib, d)
+    clean_b = grads(lib, d)
+    for n in ("q", "k", "v", "d_out"):
+        d[n][70:100] = float("nan")
+    d["v"][80, 1, 3] = float("inf")
+    got, got_b = fwd(lib, d), grads(lib, d)
+    for rows in (slice(0, 70), slice(100, 200)):
+        assert torch.equal(got[0][rows], clean[0][rows])
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(got_b[n][rows], clean_b[n][rows]), n
+    for i in (0, 2):
+        assert torch.equal(got[1][i], clean[1][i])
+        assert torch.equal(got_b["d_initial_state"][i], clean_b["d_initial_state"][i])
+
+
+def test_step_in_place_and_continues_prefill(lib):
+    """A chunked prefill, then tokens one by one on its state in place, equal one pass."""
+    d = make([150, 70], 2, 4, 128, 128, seed=10)
+    ref = forward64(d)
+    lens, cut = [150, 70], [140, 64]
+    starts = [0, 150]
+
+    def part(lo, hi):
+        rows = torch.cat([torch.arange(s + a, s + b) for s, a, b in zip(starts, lo, hi)])
+        cu = torch.tensor(np.concatenate([[0], np.cumsum([b - a for a, b in zip(lo, hi)])]), dtype=torch.int32)
+        return rows, dict({n: d[n][rows] for n in ("q", "k", "v", "g", "beta")}, cu_seqlens=cu,
+                          initial_state=d["initial_state"])
+
+    rows, p = part([0, 0], cut)
+    out, state = fwd(lib, p)
+    close("prefill", out, ref[0][rows], F32_REL)
+    for i in range(6):
+        lo = cut if i == 0 else hi
+        hi = [min(a + 1, l) if i < 5 else l for a, l in zip(lo, lens)]
+        rows, p = part(lo, hi)
+        a = on_gpu(p)
+        a["initial_state"] = state
+        out, same = lib.delta_recurrent_fwd(**a, final_state=state)
+        assert same is state
+        close(f"step {i}", out, ref[0][rows], F32_REL)
+    close("state", state, ref[1], F32_REL)
+
+
+def test_equals_channelwise_kernels(lib):
+    """The scalar rule is the channel-wise one at constant gates: the library's own kernels agree within
+    the channel-wise kernels' bar (5e-3)."""
+    d = make([200, 33], 2, 4, 128, 128, seed=11, beta_max=1.0)
+    out, state = fwd(lib, d)
+    a = on_gpu(d)
+    g = a["g"][..., None].expand(-1, -1, 128).contiguous()
+    b = a["beta"][..., None].expand(-1, -1, 128).contiguous()
+    o2, s2 = lib.chunk_fwd(a["q"], a["k"], a["v"], g, b, b, initial_state=a["initial_state"], cu_seqlens=a["cu_seqlens"])
+    for x, y in ((out, o2), (state, s2)):
+        assert (x.double() - y.double()).norm() <= 5e-3 * y.double().norm()
+
+
+# --------------------------------------------------------------- gradients --
+
+def grads(lib, d, **kw):
+    a = on_gpu(d)
+    s0, cu = a.pop("initial_state"), a.pop("cu_seqlens")
+    dht = None if d["d_final_state"] is None else d["d_final_state"].cuda()
+    got = lib.delta_chunk_bwd(**a, d_out=d["d_out"].cuda(), initial_state=s0, cu_seqlens=cu, d_final_state=dht, **kw)
+    torch.cuda.synchronize()
+    return got
+
+
+def check_grads(tag, got, ref):
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "d_initial_state"):
+        if got[n] is not None:
+            close(f"{tag} {n}", got[n], ref[n], DG_REL if n == "dg" else F32_REL)
+
+
+@pytest.mark.parametrize("D,H,HV,io,gtype", [(64, 1, 1, BF16, F32), (128, 2, 2, BF16, F32), (128, 1, 3, F16, BF16),
+                                             (64, 2, 4, F16, F32), (64, 2, 2, BF16, F16)])
+def test_backward(lib, D, H, HV, io, gtype):
+    d = make(RAGGED, H, HV, D, D, seed=20 + D + HV, io=io, gtype=gtype)
+    check_grads(f"D={D}", grads(lib, d), backward64(d))
+
+
+def test_backward_strong_decay_and_zero_gates(lib):
+    d = make([200, 64, 30], 1, 2, 128, 128, seed=21, strong=True)
+    d["beta"][::3] = 0
+    check_grads("strong", grads(lib, d), backward64(d))
+
+
+def test_backward_optional_states(lib):
+    d = make([100, 0, 20], 2, 2, 64, 64, seed=22, init=False)
+    d["d_final_state"] = None
+    got = grads(lib, d, need_d_initial_state=False)
+    assert got["d_initial_state"] is None
+    check_grads("no states", got, backward64(d))
+    a = on_gpu(d)
+    one = {n: (x if x is None else x[:100]) for n, x in a.items() if n not in ("cu_seqlens", "initial_state")}
+    got = lib.delta_chunk_bwd(**one, d_out=d["d_out"][:100].cuda(), scale=0.3)
+    e = dict(d, **{n: d[n][:100] for n in ("q", "k", "v", "g", "beta", "d_out")}, cu_seqlens=torch.tensor([0, 100]))
+    check_grads("one sequence", got, backward64(e, scale=0.3))
+
+
+def test_backward_against_differences(lib):
+    """<gradient, direction> against a central difference of the float64
+    forward: second order in a step of 1e-4, 1e-6 relative at most, next to
+    the gradients' 16-bit rounding averaged over the direction (3e-3 here)."""
+    d = make([75, 10], 1, 2, 64, 64, seed=23)
+    got = grads(lib, d)
+    rng = np.random.default_rng(0)
+
+    def loss(e):
+        o, s = forward64(e)
+        return float((o * d["d_out"].double().numpy()).sum() + (s * d["d_final_state"].double().numpy()).sum())
+
+    base = {n: d[n].double() for n in ("q", "k", "v", "g", "beta", "initial_state")}
+    for n in base:
+        step = torch.from_numpy(rng.standard_normal(base[n].shape))
+        # along the gradient in part, so that the product is not a difference of large sums
+        gn = "d_initial_state" if n == "initial_state" else "d" + n
+        ref = got[gn].cpu().double()
+        step = step / step.norm() + ref / ref.norm()
+        hi, lo = (loss(dict(d, **{n: base[n] + s * 1e-4 * step})) for s in (1, -1))
+        want, have = (hi - lo) / 2e-4, float((ref * step).sum())
+        assert abs(have - want) <= 3e-3 * abs(want), (n, have, want)
+
+
+# ------------------------------------------------------ calls and captures --
+
+def test_same_bits_every_time(lib):
+    d = make([300, 90], 2, 6, 128, 128, seed=30)
+    a, b = fwd(lib, d), fwd(lib, d)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x, y = grads(lib, d), grads(lib, d)
+    assert all(torch.equal(x[n], y[n]) for n in x)
+
+
+def test_empty_calls(lib):
+    """No tokens at all: the states pass through; no workspace is needed."""
+    d = make([0, 0], 1, 2, 64, 64, seed=31)
+    for recurrent in (False, True):
+        out, state = fwd(lib, d, recurrent)
+        assert out.numel() == 0 and torch.equal(state.cpu(), d["initial_state"])
+    got = grads(lib, d)
+    assert torch.equal(got["d_initial_state"].cpu(), d["d_final_state"])
+
+
+@pytest.mark.parametrize("which", ["chunk", "step", "bwd"])
+def test_graph_replays(lib, which):
+    """A captured call, replayed between eager calls on other inputs, gives the eager call's bits each time."""
+    d = make([130, 40], 1, 2, 64, 64, seed=32)
+    other = make([130, 40], 1, 2, 64, 64, seed=33)
+    a, o = on_gpu(d), on_gpu(other)
+    do, dht = d["d_out"].cuda(), d["d_final_state"].cuda()
+    do2 = other["d_out"].cuda()
+
+    def call(x, dy):
+        if which == "bwd":
+            got = lib.delta_chunk_bwd(**x, d_out=dy, d_final_state=dht)
+            return [got[n] for n in sorted(got)]
+        return list((lib.delta_chunk_fwd if which == "chunk" else lib.delta_recurrent_fwd)(**x))
+
+    want, want_other = call(a, do), call(o, do2)
+    static = {n: x.clone() for n, x in a.items()}
+    sdo = do.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(static, sdo)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(static, sdo)
+    for i in range(4):
+        src, dy, ref = (a, do, want) if i % 2 == 0 else (o, do2, want_other)
+        for n in static:
+            static[n].copy_(src[n])
+        sdo.copy_(dy)
+        eager = call(o if i % 2 == 0 else a, do2 if i % 2 == 0 else do)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, ref)), i
+        assert all(torch.equal(x, y) for x, y in zip(eager, want_other if i % 2 == 0 else want)), i
+
+
+def test_streams_and_threads(lib):
+    """Calls from two threads on two streams at once give the bits of the calls made alone."""
+    ds = [make([260, 100], 1, 2, 128, 128, seed=40 + i) for i in range(2)]
+    want = [(fwd(lib, d), grads(lib, d)) for d in ds]
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3):
+                    got[i] = (fwd(lib, ds[i]), grads(lib, ds[i]))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors, errors
+    for w, g in zip(want, got):
+        assert torch.equal(w[0][0], g[0][0]) and torch.equal(w[0][1], g[0][1])
+        assert all(torch.equal(w[1][n], g[1][n]) for n in w[1])
+
+
+def test_own_workspace(lib):
+    """A caller's workspace gives the same bits whatever it held; one byte less is refused."""
+    d = make([100, 30], 1, 2, 64, 64, seed=41)
+    want, want_b = fwd(lib, d), grads(lib, d)
+    n = lib.delta_chunk_fwd_workspace(130, 2, 2)
+    nb = lib.delta_chunk_bwd_workspace(130, 2, 1, 2, 64, 64)
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        got = fwd(lib, d, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        ws = torch.full((nb,), fill, dtype=torch.uint8, device="cuda")
+        got = grads(lib, d, workspace=ws)
+        assert all(torch.equal(got[x], want_b[x]) for x in got)
+    with pytest.raises(lib.Gdn2Error) as e:
+        fwd(lib, d, workspace=ws[:n - 1])
+    assert e.value.status == "WORKSPACE"
+    with pytest.raises(lib.Gdn2Error) as e:
+        grads(lib, d, workspace=ws[:nb - 1])
+    assert e.value.status == "WORKSPACE"
+    with pytest.raises(lib.Gdn2Error) as e:
+        fwd(lib, d, workspace=torch.empty(n + 256, dtype=torch.uint8, device="cuda")[16:])
+    assert e.value.status == "WORKSPACE"
+
+
+def test_malformed_cu_seqlens_stays_in_bounds(lib):
+    """Entries that decrease or leave [0, T] give unspecified values, but only inside the call's own buffers."""
+    d = make([100, 28], 1, 2, 64, 64, seed=42)
+    for cu in ([0, 500, 128], [-7, 60, 20], [128, 0, 128]):
+        e = dict(d, cu_seqlens=torch.tensor(cu, dtype=torch.int32))
+        room = torch.full((130, 2, 64), 3.0, dtype=BF16, device="cuda")
+        for recurrent in (False, True):
+            fwd(lib, e, recurrent, out=room[1:129])
+            assert (room[0] == 3.0).all() and (room[129] == 3.0).all()
+        grads(lib, e)
+    check_fwd("after", fwd(lib, d), forward64(d))
+
+
+def test_many_short_sequences(lib):
+    """More (sequence, head) chains than the GPU holds at once, one to three tokens each."""
+    lens = [1 + i % 3 for i in range(700)]
+    d = make(lens, 1, 2, 64, 64, seed=43)
+    ref = forward64(d)
+    for recurrent in (False, True):
+        check_fwd("short", fwd(lib, d, recurrent), ref)
+    check_grads("short", grads(lib, d), backward64(d))
