@@ -53,12 +53,15 @@ struct DeltaParams {
 };
 
 // One chunk's record, K-independent: the lower triangles of T and P as bf16
-// planes (high and low part: T = Th + Tl to 2^-17), then float32 vectors over
-// the chunk's 64 tokens. A plane holds rows 0..31 with 32 columns and rows
-// 32..63 with 64 columns (whatever lies above the diagonal in them is zero):
-// the columns that 32-wide products over the earlier tokens read.
+// planes (high and low part: T = Th + Tl to 2^-18), then float32 vectors over
+// the chunk's 64 tokens. A plane is a sequence of left-operand fragments of
+// 1 KiB, one per 16 rows and 32 columns on or below the diagonal (the upper
+// block of a pair on the diagonal is zero): lane 16 q4 + l16 holds row l16,
+// columns 4 q4 .. + 3 and 16 + 4 q4 .. + 3 in 16 bytes.
 struct DeltaRecord {
-    static constexpr int PLANE = 32 * 64 + 32 * 128;  // bytes
+    // fragment of rows 16 mt .., columns 32 j .. (j <= mt / 2)
+    __host__ __device__ static constexpr int frag(int mt, int j) { return (mt < 2 ? mt : 2 * mt - 2 + j) * 1024; }
+    static constexpr int PLANE = 6 * 1024;  // bytes
     static constexpr int TH = 0, TL = PLANE, PH = 2 * PLANE, PL = 3 * PLANE;
     static constexpr int VEC = 4 * PLANE;
     // vectors: e^G rk, scale e^G rq, e^(G_C - G) rk, beta, G log2(e) in two parts
@@ -90,6 +93,11 @@ struct QkParams {
     int32_t groups;
 };
 
+// Value columns per workgroup of the sequential passes, in waves of 16: the
+// fewest (2, 4 or 8) with which every workgroup is resident at once (they
+// hold most of a compute unit's LDS each), so that few chains spread over the
+// device and many do not load a chunk's tiles more often than they must.
+int delta_waves(const DeltaParams &p, int ncu);
 hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream);
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream);

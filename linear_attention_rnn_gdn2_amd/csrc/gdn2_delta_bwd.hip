@@ -35,7 +35,7 @@ struct BwdStateLds {
     static constexpr int RS = 2 * K + 16;
     static constexpr int TILE = 64 * RS;
     static constexpr int K0 = 0, Q0 = NP * TILE;
-    static constexpr int PLANE = 64 * PSTR;
+    static constexpr int PLANE = DeltaRecord::PLANE;
     static constexpr int P0 = 2 * NP * TILE;
     static constexpr int V0 = P0 + 4 * PLANE;
     static constexpr int SIZE = V0 + DeltaRecord::NVEC * 256 + 16;
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
         for (int e = 0; e < 4; ++e) dS[i][e] = p.dht ? p.dht[shead + (int64_t)(16 * i + 4 * q4 + e) * p.V + col] : 0.0f;
 
     constexpr int CPT = 64 * K / 8 / NT;
-    constexpr int RCH = 4 * 384, RPT = (RCH + NT - 1) / NT;
+    constexpr int RCH = 4 * DeltaRecord::PLANE / 16, RPT = (RCH + NT - 1) / NT;
     constexpr int VCH = DeltaRecord::NVEC * 16 + 1;
     static_assert(NT >= VCH, "one vector chunk per thread");
     i32x4 fk[CPT], fq[CPT], fr[RPT], fv;
@@ -114,9 +114,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
         for (int i = 0; i < RPT; ++i) {
             const int id = t + NT * i;
             if (RCH % NT == 0 || id < RCH) {
-                int row, cc;
-                plane_pos(id % 384, row, cc);
-                lds_st(sm, L::P0 + id / 384 * L::PLANE + row * PSTR + 16 * cc, fr[i]);
+                lds_st(sm, L::P0 + 16 * id, fr[i]);
             }
         }
         if (t < VCH) lds_st(sm, L::V0 + 16 * t, fv);
@@ -182,8 +180,8 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
                 u *= vec4(DeltaRecord::ED, mt);
 #pragma unroll
                 for (int jj = j; jj < 2; ++jj) {
-                    const bf16x8 ph = ld_col(sm + L::P0 + 2 * L::PLANE, PSTR, 32 * jj, 16 * mt, q4, l16);
-                    const bf16x8 pl = ld_col(sm + L::P0 + 3 * L::PLANE, PSTR, 32 * jj, 16 * mt, q4, l16);
+                    const bf16x8 ph = ld_frag_t(sm + L::P0 + 2 * L::PLANE, mt, jj, q4, l16);
+                    const bf16x8 pl = ld_frag_t(sm + L::P0 + 3 * L::PLANE, mt, jj, q4, l16);
                     u = mfma_bf16(ph, Oh[jj], u);
                     if constexpr (NP == 2) u = mfma_bf16(ph, Ol[jj], u);
                     u = mfma_bf16(pl, Oh[jj], u);
@@ -205,8 +203,8 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
                 f32x4 y = {0, 0, 0, 0};
 #pragma unroll
                 for (int jj = j; jj < 2; ++jj)
-                    y = mfma_split<true>(ld_col(sm + L::P0, PSTR, 32 * jj, 16 * mt, q4, l16),
-                                         ld_col(sm + L::P0 + L::PLANE, PSTR, 32 * jj, 16 * mt, q4, l16), Uh[jj], Ul[jj], y);
+                    y = mfma_split<true>(ld_frag_t(sm + L::P0, mt, jj, q4, l16),
+                                         ld_frag_t(sm + L::P0 + L::PLANE, mt, jj, q4, l16), Uh[jj], Ul[jj], y);
                 reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = y;
                 const f32x4 dv = y * vec4(DeltaRecord::BT, mt), eg = vec4(DeltaRecord::EG, mt), eq = vec4(DeltaRecord::EQ, mt);
                 f32x4 yv;

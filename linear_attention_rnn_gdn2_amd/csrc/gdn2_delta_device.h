@@ -100,19 +100,90 @@ __device__ __forceinline__ void st_parts(char *base, int plane_bytes, int off, i
     }
 }
 
-// Row and 16-byte column of chunk ci (0 .. 383) of a record's plane.
-__device__ __forceinline__ void plane_pos(int ci, int &row, int &col)
+// A record's fragment as a left operand, and the same plane transposed:
+// element (m, k) is plane[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 ..,
+// columns m = 16 mt + l16 (mt <= 2 j + 1).
+__device__ __forceinline__ bf16x8 ld_frag(const char *plane, int mt, int j, int lane)
 {
-    if (ci < 128) {
-        row = ci >> 2;
-        col = ci & 3;
-    } else {
-        row = 32 + ((ci - 128) >> 3);
-        col = (ci - 128) & 7;
-    }
+    return *reinterpret_cast<const bf16x8 *>(plane + DeltaRecord::frag(mt, j) + 16 * lane);
+}
+__device__ __forceinline__ bf16x8 ld_frag_t(const char *plane, int mt, int j, int q4, int l16)
+{
+    const int a = ((l16 & 3) * 16 + 4 * q4 + (l16 >> 2)) * 16 + (mt & 1) * 8;
+    return cat4(lds_tr(plane, DeltaRecord::frag(2 * j, mt / 2) + a), lds_tr(plane, DeltaRecord::frag(2 * j + 1, mt / 2) + a));
 }
 
 __device__ __forceinline__ int64_t delta_item(const DeltaParams &p, int64_t slot, int hv) { return slot * p.HV + hv; }
+
+// A float32 right operand of N 32-row steps in two parts of the io type, for
+// products with rows of q or k. bf16: as everywhere. fp16: the inputs are fp16
+// values as they stand, so the operand is taken in fp16 too, scaled per column
+// by a power of two that brings its largest value near 2^14: 22 significant
+// bits next to that value, and no value of the state out of fp16's range.
+template <int IO, int N>
+struct RightOp {
+    i32x4 h[N], l[N];
+    float inv = 1.0f;  // what a product is multiplied by
+
+    __device__ __forceinline__ void set(const f32x4 (&x)[2 * N])
+    {
+        if constexpr (IO == IO_F16) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[i][e]));
+            const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+            m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+            const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+            m = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+            int ex = 14 - __builtin_amdgcn_frexp_expf(m);
+            ex = ex > 120 ? 120 : ex;  // (an exponent of zero, infinity or NaN is 0)
+            const float sc = ldexpf(1.0f, ex);
+            inv = ldexpf(1.0f, -ex);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const f32x4 y0 = x[2 * j] * sc, y1 = x[2 * j + 1] * sc;
+                const f16x4 h0 = __builtin_convertvector(y0, f16x4), h1 = __builtin_convertvector(y1, f16x4);
+                const f16x4 l0 = __builtin_convertvector(y0 - __builtin_convertvector(h0, f32x4), f16x4);
+                const f16x4 l1 = __builtin_convertvector(y1 - __builtin_convertvector(h1, f32x4), f16x4);
+                h[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
+                l[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                bf16x4 h0, l0, h1, l1;
+                split4(x[2 * j], h0, l0);
+                split4(x[2 * j + 1], h1, l1);
+                h[j] = __builtin_bit_cast(i32x4, cat4(h0, h1));
+                l[j] = __builtin_bit_cast(i32x4, cat4(l0, l1));
+            }
+        }
+    }
+    // acc + a times the high (part 0) or low part of step j, a left operand of the io type
+    __device__ __forceinline__ f32x4 mul1(bf16x8 a, int j, int part, f32x4 acc) const
+    {
+        const i32x4 b = part ? l[j] : h[j];
+        if constexpr (IO == IO_F16)
+            return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+        else return mfma_bf16(a, __builtin_bit_cast(bf16x8, b), acc);
+    }
+    // a sum of such products in the operand's own scale
+    __device__ __forceinline__ f32x4 scaled(f32x4 acc) const
+    {
+        if constexpr (IO == IO_F16) return acc * inv;
+        else return acc;
+    }
+};
+
+// Four 16-bit io values as float32.
+template <int IO>
+__device__ __forceinline__ f32x4 io4_f32(bf16x4 x)
+{
+    if constexpr (IO == IO_F16) return __builtin_convertvector(__builtin_bit_cast(f16x4, x), f32x4);
+    else return __builtin_convertvector(x, f32x4);
+}
 
 // Sum over the 16 lanes of a row (lanes with equal q4); every lane gets it.
 __device__ __forceinline__ float sum16(float x)

@@ -32,24 +32,28 @@ namespace {
 using namespace dev;
 
 // ------------------------------------------------------------ preparation --
-// One workgroup (4 waves) per (chunk, value head). Wave w owns block row w
-// (16 tokens) of the two score products, inverts the diagonal block w by
-// forward substitution, and then carries block column w of the inverse:
-//     T_ij = -T_ii (sum_{j <= m < i} A_im T_mj)
-// in float32 MFMA (16x16x4), whose accumulators are its next right operands.
+// One workgroup (4 waves) per (chunk, value head). Wave w owns the rows
+// r = 16 w .. of both score products, computed transposed (the left operand
+// is the earlier token's key), so that a lane holds four consecutive columns
+// of one row: that is its share of the record's fragments, stored from
+// registers. T follows by blocks of 16, also transposed: the diagonal blocks
+// by forward substitution, one per wave, and then for wave i, column by
+// column towards the left,
+//     T_ij^T = -T_jj^T (sum_{j < m <= i} A_mj^T T_im^T)
+// on float32 MFMA (16x16x4), whose accumulators are its next right operands.
 template <int K>
 struct WyLds {
     static constexpr int RS = 2 * K + 16;  // row stride of a staged tile (bytes): rows 16 bytes apart in banks
     static constexpr int TILE = 64 * RS;
     static constexpr int K0 = 0, Q0 = TILE;
-    static constexpr int PL = 0;           // output planes, over the tiles once both products are done
-    static constexpr int PLANE = 64 * PSTR;
-    static constexpr int AS = 68;          // floats per row of A
-    static constexpr int A0 = 2 * TILE > 4 * PLANE ? 2 * TILE : 4 * PLANE;
-    static constexpr int TS = 20;          // floats per row of an inverted diagonal block
+    // over the tiles, once both products are done
+    static constexpr int AS = 68;          // floats per row of A^T
+    static constexpr int A0 = 0;
+    static constexpr int TS = 20;          // floats per row of a transposed diagonal block of T
     static constexpr int T0 = A0 + 64 * AS * 4;
-    static constexpr int V0 = T0 + 4 * 16 * TS * 4;
-    static constexpr int SIZE = V0 + 6 * 256;
+    static constexpr int TEND = T0 + 64 * TS * 4;
+    static constexpr int V0 = 2 * TILE > TEND ? 2 * TILE : TEND;
+    static constexpr int SIZE = V0 + 5 * 256;
 };
 
 template <int K, int IO, bool L2N>
@@ -87,7 +91,7 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
             lds_st(sm, L::Q0 + row * L::RS + col * 16, b[i]);
         }
     }
-    float *vec = reinterpret_cast<float *>(sm + L::V0);  // G hi, G lo, beta, e^G (unscaled), rk, rq
+    float *vec = reinterpret_cast<float *>(sm + L::V0);  // G in two parts, beta, rk, rq
     char *rec = p.rec + delta_item(p, slot, hv) * (int64_t)DeltaRecord::BYTES;
     float *rvec = reinterpret_cast<float *>(rec + DeltaRecord::VEC);
     double G = 0.0, GC = 0.0;
@@ -119,7 +123,6 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
         vec[128 + lane] = bt;
     }
     __syncthreads();
-    float rkv = 1.0f, rqv = 1.0f;
     if constexpr (L2N) {
         // reciprocal norms of the rows of q and k: four threads per row
         const int row = t >> 2, part = t & 3;
@@ -140,183 +143,167 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
         sk += __shfl_xor(sk, 2);
         sq += __shfl_xor(sq, 2);
         if (part == 0) {
-            vec[256 + row] = 1.0f / fmaxf(sqrtf(sk), 1e-12f);
-            vec[320 + row] = 1.0f / fmaxf(sqrtf(sq), 1e-12f);
+            // (a row of zeros stays one: its factor must not set the scale of an fp16 operand)
+            vec[192 + row] = sk == 0.0f ? 0.0f : 1.0f / fmaxf(sqrtf(sk), 1e-12f);
+            vec[256 + row] = 1.0f / fmaxf(sqrtf(sq), 1e-12f);
         }
         __syncthreads();
     }
     if (wave == 0) {
-        if constexpr (L2N) {
-            rkv = vec[256 + lane];
-            rqv = vec[320 + lane];
-        }
-        const float eg = ex2((float)G);
-        rvec[DeltaRecord::EG * 64 + lane] = eg * rkv;
-        rvec[DeltaRecord::EQ * 64 + lane] = eg * rqv * p.scale;
-        rvec[DeltaRecord::ED * 64 + lane] = ex2((float)(GC - G)) * rkv;
+        const float rk = L2N ? vec[192 + lane] : 1.0f, rq = L2N ? vec[256 + lane] : 1.0f;
+        const float eg = ex2((float)G), gh = (float)G;
+        rvec[DeltaRecord::EG * 64 + lane] = eg * rk;
+        rvec[DeltaRecord::EQ * 64 + lane] = eg * rq * p.scale;
+        rvec[DeltaRecord::ED * 64 + lane] = ex2((float)(GC - G)) * rk;
         rvec[DeltaRecord::BT * 64 + lane] = bt;
-        rvec[DeltaRecord::GH * 64 + lane] = (float)G;
-        rvec[DeltaRecord::GL * 64 + lane] = (float)(G - (double)(float)G);
+        rvec[DeltaRecord::GH * 64 + lane] = gh;
+        rvec[DeltaRecord::GL * 64 + lane] = (float)(G - (double)gh);
         if (lane == 0) *reinterpret_cast<float *>(rec + DeltaRecord::GAMMA) = ex2((float)GC);
     }
 
-    // block row `wave` of K K^T and Q K^T, decayed and masked
-    float *A = reinterpret_cast<float *>(sm + L::A0);
-    f32x4 P[4];
+    // rows r = 16 wave + l16 of A and P, columns 16 s + 4 q4 + e
+    auto mm = [](i32x4 a, i32x4 b, f32x4 acc) {
+        if constexpr (IO == IO_F16)
+            return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+        else return mfma_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc);
+    };
+    const int r = 16 * wave + l16;
+    f32x4 At[4], Pt[4];
     {
-        auto mm = [](i32x4 a, i32x4 b, f32x4 acc) {
-            if constexpr (IO == IO_F16)
-                return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
-            else return mfma_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc);
-        };
-        i32x4 ka[K / 32], qa[K / 32];
+        i32x4 kb[K / 32], qb[K / 32];
 #pragma unroll
         for (int j = 0; j < K / 32; ++j) {
-            ka[j] = lds_ld<i32x4>(sm, L::K0 + (16 * wave + l16) * L::RS + 64 * j + 16 * q4);
-            qa[j] = lds_ld<i32x4>(sm, L::Q0 + (16 * wave + l16) * L::RS + 64 * j + 16 * q4);
+            kb[j] = lds_ld<i32x4>(sm, L::K0 + r * L::RS + 64 * j + 16 * q4);
+            qb[j] = lds_ld<i32x4>(sm, L::Q0 + r * L::RS + 64 * j + 16 * q4);
         }
-        const f32x4 gh = lds_ld<f32x4>(sm, L::V0 + (16 * wave + 4 * q4) * 4);
-        const f32x4 gl = lds_ld<f32x4>(sm, L::V0 + 256 + (16 * wave + 4 * q4) * 4);
-        const f32x4 b4 = lds_ld<f32x4>(sm, L::V0 + 512 + (16 * wave + 4 * q4) * 4);
-        f32x4 rk4 = {1, 1, 1, 1}, rq4 = {1, 1, 1, 1};
-        if constexpr (L2N) {
-            rk4 = lds_ld<f32x4>(sm, L::V0 + 1024 + (16 * wave + 4 * q4) * 4);
-            rq4 = lds_ld<f32x4>(sm, L::V0 + 1280 + (16 * wave + 4 * q4) * 4);
-        }
+        const float gh = vec[r], gl = vec[64 + r], br = vec[128 + r] * (L2N ? vec[192 + r] : 1.0f);
+        const float sr = p.scale * (L2N ? vec[256 + r] : 1.0f);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            P[s] = f32x4{0, 0, 0, 0};
+            At[s] = Pt[s] = f32x4{0, 0, 0, 0};
             if (s > wave) continue;
             f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < K / 32; ++j) {
-                const i32x4 b = lds_ld<i32x4>(sm, L::K0 + (16 * s + l16) * L::RS + 64 * j + 16 * q4);
-                kk = mm(ka[j], b, kk);
-                qk = mm(qa[j], b, qk);
+                const i32x4 a = lds_ld<i32x4>(sm, L::K0 + (16 * s + l16) * L::RS + 64 * j + 16 * q4);
+                kk = mm(a, kb[j], kk);
+                qk = mm(a, qb[j], qk);
             }
-            const int col = 16 * s + l16;
-            const float gsh = vec[col], gsl = vec[64 + col];
-            float rks = 1.0f;
-            if constexpr (L2N) rks = vec[256 + col];
+            const f32x4 gsh = lds_ld<f32x4>(sm, L::V0 + (16 * s + 4 * q4) * 4);
+            const f32x4 gsl = lds_ld<f32x4>(sm, L::V0 + 256 + (16 * s + 4 * q4) * 4);
+            f32x4 rks = {1, 1, 1, 1};
+            if constexpr (L2N) rks = lds_ld<f32x4>(sm, L::V0 + 768 + (16 * s + 4 * q4) * 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int row = 16 * wave + 4 * q4 + e;
-                // the exponent is not positive for s <= r; above the diagonal the product is not used
-                const float d = ex2(fminf((gh[e] - gsh) + (gl[e] - gsl), 0.0f)) * rks;
-                A[row * L::AS + col] = col < row ? b4[e] * d * rk4[e] * kk[e] : 0.0f;
-                P[s][e] = col <= row ? p.scale * d * rq4[e] * qk[e] : 0.0f;
+                const int col = 16 * s + 4 * q4 + e;
+                // the exponent is not positive for col <= r; above the diagonal the product is not used
+                const float d = ex2(fminf((gh - gsh[e]) + (gl - gsl[e]), 0.0f)) * rks[e];
+                At[s][e] = col < r ? br * d * kk[e] : 0.0f;
+                Pt[s][e] = col <= r ? sr * d * qk[e] : 0.0f;
             }
         }
     }
-    __syncthreads();  // A is complete; the tiles are done with
-
-    // P and the zero blocks above the diagonal
-    auto st_plane = [&](int plane, int brow, int bcol, f32x4 x) {
-        bf16x4 h, l;
-        split4(x, h, l);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int o = L::PL + plane * L::PLANE + (16 * brow + 4 * q4 + e) * PSTR + 2 * (16 * bcol + l16);
-            lds_st(sm, o, h[e]);
-            lds_st(sm, o + L::PLANE, l[e]);
-        }
+    // blocks 2 j and 2 j + 1 of block row `wave` to the record's planes
+    auto st_pair = [&](int plane, int j, f32x4 x0, f32x4 x1) {
+        bf16x4 h0, l0, h1, l1;
+        split4(x0, h0, l0);
+        split4(x1, h1, l1);
+        char *dst = rec + plane + DeltaRecord::frag(wave, j) + 16 * lane;
+        *reinterpret_cast<bf16x8 *>(dst) = cat4(h0, h1);
+        *reinterpret_cast<bf16x8 *>(dst + DeltaRecord::PLANE) = cat4(l0, l1);
     };
+    st_pair(DeltaRecord::PH, 0, Pt[0], Pt[1]);
+    if (wave >= 2) st_pair(DeltaRecord::PH, 1, Pt[2], Pt[3]);
+    __syncthreads();  // the tiles are done with
+
+    float *A = reinterpret_cast<float *>(sm + L::A0), *TD = reinterpret_cast<float *>(sm + L::T0);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-        if (s <= wave) st_plane(2, wave, s, P[s]);
-    if (!(wave & 1)) {
-        st_plane(2, wave, wave + 1, f32x4{0, 0, 0, 0});
-        st_plane(0, wave, wave + 1, f32x4{0, 0, 0, 0});
-    }
-
+        if (s <= wave)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) A[(16 * s + 4 * q4 + e) * L::AS + r] = At[s][e];
+    __syncthreads();
     // diagonal block `wave` of T: column l16 by forward substitution
-    float *TD = reinterpret_cast<float *>(sm + L::T0);
     {
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == l16 ? 1.0f : 0.0f;
         const float *Ad = A + 16 * wave * L::AS + 16 * wave;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) {
-            float s = x[i];
+        for (int m = 0; m < 15; ++m)
 #pragma unroll
-            for (int m4 = 0; m4 < (i + 3) / 4; ++m4) {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(Ad + i * L::AS + 4 * m4);
+            for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(Ad + m * L::AS + 4 * i4);
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (4 * m4 + m < i) s = fmaf(-a[m], x[4 * m4 + m], s);
+                for (int e = 0; e < 4; ++e)
+                    if (4 * i4 + e > m) x[4 * i4 + e] = fmaf(-a[e], x[m], x[4 * i4 + e]);
             }
-            x[i] = s;
-        }
         if (q4 == 0)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) TD[(16 * wave + i) * L::TS + l16] = x[i];
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4 *>(TD + (16 * wave + l16) * L::TS + 4 * i) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
     }
     __syncthreads();
-    // block column `wave`
-    {
-        f32x4 Tc[4];
+    // block row `wave`, from the diagonal to the left
+    f32x4 Tt[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i < wave) continue;
-            if (i == wave) {
+    for (int s = 3; s >= 0; --s) {
+        Tt[s] = f32x4{0, 0, 0, 0};
+        if (s > wave) continue;
+        if (s == wave) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Tc[i][e] = TD[(16 * i + 4 * q4 + e) * L::TS + l16];
-            } else {
-                f32x4 acc = {0, 0, 0, 0}, res = {0, 0, 0, 0};
+            for (int e = 0; e < 4; ++e) Tt[s][e] = TD[(16 * s + 4 * q4 + e) * L::TS + l16];
+        } else {
+            f32x4 acc = {0, 0, 0, 0}, res = {0, 0, 0, 0};
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    if (m < wave || m >= i) continue;
-                    const f32x4 a = *reinterpret_cast<const f32x4 *>(A + (16 * i + l16) * L::AS + 16 * m + 4 * q4);
+            for (int m = 3; m > s; --m) {
+                if (m > wave) continue;
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(A + (16 * s + l16) * L::AS + 16 * m + 4 * q4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], Tc[m][e], acc, 0, 0, 0);
-                }
-                const f32x4 td = *reinterpret_cast<const f32x4 *>(TD + (16 * i + l16) * L::TS + 4 * q4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) res = __builtin_amdgcn_mfma_f32_16x16x4f32(td[e], acc[e], res, 0, 0, 0);
-                Tc[i] = -res;
+                for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], Tt[m][e], acc, 0, 0, 0);
             }
-            st_plane(0, i, wave, Tc[i]);
+            const f32x4 td = *reinterpret_cast<const f32x4 *>(TD + (16 * s + l16) * L::TS + 4 * q4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) res = __builtin_amdgcn_mfma_f32_16x16x4f32(td[e], acc[e], res, 0, 0, 0);
+            Tt[s] = -res;
         }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-        const int id = t + 256 * i, plane = id / 384, ci = id % 384;
-        int row, col;
-        plane_pos(ci, row, col);
-        *reinterpret_cast<i32x4 *>(rec + plane * DeltaRecord::PLANE + 16 * ci) =
-            lds_ld<i32x4>(sm, L::PL + plane * L::PLANE + row * PSTR + 16 * col);
-    }
+    st_pair(DeltaRecord::TH, 0, Tt[0], Tt[1]);
+    if (wave >= 2) st_pair(DeltaRecord::TH, 1, Tt[2], Tt[3]);
 }
 
 // -------------------------------------------------------- sequential pass --
-// One workgroup per (sequence, value head, 16 NW value columns); wave w owns
-// 16 columns. The next chunk's tiles are loaded into registers while the
-// current one is computed from LDS.
-template <int K, int NP, int NW, bool CKPT>
+// One workgroup per (sequence, value head, 16 NC value columns): NC computing
+// waves, each with 16 columns of S in registers, and 4 waves that stage the
+// chunks two ahead of them (loads a chunk ahead in registers, tiles a chunk
+// ahead in the other half of LDS) and store the outputs of the chunk before.
+// One barrier per chunk; the computing waves touch no global memory but for
+// the state.
+constexpr int LW = 4;  // staging waves
+
+template <int K, int NC, bool CKPT>
 struct StateLds {
     static constexpr int RS = 2 * K + 16;
     static constexpr int TILE = 64 * RS;
+    static constexpr int VS = 32 * NC + 16;  // row stride of the V tile (later the chunk's outputs)
     static constexpr int K0 = 0;
-    static constexpr int Q0 = NP * TILE;
-    static constexpr int PLANE = 64 * PSTR;
-    static constexpr int NPL = CKPT ? 2 : 4;  // T only, or T and P
-    static constexpr int P0 = (CKPT ? 1 : 2) * NP * TILE;
-    static constexpr int V0 = P0 + NPL * PLANE;
-    static constexpr int VB = DeltaRecord::NVEC * 256 + 16;  // vectors and gamma
-    static constexpr int SIZE = V0 + VB;
+    static constexpr int Q0 = TILE;          // (outputs only)
+    static constexpr int V0 = CKPT ? TILE : 2 * TILE;
+    static constexpr int R0 = V0 + 64 * VS;  // the record: planes of T (and P), vectors
+    static constexpr int RP = CKPT ? DeltaRecord::PH : DeltaRecord::VEC;  // bytes of planes
+    static constexpr int RCH = (RP + DeltaRecord::GAMMA + 16 - DeltaRecord::VEC) / 16;
+    static constexpr int G0 = R0 + RP;       // its vectors
+    static constexpr int HALF = R0 + 16 * RCH;
+    static constexpr int SIZE = 2 * HALF;
 };
 
-template <int K, int IO, int NW, bool CKPT>
-__global__ __launch_bounds__(64 * NW) void delta_state_kernel(DeltaParams p)
+template <int K, int IO, int NC, bool CKPT>
+__global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams p)
 {
-    constexpr int NP = IO == IO_F16 ? 2 : 1;
-    using L = StateLds<K, NP, NW, CKPT>;
-    constexpr int NT = 64 * NW;
+    using L = StateLds<K, NC, CKPT>;
     constexpr int KT = K / 16, KS = K / 32;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
-    const int nvb = p.V / (16 * NW);
+    const int nvb = p.V / (16 * NC);
     int item = blockIdx.x;
     const int vb = item % nvb;
     item /= nvb;
@@ -325,186 +312,217 @@ __global__ __launch_bounds__(64 * NW) void delta_state_kernel(DeltaParams p)
     const SeqRange rng = seq_of(p, n);
     const int64_t nch = chunks_of(rng);
     const int64_t slot0 = chunk_slot(rng.b, n, 0);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, q4 = lane >> 4, l16 = lane & 15;
-    const int col = (vb * NW + wave) * 16 + l16;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+
+    if (wave >= NC) {
+        const int t = threadIdx.x - 64 * NC;
+        constexpr int NT = 64 * LW;
+        constexpr int CPT = 64 * K / 8 / NT;             // 16-byte pieces of a K or Q tile per thread
+        constexpr int VCH = 64 * 2 * NC;                 // pieces of the V tile
+        constexpr int VPT = (VCH + NT - 1) / NT;
+        constexpr int RPT = (L::RCH + NT - 1) / NT;
+        i32x4 fk[CPT], fq[CPT], fv[VPT], fr[RPT];
+        auto fetch = [&](int64_t c) {
+            const int64_t t0 = rng.b + c * CHUNK;
+            const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
+            const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
+            const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + K) * 2));
+            const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
+                fk[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
+                if constexpr (!CKPT) fq[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
+                if (VCH % NT == 0 || ci < VCH)
+                    fv[i] = buf_ld16<i32x4>(rv, (uint32_t)(row * (int)p.sv + vb * 16 * NC + cc * 8) * 2);
+            }
+            const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const int id = t + NT * i;  // planes first, then (past P without outputs) the vectors
+                if (id < L::RCH)
+                    fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id + (CKPT && 16 * id >= L::RP ? DeltaRecord::VEC - L::RP : 0));
+            }
+        };
+        auto stage = [&](char *half) {
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
+                lds_st(half, L::K0 + row * L::RS + cc * 16, fk[i]);
+                if constexpr (!CKPT) lds_st(half, L::Q0 + row * L::RS + cc * 16, fq[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
+                if (VCH % NT == 0 || ci < VCH) lds_st(half, L::V0 + row * L::VS + cc * 16, fv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const int id = t + NT * i;
+                if (id < L::RCH) lds_st(half, L::R0 + 16 * id, fr[i]);
+            }
+        };
+        // the outputs of chunk c, left where its V tile was (read and later overwritten by the same thread)
+        auto flush = [&](int64_t c) {
+            const char *half = sm + (c & 1) * L::HALF;
+            const int64_t t0 = rng.b + c * CHUNK;
+            const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
+                if (ci < VCH && row < len)
+                    *reinterpret_cast<i32x4 *>(p.out + (t0 + row) * p.so + hv * p.hso + vb * 16 * NC + cc * 8) =
+                        lds_ld<i32x4>(half, L::V0 + row * L::VS + cc * 16);
+            }
+        };
+        if (nch > 0) {
+            fetch(0);
+            stage(sm);
+            if (nch > 1) fetch(1);
+        }
+        __syncthreads();
+        for (int64_t c = 0; c < nch; ++c) {
+            if constexpr (!CKPT)
+                if (c > 0) flush(c - 1);
+            if (c + 1 < nch) stage(sm + ((c + 1) & 1) * L::HALF);
+            if (c + 2 < nch) fetch(c + 2);
+            __syncthreads();
+        }
+        if constexpr (!CKPT)
+            if (nch > 0) flush(nch - 1);
+        return;
+    }
+
+    const int q4 = lane >> 4, l16 = lane & 15;
+    const int col = (vb * NC + wave) * 16 + l16;
     const int64_t shead = ((int64_t)n * p.HV + hv) * K * p.V;
     const int64_t sr = p.state_vmajor ? 1 : p.V, sc = p.state_vmajor ? K : 1;
-
     f32x4 S[KT];
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc) : 0.0f;
-
-    constexpr int CPT = 64 * K / 8 / NT;                    // 16-byte chunks of a tile per thread
-    constexpr int RCH = L::NPL * 384;
-    constexpr int RPT = (RCH + NT - 1) / NT;                // ... of the record's planes
-    constexpr int VCH = DeltaRecord::NVEC * 16 + 1;         // ... of its vectors
-    static_assert(NT >= VCH, "one vector chunk per thread");
-    i32x4 fk[CPT], fq[CKPT ? 1 : CPT], fr[RPT], fv;
-    uint16_t vv[16];
-
-    auto fetch = [&](int64_t c) {
-        const int64_t t0 = rng.b + c * CHUNK;
-        const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
-        const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-            fk[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
-        }
-        if constexpr (!CKPT) {
-            const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + K) * 2));
-#pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-                fq[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
-            }
-        }
-        const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int id = t + NT * i;
-            if (RCH % NT == 0 || id < RCH) fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id);
-        }
-        if (t < VCH) fv = *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t);
-        const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            vv[i] = __builtin_amdgcn_raw_buffer_load_b16(rv, (uint32_t)((16 * (i >> 2) + 4 * q4 + (i & 3)) * (int)p.sv + col) * 2, 0, 0);
-    };
-    auto stage = [&]() {
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-            st_parts<NP>(sm + L::K0, L::TILE, row * L::RS + cc * 16, fk[i]);
-            if constexpr (!CKPT) st_parts<NP>(sm + L::Q0, L::TILE, row * L::RS + cc * 16, fq[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int id = t + NT * i;
-            if (RCH % NT == 0 || id < RCH) {
-                const int plane = id / 384;
-                int row, cc;
-                plane_pos(id % 384, row, cc);
-                lds_st(sm, L::P0 + plane * L::PLANE + row * PSTR + 16 * cc, fr[i]);
-            }
-        }
-        if (t < VCH) lds_st(sm, L::V0 + 16 * t, fv);
-    };
-
-    if (nch > 0) fetch(0);
+    RightOp<IO, KS> So;
+    So.set(S);
+    __syncthreads();
     for (int64_t c = 0; c < nch; ++c) {
-        const int64_t t0 = rng.b + c * CHUNK;
-        const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
-        float v32[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v32[i] = io_f32<IO>(vv[i]);
-        stage();
-        __syncthreads();
-        if (c + 1 < nch) fetch(c + 1);
+        char *half = sm + (c & 1) * L::HALF;
+        const char *TH = half + L::R0, *TL = TH + DeltaRecord::PLANE, *PH = TL + DeltaRecord::PLANE, *PL = PH + DeltaRecord::PLANE;
+        const int64_t frag = delta_item(p, slot0 + c, hv) * (p.V / 16) + (vb * NC + wave);
+        auto vec4 = [&](int which, int mt) { return lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4); };
+        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
+        const int vo = L::V0 + (4 * q4 + (l16 >> 2)) * L::VS + 2 * (16 * wave + 4 * (l16 & 3));  // of a transpose read
 
-        const int64_t frag = delta_item(p, slot0 + c, hv) * (p.V / 16) + (vb * NW + wave);
-        auto vec4 = [&](int which, int mt) { return lds_ld<f32x4>(sm, L::V0 + which * 256 + (16 * mt + 4 * q4) * 4); };
-        const float gamma = lds_ld<float>(sm, L::V0 + DeltaRecord::NVEC * 256);
-
-        bf16x8 Sh[KS], Sl[KS];
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-            bf16x4 h0, l0, h1, l1;
-            split4(S[2 * j], h0, l0);
-            split4(S[2 * j + 1], h1, l1);
-            Sh[j] = cat4(h0, h1);
-            Sl[j] = cat4(l0, l1);
-        }
         if constexpr (CKPT) {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.s_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = S[i];
         }
-        // [tile] S for the K (and Q) tile at LDS offset `base`: rows 16 mt ..
-        auto times_state = [&](int base, int mt) {
-            f32x4 acc = {0, 0, 0, 0};
+        // (independent accumulators next to each other everywhere: a product
+        // that waits for the one before it takes twice its issue time)
+        // x = (K or Q) S, all 64 rows
+        auto times_state = [&](int base, f32x4 (&x)[4]) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) x[mt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
-                const bf16x8 a = ld_row(sm + base, L::RS, 16 * mt + l16, 32 * j, q4);
-                bf16x8 al = a;
-                if constexpr (NP == 2) al = ld_row(sm + base + L::TILE, L::RS, 16 * mt + l16, 32 * j, q4);
-                acc = mfma_split<NP == 2>(a, al, Sh[j], Sl[j], acc);
+                bf16x8 a[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) a[mt] = ld_row(half + base, L::RS, 16 * mt + l16, 32 * j, q4);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) x[mt] = So.mul1(a[mt], j, part, x[mt]);
             }
-            return acc;
+        };
+        // x += (plane pair) (h + l), lower triangle
+        auto times_lower = [&](const char *hi, const char *lo, const bf16x8 (&h)[2], const bf16x8 (&l)[2], f32x4 (&x)[4]) {
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+                bf16x8 a[4], al[4];
+#pragma unroll
+                for (int mt = 2 * jj; mt < 4; ++mt) {
+                    a[mt] = ld_frag(hi, mt, jj, lane);
+                    al[mt] = ld_frag(lo, mt, jj, lane);
+                }
+#pragma unroll
+                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(a[mt], h[jj], x[mt]);
+#pragma unroll
+                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(a[mt], l[jj], x[mt]);
+#pragma unroll
+                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(al[mt], h[jj], x[mt]);
+            }
+        };
+        auto parts = [&](const f32x4 (&x)[4], bf16x8 (&h)[2], bf16x8 (&l)[2]) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                bf16x4 h0, l0, h1, l1;
+                split4(x[2 * j], h0, l0);
+                split4(x[2 * j + 1], h1, l1);
+                h[j] = cat4(h0, h1);
+                l[j] = cat4(l0, l1);
+            }
         };
         // R = beta (V - e^G K S) as a right operand
-        bf16x8 Rh[2], Rl[2];
+        f32x4 R[4], o[4], U[4], W[4];
+        bf16x8 h2[2], l2[2];
+        times_state(L::K0, R);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bf16x4 h[2], l[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int mt = 2 * j + i;
-                const f32x4 x = times_state(L::K0, mt), eg = vec4(DeltaRecord::EG, mt), bt = vec4(DeltaRecord::BT, mt);
-                f32x4 r;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = bt[e] * (v32[4 * mt + e] - eg[e] * x[e]);
-                split4(r, h[i], l[i]);
-            }
-            Rh[j] = cat4(h[0], h[1]);
-            Rl[j] = cat4(l[0], l[1]);
-        }
+        for (int mt = 0; mt < 4; ++mt)
+            R[mt] = vec4(DeltaRecord::BT, mt) *
+                    (io4_f32<IO>(lds_tr(half, vo + 16 * mt * L::VS)) - vec4(DeltaRecord::EG, mt) * So.scaled(R[mt]));
+        parts(R, h2, l2);
+        if constexpr (!CKPT) times_state(L::Q0, o);
         // U = T R, and e^(G_C - G) U
-        bf16x8 Uh[2], Ul[2], Wh[2], Wl[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bf16x4 h[2], l[2], wh[2], wl[2];
+        for (int mt = 0; mt < 4; ++mt) U[mt] = f32x4{0, 0, 0, 0};
+        times_lower(TH, TL, h2, l2, U);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int mt = 2 * j + i;
-                f32x4 u = {0, 0, 0, 0};
-#pragma unroll
-                for (int jj = 0; jj <= j; ++jj)
-                    u = mfma_split<true>(ld_row(sm + L::P0, PSTR, 16 * mt + l16, 32 * jj, q4),
-                                         ld_row(sm + L::P0 + L::PLANE, PSTR, 16 * mt + l16, 32 * jj, q4), Rh[jj], Rl[jj], u);
-                if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = u;
-                const f32x4 ed = vec4(DeltaRecord::ED, mt);
-                split4(u, h[i], l[i]);
-                split4(u * ed, wh[i], wl[i]);
-            }
-            Uh[j] = cat4(h[0], h[1]);
-            Ul[j] = cat4(l[0], l[1]);
-            Wh[j] = cat4(wh[0], wh[1]);
-            Wl[j] = cat4(wl[0], wl[1]);
+        for (int mt = 0; mt < 4; ++mt) {
+            if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
+            W[mt] = U[mt] * vec4(DeltaRecord::ED, mt);
         }
+        RightOp<IO, 2> Wo;
+        Wo.set(W);
         if constexpr (!CKPT) {
-            const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.out + t0 * p.so + hv * p.hso, (int)(((len - 1) * p.so + p.V) * 2));
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                f32x4 o = times_state(L::Q0, mt) * vec4(DeltaRecord::EQ, mt);
-#pragma unroll
-                for (int jj = 0; jj <= mt / 2; ++jj)
-                    o = mfma_split<true>(ld_row(sm + L::P0 + 2 * L::PLANE, PSTR, 16 * mt + l16, 32 * jj, q4),
-                                         ld_row(sm + L::P0 + 3 * L::PLANE, PSTR, 16 * mt + l16, 32 * jj, q4), Uh[jj], Ul[jj], o);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // a row past the chunk's end lies past the buffer's range and is dropped
-                    __builtin_amdgcn_raw_buffer_store_b16(f32_io<IO>(o[e]), ro, (uint32_t)((16 * mt + 4 * q4 + e) * (int)p.so + col) * 2, 0, 0);
-                }
-            }
+            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * vec4(DeltaRecord::EQ, mt);
         }
         // S <- e^(G_C) S + K^T (e^(G_C - G) U)
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            f32x4 s = S[i] * gamma;
+        for (int i0 = 0; i0 < KT; i0 += 4) {
+            f32x4 s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = IO == IO_F16 ? f32x4{0, 0, 0, 0} : S[i0 + i] * gamma;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bf16x8 a = ld_col(sm + L::K0, L::RS, 32 * j, 16 * i, q4, l16);
-                bf16x8 al = a;
-                if constexpr (NP == 2) al = ld_col(sm + L::K0 + L::TILE, L::RS, 32 * j, 16 * i, q4, l16);
-                s = mfma_split<NP == 2>(a, al, Wh[j], Wl[j], s);
+                bf16x8 a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = ld_col(half + L::K0, L::RS, 32 * j, 16 * (i0 + i), q4, l16);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = Wo.mul1(a[i], j, part, s[i]);
             }
-            S[i] = s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[i0 + i] = IO == IO_F16 ? S[i0 + i] * gamma + s[i] * Wo.inv : s[i];
         }
-        __syncthreads();  // everybody is done with this chunk's tiles
+        So.set(S);
+        if constexpr (!CKPT) {
+            parts(U, h2, l2);
+            times_lower(PH, PL, h2, l2, o);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    lds_st(half, L::V0 + (16 * mt + 4 * q4 + e) * L::VS + 2 * (16 * wave + l16), f32_io<IO>(o[mt][e]));
+        }
+        __syncthreads();
     }
     if (p.ht)
 #pragma unroll
@@ -521,12 +539,20 @@ void launch_wy_l2(const DeltaParams &p, dim3 grid, hipStream_t stream)
     else hipLaunchKernelGGL((delta_wy_kernel<K, IO, false>), grid, dim3(256), 0, stream, p);
 }
 
-template <int K, int IO, int NW>
+template <int K, int IO, int NC>
 void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / (16 * NW))));
-    if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NW, true>), grid, dim3(64 * NW), 0, stream, p);
-    else hipLaunchKernelGGL((delta_state_kernel<K, IO, NW, false>), grid, dim3(64 * NW), 0, stream, p);
+    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / (16 * NC)))), block(64 * (NC + LW));
+    if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, false>), grid, block, 0, stream, p);
+}
+
+template <int K, int IO>
+void launch_state_nc(const DeltaParams &p, bool ckpt, int nc, hipStream_t stream)
+{
+    if (nc == 8) launch_state_ck<K, IO, 8>(p, ckpt, stream);
+    else if (nc == 4) launch_state_ck<K, IO, 4>(p, ckpt, stream);
+    else launch_state_ck<K, IO, 2>(p, ckpt, stream);
 }
 
 }  // namespace
@@ -545,15 +571,23 @@ hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream)
     return hipGetLastError();
 }
 
+int delta_waves(const DeltaParams &p, int ncu)
+{
+    const int64_t chains = (int64_t)p.N * p.HV;
+    for (int nc = 2; nc < p.V / 16; nc *= 2)
+        if (chains * (p.V / (16 * nc)) <= ncu) return nc;
+    return p.V / 16;
+}
+
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream)
 {
-    (void)ncu;
+    const int nc = delta_waves(p, ncu);
     if (p.K == 128) {
-        if (p.io == IO_F16) launch_state_ck<128, IO_F16, 4>(p, ckpt, stream);
-        else launch_state_ck<128, IO_BF16, 4>(p, ckpt, stream);
+        if (p.io == IO_F16) launch_state_nc<128, IO_F16>(p, ckpt, nc, stream);
+        else launch_state_nc<128, IO_BF16>(p, ckpt, nc, stream);
     } else {
-        if (p.io == IO_F16) launch_state_ck<64, IO_F16, 4>(p, ckpt, stream);
-        else launch_state_ck<64, IO_BF16, 4>(p, ckpt, stream);
+        if (p.io == IO_F16) launch_state_nc<64, IO_F16>(p, ckpt, nc, stream);
+        else launch_state_nc<64, IO_BF16>(p, ckpt, nc, stream);
     }
     return hipGetLastError();
 }
