@@ -93,11 +93,11 @@ struct QkParams {
     int32_t groups;
 };
 
-// Value columns per workgroup of the sequential passes, in waves of 16: the
-// fewest (2, 4 or 8) with which every workgroup is resident at once (they
-// hold most of a compute unit's LDS each), so that few chains spread over the
-// device and many do not load a chunk's tiles more often than they must.
-int delta_waves(const DeltaParams &p, int ncu);
+// Value columns per workgroup of the sequential passes: the fewest (32, 64 or
+// 128) with which every workgroup is resident at once (they hold most of a
+// compute unit's LDS each), so that few chains spread over the device and
+// many do not load a chunk's tiles more often than they must.
+int delta_columns(const DeltaParams &p, int ncu);
 hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream);
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream);

@@ -26,16 +26,31 @@ namespace dev {
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr int PSTR = 144;  // LDS row stride of a 64-column bf16 plane (bytes): 16 rows apart in banks by 16 bytes
 
-// x = h + l
+// x = h + l. In pairs: a packed pair of high parts is widened by a shift and
+// a mask, where converting it back element by element costs twice as much.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &l)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x0, x1}, bf16x2));
+    l = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x0 - __uint_as_float(h << 16),
+                                                                    x1 - __uint_as_float(h & 0xffff0000u)}, bf16x2));
+}
 __device__ __forceinline__ void split4(f32x4 x, bf16x4 &h, bf16x4 &l)
 {
-    h = f32x4_to_bf16(x);
-    l = f32x4_to_bf16(x - __builtin_convertvector(h, f32x4));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    uint32_t h0, l0, h1, l1;
+    split2(x[0], x[1], h0, l0);
+    split2(x[2], x[3], h1, l1);
+    h = __builtin_bit_cast(bf16x4, u32x2{h0, h1});
+    l = __builtin_bit_cast(bf16x4, u32x2{l0, l1});
 }
 __device__ __forceinline__ void split8(f32x8 x, bf16x8 &h, bf16x8 &l)
 {
-    h = f32x8_to_bf16(x);
-    l = f32x8_to_bf16(x - __builtin_convertvector(h, f32x8));
+    bf16x4 h0, l0, h1, l1;
+    split4(__builtin_shufflevector(x, x, 0, 1, 2, 3), h0, l0);
+    split4(__builtin_shufflevector(x, x, 4, 5, 6, 7), h1, l1);
+    h = cat4(h0, h1);
+    l = cat4(l0, l1);
 }
 
 template <int IO>
@@ -75,6 +90,42 @@ __device__ __forceinline__ bf16x8 ld_col_plain(const char *base, int stride, int
     const int a = (k0 + 8 * q4 + (l16 >> 2)) * stride + 2 * (c0 + 4 * (l16 & 3));
     return cat4(lds_tr(base, a), lds_tr(base, a + 4 * stride));
 }
+
+// A staged tile of 64 rows of K 16-bit values: the two halves of the columns
+// as sub-tiles of 64 rows of K bytes. It is read in two ways: 16 rows at two
+// runs of 4 columns K / 2 apart (left operands of K S: one run per sub-tile),
+// and 8 rows at 16 columns (transposed, of K^T U). The 16-byte pieces of a row
+// are permuted by the row's bits (swz) so that 32 lanes of either read touch
+// every bank once, and runs, rows 16 apart and tiles lie multiples of 512
+// bytes apart, so that one address per 32-wide step serves all of them.
+template <int K>
+struct Tile {
+    static constexpr int SUB = 64 * K;
+    static constexpr int BYTES = 2 * SUB;
+    __device__ static __forceinline__ int swz(int r)
+    {
+        return K == 128 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : (r >> 2 & 1) << 1 | (r >> 3 & 1);
+    }
+    // byte offset of 16-byte piece c of row r
+    __device__ static __forceinline__ int piece(int r, int c)
+    {
+        return c / (K / 16) * SUB + r * K + (((c % (K / 16)) ^ swz(r)) << 4);
+    }
+    // rows 16 mt + l16, columns 16 j + 4 q4 .. and K / 2 + 16 j + 4 q4 ..
+    __device__ static __forceinline__ bf16x8 row(const char *tile, int mt, int j, int q4, int l16)
+    {
+        const int a = l16 * K + (((2 * j + (q4 >> 1)) ^ swz(l16)) << 4) + 8 * (q4 & 1);
+        return cat4(lds_ld<bf16x4>(tile, a + 16 * K * mt), lds_ld<bf16x4>(tile, a + 16 * K * mt + SUB));
+    }
+    // transposed: element (m, k) = tile[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns m = 16 i + l16
+    __device__ static __forceinline__ bf16x8 col(const char *tile, int i, int j, int q4, int l16)
+    {
+        const int r = 4 * q4 + (l16 >> 2);
+        const int a = r * K + (((2 * (i % (K / 32)) + (l16 >> 1 & 1)) ^ swz(r)) << 4) + 8 * (l16 & 1);
+        const int o = i / (K / 32) * SUB + 32 * K * j;
+        return cat4(lds_tr(tile, a + o), lds_tr(tile, a + o + 16 * K));
+    }
+};
 
 // acc + (ah [+ al]) (bh + bl), without al bl
 template <bool TWO>
@@ -116,12 +167,15 @@ __device__ __forceinline__ bf16x8 ld_frag_t(const char *plane, int mt, int j, in
 __device__ __forceinline__ int64_t delta_item(const DeltaParams &p, int64_t slot, int hv) { return slot * p.HV + hv; }
 
 // A float32 right operand of N 32-row steps in two parts of the io type, for
-// products with rows of q or k. bf16: as everywhere. fp16: the inputs are fp16
+// products with q or k. Step j holds tiles j and j + N (FAR, as Tile::row
+// reads) or 2 j and 2 j + 1 (as Tile::col reads). bf16: as everywhere. fp16: the inputs are fp16
 // values as they stand, so the operand is taken in fp16 too, scaled per column
 // by a power of two that brings its largest value near 2^14: 22 significant
 // bits next to that value, and no value of the state out of fp16's range.
-template <int IO, int N>
+template <int IO, int N, bool FAR>
 struct RightOp {
+    __device__ static constexpr int first(int j) { return FAR ? j : 2 * j; }
+    __device__ static constexpr int second(int j) { return FAR ? j + N : 2 * j + 1; }
     i32x4 h[N], l[N];
     float inv = 1.0f;  // what a product is multiplied by
 
@@ -143,7 +197,7 @@ struct RightOp {
             inv = ldexpf(1.0f, -ex);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const f32x4 y0 = x[2 * j] * sc, y1 = x[2 * j + 1] * sc;
+                const f32x4 y0 = x[first(j)] * sc, y1 = x[second(j)] * sc;
                 const f16x4 h0 = __builtin_convertvector(y0, f16x4), h1 = __builtin_convertvector(y1, f16x4);
                 const f16x4 l0 = __builtin_convertvector(y0 - __builtin_convertvector(h0, f32x4), f16x4);
                 const f16x4 l1 = __builtin_convertvector(y1 - __builtin_convertvector(h1, f32x4), f16x4);
@@ -154,8 +208,8 @@ struct RightOp {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 bf16x4 h0, l0, h1, l1;
-                split4(x[2 * j], h0, l0);
-                split4(x[2 * j + 1], h1, l1);
+                split4(x[first(j)], h0, l0);
+                split4(x[second(j)], h1, l1);
                 h[j] = __builtin_bit_cast(i32x4, cat4(h0, h1));
                 l[j] = __builtin_bit_cast(i32x4, cat4(l0, l1));
             }
@@ -184,6 +238,42 @@ __device__ __forceinline__ f32x4 io4_f32(bf16x4 x)
     if constexpr (IO == IO_F16) return __builtin_convertvector(__builtin_bit_cast(f16x4, x), f32x4);
     else return __builtin_convertvector(x, f32x4);
 }
+
+// 64 tokens of a right operand in two bf16 parts (steps of tiles 0, 1 and 2, 3).
+__device__ __forceinline__ void split_rows(const f32x4 (&x)[4], bf16x8 (&h)[2], bf16x8 (&l)[2])
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        bf16x4 h0, l0, h1, l1;
+        split4(x[2 * j], h0, l0);
+        split4(x[2 * j + 1], h1, l1);
+        h[j] = cat4(h0, h1);
+        l[j] = cat4(l0, l1);
+    }
+}
+
+// Four rows (4 q4 ..) of a wave's 16 columns, rounded to the io type, into a
+// row-major tile of 16-bit values at `at` (the byte of row 4 q4's column 0).
+// Neighbouring lanes trade halves of their rows, so that every store is a
+// whole dword (16-bit stores cost bank conflicts: measured 2200 cycles per
+// chunk with eight waves).
+template <int IO>
+__device__ __forceinline__ void st_rows16(char *at, int stride, f32x4 x, int l16)
+{
+    const uint32_t p0 = (uint32_t)f32_io<IO>(x[0]) | (uint32_t)f32_io<IO>(x[1]) << 16;
+    const uint32_t p1 = (uint32_t)f32_io<IO>(x[2]) | (uint32_t)f32_io<IO>(x[3]) << 16;
+    const bool odd = l16 & 1;
+    const uint32_t keep = odd ? p1 : p0;
+    const uint32_t got = __builtin_amdgcn_update_dpp(0, odd ? p0 : p1, 0xB1, 0xf, 0xf, true);  // lane ^ 1
+    const uint32_t first = odd ? got : keep, second = odd ? keep : got;                        // columns l16 & ~1, | 1
+    char *a = at + (odd ? 2 * stride : 0) + 2 * (l16 & ~1);
+    *reinterpret_cast<uint32_t *>(a) = __builtin_amdgcn_perm(second, first, 0x05040100u);
+    *reinterpret_cast<uint32_t *>(a + stride) = __builtin_amdgcn_perm(second, first, 0x07060302u);
+}
+
+// Nothing moves across: the sequential passes are latency-bound, and a
+// region's loads are those of the products two regions on.
+__device__ __forceinline__ void region() { __builtin_amdgcn_sched_barrier(0); }
 
 // Sum over the 16 lanes of a row (lanes with equal q4); every lane gets it.
 __device__ __forceinline__ float sum16(float x)

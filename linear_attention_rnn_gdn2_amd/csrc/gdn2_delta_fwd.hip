@@ -273,37 +273,42 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
 }
 
 // -------------------------------------------------------- sequential pass --
-// One workgroup per (sequence, value head, 16 NC value columns): NC computing
-// waves, each with 16 columns of S in registers, and 4 waves that stage the
-// chunks two ahead of them (loads a chunk ahead in registers, tiles a chunk
-// ahead in the other half of LDS) and store the outputs of the chunk before.
-// One barrier per chunk; the computing waves touch no global memory but for
-// the state.
+// One workgroup per (sequence, value head, 16 NC value columns): NC
+// computing waves, each with 16 columns of S in registers, and 4
+// waves that stage the chunks two ahead of them (loads a chunk ahead in
+// registers, tiles a chunk ahead in the other half of LDS) and store the
+// outputs of the chunk before. One barrier per chunk; the computing waves
+// touch no global memory but for the states.
+#ifndef MAX64
+#define MAX64 0
+#endif
 constexpr int LW = 4;  // staging waves
 
-template <int K, int NC, bool CKPT>
+template <int K, int COLS, bool CKPT>
 struct StateLds {
-    static constexpr int RS = 2 * K + 16;
-    static constexpr int TILE = 64 * RS;
-    static constexpr int VS = 32 * NC + 16;  // row stride of the V tile (later the chunk's outputs)
+    static constexpr int TILE = Tile<K>::BYTES;
+    static constexpr int VS = 2 * COLS + 16;  // row stride of the V tile (later the chunk's outputs)
     static constexpr int K0 = 0;
-    static constexpr int Q0 = TILE;          // (outputs only)
+    static constexpr int Q0 = TILE;           // (outputs only)
     static constexpr int V0 = CKPT ? TILE : 2 * TILE;
-    static constexpr int R0 = V0 + 64 * VS;  // the record: planes of T (and P), vectors
+    static constexpr int R0 = V0 + 64 * VS;   // the record: planes of T (and P), vectors
     static constexpr int RP = CKPT ? DeltaRecord::PH : DeltaRecord::VEC;  // bytes of planes
     static constexpr int RCH = (RP + DeltaRecord::GAMMA + 16 - DeltaRecord::VEC) / 16;
-    static constexpr int G0 = R0 + RP;       // its vectors
-    static constexpr int HALF = R0 + 16 * RCH;
+    static constexpr int G0 = R0 + RP;        // its vectors
+    static constexpr int HALF = (R0 + 16 * RCH + 511) / 512 * 512;
     static constexpr int SIZE = 2 * HALF;
 };
 
 template <int K, int IO, int NC, bool CKPT>
 __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams p)
 {
-    using L = StateLds<K, NC, CKPT>;
+    constexpr int COLS = 16 * NC;
+    using L = StateLds<K, COLS, CKPT>;
+    using TL = Tile<K>;
     constexpr int KT = K / 16, KS = K / 32;
+    constexpr bool AHEAD = NC < 8;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
-    const int nvb = p.V / (16 * NC);
+    const int nvb = p.V / COLS;
     int item = blockIdx.x;
     const int vb = item % nvb;
     item /= nvb;
@@ -316,11 +321,11 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 
     if (wave >= NC) {
         const int t = threadIdx.x - 64 * NC;
-        constexpr int NT = 64 * LW;
-        constexpr int CPT = 64 * K / 8 / NT;             // 16-byte pieces of a K or Q tile per thread
-        constexpr int VCH = 64 * 2 * NC;                 // pieces of the V tile
-        constexpr int VPT = (VCH + NT - 1) / NT;
-        constexpr int RPT = (L::RCH + NT - 1) / NT;
+        constexpr int TH = 64 * LW;
+        constexpr int CPT = 64 * K / 8 / TH;             // 16-byte pieces of a K or Q tile per thread
+        constexpr int VCH = 64 * COLS / 8;               // pieces of the V tile
+        constexpr int VPT = (VCH + TH - 1) / TH;
+        constexpr int RPT = (L::RCH + TH - 1) / TH;
         i32x4 fk[CPT], fq[CPT], fv[VPT], fr[RPT];
         auto fetch = [&](int64_t c) {
             const int64_t t0 = rng.b + c * CHUNK;
@@ -330,20 +335,20 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
+                const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
                 fk[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
                 if constexpr (!CKPT) fq[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
             }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
-                if (VCH % NT == 0 || ci < VCH)
-                    fv[i] = buf_ld16<i32x4>(rv, (uint32_t)(row * (int)p.sv + vb * 16 * NC + cc * 8) * 2);
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
+                if (VCH % TH == 0 || ci < VCH)
+                    fv[i] = buf_ld16<i32x4>(rv, (uint32_t)(row * (int)p.sv + vb * COLS + cc * 8) * 2);
             }
             const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                const int id = t + NT * i;  // planes first, then (past P without outputs) the vectors
+                const int id = t + TH * i;  // planes first, then (past P without outputs) the vectors
                 if (id < L::RCH)
                     fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id + (CKPT && 16 * id >= L::RP ? DeltaRecord::VEC - L::RP : 0));
             }
@@ -351,18 +356,18 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         auto stage = [&](char *half) {
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-                lds_st(half, L::K0 + row * L::RS + cc * 16, fk[i]);
-                if constexpr (!CKPT) lds_st(half, L::Q0 + row * L::RS + cc * 16, fq[i]);
+                const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
+                lds_st(half, L::K0 + TL::piece(row, cc), fk[i]);
+                if constexpr (!CKPT) lds_st(half, L::Q0 + TL::piece(row, cc), fq[i]);
             }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
-                if (VCH % NT == 0 || ci < VCH) lds_st(half, L::V0 + row * L::VS + cc * 16, fv[i]);
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
+                if (VCH % TH == 0 || ci < VCH) lds_st(half, L::V0 + row * L::VS + cc * 16, fv[i]);
             }
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                const int id = t + NT * i;
+                const int id = t + TH * i;
                 if (id < L::RCH) lds_st(half, L::R0 + 16 * id, fr[i]);
             }
         };
@@ -373,9 +378,9 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int ci = t + NT * i, row = ci / (2 * NC), cc = ci % (2 * NC);
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
                 if (ci < VCH && row < len)
-                    *reinterpret_cast<i32x4 *>(p.out + (t0 + row) * p.so + hv * p.hso + vb * 16 * NC + cc * 8) =
+                    *reinterpret_cast<i32x4 *>(p.out + (t0 + row) * p.so + hv * p.hso + vb * COLS + cc * 8) =
                         lds_ld<i32x4>(half, L::V0 + row * L::VS + cc * 16);
             }
         };
@@ -397,6 +402,10 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         return;
     }
 
+    // The computing waves that share a SIMD start every chunk together; with
+    // one ahead of the other, its matrix products run beside the other's
+    // vector work instead of both waiting for the same unit.
+    if (wave >= 4) __builtin_amdgcn_s_setprio(1);
     const int q4 = lane >> 4, l16 = lane & 15;
     const int col = (vb * NC + wave) * 16 + l16;
     const int64_t shead = ((int64_t)n * p.HV + hv) * K * p.V;
@@ -407,120 +416,193 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc) : 0.0f;
-    RightOp<IO, KS> So;
+    RightOp<IO, KS, true> So;
     So.set(S);
     __syncthreads();
     for (int64_t c = 0; c < nch; ++c) {
         char *half = sm + (c & 1) * L::HALF;
-        const char *TH = half + L::R0, *TL = TH + DeltaRecord::PLANE, *PH = TL + DeltaRecord::PLANE, *PL = PH + DeltaRecord::PLANE;
+        const char *KL = half + L::K0, *QL = half + L::Q0;
+        const char *TH = half + L::R0, *PH = TH + 2 * DeltaRecord::PLANE;
         const int64_t frag = delta_item(p, slot0 + c, hv) * (p.V / 16) + (vb * NC + wave);
-        auto vec4 = [&](int which, int mt) { return lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4); };
-        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
-        const int vo = L::V0 + (4 * q4 + (l16 >> 2)) * L::VS + 2 * (16 * wave + 4 * (l16 & 3));  // of a transpose read
+        auto vec = [&](int which, f32x4 (&x)[4]) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) x[mt] = lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4);
+        };
+        // the left operands of four independent products, and the products
+        auto rows = [&](const char *tile, int j, bf16x8 (&a)[4]) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) a[mt] = TL::row(tile, mt, j, q4, l16);
+        };
+        auto cols = [&](int i0, int j, bf16x8 (&a)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = TL::col(KL, i0 + i, j, q4, l16);
+        };
+        auto times = [&](const auto &op, const bf16x8 (&a)[4], int j, f32x4 (&y)[4]) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = op.mul1(a[i], j, part, y[i]);
+        };
+        auto frags = [&](const char *plane, int j, bf16x8 (&a)[4]) {
+#pragma unroll
+            for (int mt = 2 * j; mt < 4; ++mt) a[mt] = ld_frag(plane, mt, j, lane);
+        };
+        auto lower = [&](const bf16x8 (&ah)[4], const bf16x8 (&al)[4], bf16x8 h, bf16x8 l, int j, f32x4 (&y)[4]) {
+#pragma unroll
+            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(ah[mt], h, y[mt]);
+#pragma unroll
+            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(ah[mt], l, y[mt]);
+#pragma unroll
+            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(al[mt], h, y[mt]);
+        };
+        constexpr f32x4 zero = {0, 0, 0, 0};
+        f32x4 R[4] = {zero, zero, zero, zero}, o[4] = {zero, zero, zero, zero}, U[4] = {zero, zero, zero, zero};
+        f32x4 v[4], bt[4], eg[4];
+        bf16x8 a0[4], a1[4], b0[4], b1[4], h2[2], l2[2];
 
+        // Every block of loads stands where the products two regions before
+        // its use begin (AHEAD), or at its use: two computing waves per SIMD
+        // hide each other's waits, and have a third fewer registers.
+        auto early = [&](auto load) {
+            if constexpr (AHEAD) load();
+        };
+        auto late = [&](auto load) {
+            if constexpr (!AHEAD) load();
+        };
+        auto fence = [&]() {
+            if constexpr (AHEAD) region();
+        };
+        auto rv = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+                v[mt] = io4_f32<IO>(lds_tr(half, L::V0 + (16 * mt + 4 * q4 + (l16 >> 2)) * L::VS + 2 * (16 * wave + 4 * (l16 & 3))));
+            vec(DeltaRecord::EG, eg);
+            vec(DeltaRecord::BT, bt);
+        };
+        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
+
+        // K S
+        early([&] { rows(KL, 0, a0), rows(KL, 1, a1); });
         if constexpr (CKPT) {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.s_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = S[i];
         }
-        // (independent accumulators next to each other everywhere: a product
-        // that waits for the one before it takes twice its issue time)
-        // x = (K or Q) S, all 64 rows
-        auto times_state = [&](int base, f32x4 (&x)[4]) {
+        fence();
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) x[mt] = f32x4{0, 0, 0, 0};
+        for (int j = 0; j < KS; j += 2) {
+            late([&] { rows(KL, j, a0); });
+            times(So, a0, j, R);
+            early([&] {
+                if (j + 2 < KS) rows(KL, j + 2, a0);
+                else if (!CKPT) rows(QL, 0, a0);
+            });
+            fence();
+            late([&] { rows(KL, j + 1, a1); });
+            times(So, a1, j + 1, R);
+            early([&] {
+                if (j + 2 < KS) rows(KL, j + 3, a1);
+                else rv();
+                if (j + 2 >= KS && !CKPT) rows(QL, 1, a1);
+            });
+            fence();
+        }
+        // R = beta (V - e^G K S) as a right operand, beside half of Q S
+        late(rv);
+        early([&] { frags(TH, 0, b0), frags(TH + DeltaRecord::PLANE, 0, b1); });
+        if constexpr (!CKPT && AHEAD) {
+            times(So, a0, 0, o);
+            if (KS > 2) rows(QL, 2, a0);
+            times(So, a1, 1, o);
+            if (KS > 2) rows(QL, 3, a1);
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) R[mt] = bt[mt] * (v[mt] - eg[mt] * So.scaled(R[mt]));
+        split_rows(R, h2, l2);
+        fence();
+        // U = T R, and e^(G_C - G) U, beside the other half
+        late([&] { frags(TH, 0, b0), frags(TH + DeltaRecord::PLANE, 0, b1); });
+        lower(b0, b1, h2[0], l2[0], 0, U);
+        f32x4 ed[4], W[4];
+        early([&] { frags(TH, 1, b0), frags(TH + DeltaRecord::PLANE, 1, b1), vec(DeltaRecord::ED, ed); });
+        fence();
+        late([&] { frags(TH, 1, b0), frags(TH + DeltaRecord::PLANE, 1, b1); });
+        lower(b0, b1, h2[1], l2[1], 1, U);
+        early([&] { cols(0, 0, b0), cols(0, 1, b1); });
+        fence();
+        if constexpr (!CKPT && KS > 2 && AHEAD) {
+            times(So, a0, 2, o);
+            times(So, a1, 3, o);
+        }
+        // O = scale e^G Q S + P U, left where this wave's columns of V were
+        auto store_out = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) st_rows16<IO>(half + L::V0 + (16 * mt + 4 * q4) * L::VS + 32 * wave, L::VS, o[mt], l16);
+        };
+        if constexpr (!CKPT && !AHEAD) {
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
-                bf16x8 a[4];
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) a[mt] = ld_row(half + base, L::RS, 16 * mt + l16, 32 * j, q4);
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) x[mt] = So.mul1(a[mt], j, part, x[mt]);
+                rows(QL, j, a0);
+                times(So, a0, j, o);
             }
-        };
-        // x += (plane pair) (h + l), lower triangle
-        auto times_lower = [&](const char *hi, const char *lo, const bf16x8 (&h)[2], const bf16x8 (&l)[2], f32x4 (&x)[4]) {
+            vec(DeltaRecord::EQ, ed);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                bf16x8 a[4], al[4];
-#pragma unroll
-                for (int mt = 2 * jj; mt < 4; ++mt) {
-                    a[mt] = ld_frag(hi, mt, jj, lane);
-                    al[mt] = ld_frag(lo, mt, jj, lane);
-                }
-#pragma unroll
-                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(a[mt], h[jj], x[mt]);
-#pragma unroll
-                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(a[mt], l[jj], x[mt]);
-#pragma unroll
-                for (int mt = 2 * jj; mt < 4; ++mt) x[mt] = mfma_bf16(al[mt], h[jj], x[mt]);
-            }
-        };
-        auto parts = [&](const f32x4 (&x)[4], bf16x8 (&h)[2], bf16x8 (&l)[2]) {
+            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * ed[mt];
+            split_rows(U, h2, l2);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                bf16x4 h0, l0, h1, l1;
-                split4(x[2 * j], h0, l0);
-                split4(x[2 * j + 1], h1, l1);
-                h[j] = cat4(h0, h1);
-                l[j] = cat4(l0, l1);
+                frags(PH, j, b0);
+                frags(PH + DeltaRecord::PLANE, j, b1);
+                lower(b0, b1, h2[j], l2[j], j, o);
             }
-        };
-        // R = beta (V - e^G K S) as a right operand
-        f32x4 R[4], o[4], U[4], W[4];
-        bf16x8 h2[2], l2[2];
-        times_state(L::K0, R);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-            R[mt] = vec4(DeltaRecord::BT, mt) *
-                    (io4_f32<IO>(lds_tr(half, vo + 16 * mt * L::VS)) - vec4(DeltaRecord::EG, mt) * So.scaled(R[mt]));
-        parts(R, h2, l2);
-        if constexpr (!CKPT) times_state(L::Q0, o);
-        // U = T R, and e^(G_C - G) U
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) U[mt] = f32x4{0, 0, 0, 0};
-        times_lower(TH, TL, h2, l2, U);
+            store_out();
+        }
+        late([&] { vec(DeltaRecord::ED, ed); });
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
-            W[mt] = U[mt] * vec4(DeltaRecord::ED, mt);
+            W[mt] = U[mt] * ed[mt];
         }
-        RightOp<IO, 2> Wo;
+        RightOp<IO, 2, false> Wo;
         Wo.set(W);
-        if constexpr (!CKPT) {
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * vec4(DeltaRecord::EQ, mt);
-        }
+        fence();
         // S <- e^(G_C) S + K^T (e^(G_C - G) U)
+        f32x4 eq[4];
 #pragma unroll
         for (int i0 = 0; i0 < KT; i0 += 4) {
             f32x4 s[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = IO == IO_F16 ? f32x4{0, 0, 0, 0} : S[i0 + i] * gamma;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                bf16x8 a[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = ld_col(half + L::K0, L::RS, 32 * j, 16 * (i0 + i), q4, l16);
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = Wo.mul1(a[i], j, part, s[i]);
-            }
+            for (int i = 0; i < 4; ++i) s[i] = IO == IO_F16 ? zero : S[i0 + i] * gamma;
+            late([&] { cols(i0, 0, b0); });
+            times(Wo, b0, 0, s);
+            early([&] {
+                if (i0 + 4 < KT) cols(i0 + 4, 0, b0);
+                else if (!CKPT) frags(PH, 0, b0);
+            });
+            fence();
+            late([&] { cols(i0, 1, b1); });
+            times(Wo, b1, 1, s);
+            early([&] {
+                if (i0 + 4 < KT) cols(i0 + 4, 1, b1);
+                else if (!CKPT) frags(PH + DeltaRecord::PLANE, 0, b1), vec(DeltaRecord::EQ, eq);
+            });
+            if (!CKPT && AHEAD && i0 == 0) split_rows(U, h2, l2);
+            fence();
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[i0 + i] = IO == IO_F16 ? S[i0 + i] * gamma + s[i] * Wo.inv : s[i];
         }
-        So.set(S);
-        if constexpr (!CKPT) {
-            parts(U, h2, l2);
-            times_lower(PH, PL, h2, l2, o);
+        if constexpr (!CKPT && AHEAD) {
+            // beside the next chunk's operand of S
+            frags(PH, 1, a0);
+            frags(PH + DeltaRecord::PLANE, 1, a1);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    lds_st(half, L::V0 + (16 * mt + 4 * q4 + e) * L::VS + 2 * (16 * wave + l16), f32_io<IO>(o[mt][e]));
+            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * eq[mt];
+            lower(b0, b1, h2[0], l2[0], 0, o);
+            So.set(S);
+            lower(a0, a1, h2[1], l2[1], 1, o);
+            store_out();
+        } else {
+            So.set(S);
         }
         __syncthreads();
     }
@@ -528,8 +610,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                state_st(p.ht, p.ht_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc, S[i][e]);
+            for (int e = 0; e < 4; ++e) state_st(p.ht, p.ht_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc, S[i][e]);
 }
 
 template <int K, int IO>
@@ -548,10 +629,10 @@ void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
 }
 
 template <int K, int IO>
-void launch_state_nc(const DeltaParams &p, bool ckpt, int nc, hipStream_t stream)
+void launch_state_cols(const DeltaParams &p, bool ckpt, int cols, hipStream_t stream)
 {
-    if (nc == 8) launch_state_ck<K, IO, 8>(p, ckpt, stream);
-    else if (nc == 4) launch_state_ck<K, IO, 4>(p, ckpt, stream);
+    if (cols == 128 && !MAX64) launch_state_ck<K, IO, 8>(p, ckpt, stream);
+    else if (cols >= 64) launch_state_ck<K, IO, 4>(p, ckpt, stream);
     else launch_state_ck<K, IO, 2>(p, ckpt, stream);
 }
 
@@ -571,23 +652,23 @@ hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream)
     return hipGetLastError();
 }
 
-int delta_waves(const DeltaParams &p, int ncu)
+int delta_columns(const DeltaParams &p, int ncu)
 {
     const int64_t chains = (int64_t)p.N * p.HV;
-    for (int nc = 2; nc < p.V / 16; nc *= 2)
-        if (chains * (p.V / (16 * nc)) <= ncu) return nc;
-    return p.V / 16;
+    for (int cols = 32; cols < p.V; cols *= 2)
+        if (chains * (p.V / cols) <= ncu) return cols;
+    return p.V;
 }
 
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream)
 {
-    const int nc = delta_waves(p, ncu);
+    const int cols = delta_columns(p, ncu);
     if (p.K == 128) {
-        if (p.io == IO_F16) launch_state_nc<128, IO_F16>(p, ckpt, nc, stream);
-        else launch_state_nc<128, IO_BF16>(p, ckpt, nc, stream);
+        if (p.io == IO_F16) launch_state_cols<128, IO_F16>(p, ckpt, cols, stream);
+        else launch_state_cols<128, IO_BF16>(p, ckpt, cols, stream);
     } else {
-        if (p.io == IO_F16) launch_state_nc<64, IO_F16>(p, ckpt, nc, stream);
-        else launch_state_nc<64, IO_BF16>(p, ckpt, nc, stream);
+        if (p.io == IO_F16) launch_state_cols<64, IO_F16>(p, ckpt, cols, stream);
+        else launch_state_cols<64, IO_BF16>(p, ckpt, cols, stream);
     }
     return hipGetLastError();
 }
