@@ -38,7 +38,8 @@ struct DeltaParams {
     char *rec;
     // backward only. The checkpoints are in accumulator order: per (slot,
     // value head, 16 value columns) the float32 fragments f32x4[tile][lane]
-    // of a wave, tiles of 16 rows (DeltaFrag).
+    // of a wave: lane 16 q4 + l16 holds four rows of column l16, key rows
+    // state_row(tile, q4) .. or tokens 16 tile + 4 q4 ..
     const uint16_t *dout;   // [T, HV, V] io
     const float *dht;       // [N, HV, K, V] or nullptr (zero)
     float *dh0;             // [N, HV, K, V] or nullptr (not written)
@@ -48,7 +49,6 @@ struct DeltaParams {
     uint16_t *dbeta;        // [T, HV] io
     float *s_ck, *ds_ck;    // state entering / gradient of the state leaving each chunk: K x V per item
     float *u_ck, *y_ck;     // U and dY of each chunk: 64 x V per item
-    float *yv;              // [item][V / 16][64]: partial sums of dY . v over 16 columns
     float *dq_ws, *dk_ws;   // [T, HV, K] per value head (grouped heads only)
 };
 

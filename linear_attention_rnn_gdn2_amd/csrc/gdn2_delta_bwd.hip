@@ -20,6 +20,8 @@
 // of decays that spans token t, so that no two sums are subtracted.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include <hip/hip_runtime.h>
 
 #include "gdn2_delta_device.h"
@@ -30,26 +32,53 @@ namespace {
 using namespace dev;
 
 // ----------------------------------------------------- reverse sequential --
-template <int K, int NP, int NW>
-struct BwdStateLds {
-    static constexpr int RS = 2 * K + 16;
-    static constexpr int TILE = 64 * RS;
-    static constexpr int K0 = 0, Q0 = NP * TILE;
-    static constexpr int PLANE = DeltaRecord::PLANE;
-    static constexpr int P0 = 2 * NP * TILE;
-    static constexpr int V0 = P0 + 4 * PLANE;
-    static constexpr int SIZE = V0 + DeltaRecord::NVEC * 256 + 16;
+// As the forward's sequential pass: NC computing waves of 16 value columns
+// each, 4 staging waves. T and P are used transposed, through transpose reads
+// of their planes, which are staged row-major for that (PlaneTile).
+constexpr int LW = 4;  // staging waves
+
+// A record's plane, row-major: columns 0 .. 31 of all rows, then columns
+// 32 .. 63 of rows 32 .. 63 (the others are above the diagonal), in rows of 64
+// bytes whose 16-byte pieces are permuted so that a transpose read touches
+// every bank once.
+struct PlaneTile {
+    static constexpr int BYTES = 6144;
+    __device__ static __forceinline__ int swz(int r) { return (r >> 2 & 1) << 1 | (r >> 3 & 1); }
+    // byte offset of the four columns 4 c .. of row r
+    __device__ static __forceinline__ int quad(int r, int c)
+    {
+        return c / 8 * 2048 + r * 64 + (((c % 8 >> 1) ^ swz(r)) << 4) + 8 * (c & 1);
+    }
+    // transposed: element (m, k) = plane[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns m = 16 i + l16, i <= 2 j + 1
+    __device__ static __forceinline__ bf16x8 col(const char *plane, int i, int j, int q4, int l16)
+    {
+        const int a = quad(4 * q4 + (l16 >> 2), 4 * (i & 1) + (l16 & 3)) + i / 2 * 2048 + 32 * 64 * j;
+        return cat4(lds_tr(plane, a), lds_tr(plane, a + 16 * 64));
+    }
 };
 
-template <int K, int IO, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
+template <int K, int COLS>
+struct BwdStateLds {
+    static constexpr int TILE = Tile<K>::BYTES;
+    static constexpr int OS = 2 * COLS + 16;  // row stride of the dO tile (later the chunk's dV)
+    static constexpr int K0 = 0, Q0 = TILE;
+    static constexpr int O0 = 2 * TILE;
+    static constexpr int R0 = O0 + 64 * OS;   // planes of T and P
+    static constexpr int G0 = R0 + 4 * PlaneTile::BYTES;
+    static constexpr int VCH = (DeltaRecord::GAMMA + 16 - DeltaRecord::VEC) / 16;
+    static constexpr int HALF = (G0 + 16 * VCH + 511) / 512 * 512;
+    static constexpr int SIZE = 2 * HALF;
+};
+
+template <int K, int IO, int NC>
+__global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaParams p)
 {
-    constexpr int NP = IO == IO_F16 ? 2 : 1;
-    using L = BwdStateLds<K, NP, NW>;
-    constexpr int NT = 64 * NW;
+    constexpr int COLS = 16 * NC;
+    using L = BwdStateLds<K, COLS>;
+    using TL = Tile<K>;
     constexpr int KT = K / 16, KS = K / 32;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
-    const int nvb = p.V / (16 * NW);
+    const int nvb = p.V / COLS;
     int item = blockIdx.x;
     const int vb = item % nvb;
     item /= nvb;
@@ -58,194 +87,230 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_state_kernel(DeltaParams p)
     const SeqRange rng = seq_of(p, n);
     const int64_t nch = chunks_of(rng);
     const int64_t slot0 = chunk_slot(rng.b, n, 0);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, q4 = lane >> 4, l16 = lane & 15;
-    const int col = (vb * NW + wave) * 16 + l16;
-    const int64_t shead = ((int64_t)n * p.HV + hv) * K * p.V;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 
+    if (wave >= NC) {
+        const int t = threadIdx.x - 64 * NC;
+        constexpr int TH = 64 * LW;
+        constexpr int CPT = 64 * K / 8 / TH;
+        constexpr int OCH = 64 * COLS / 8, OPT = (OCH + TH - 1) / TH;
+        constexpr int RPT = 4 * DeltaRecord::PLANE / 16 / TH;  // 6
+        static_assert(L::VCH <= TH && 4 * DeltaRecord::PLANE == 16 * RPT * TH, "pieces per thread");
+        i32x4 fk[CPT], fq[CPT], fo[OPT], fr[RPT], fv;
+        auto fetch = [&](int64_t c) {
+            const int64_t t0 = rng.b + c * CHUNK;
+            const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
+            const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
+            const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + K) * 2));
+            const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.dout + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
+                fk[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
+                fq[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
+            }
+#pragma unroll
+            for (int i = 0; i < OPT; ++i) {
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
+                if (OCH % TH == 0 || ci < OCH)
+                    fo[i] = buf_ld16<i32x4>(ro, (uint32_t)(row * (int)p.sv + vb * COLS + cc * 8) * 2);
+            }
+            const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * (t + TH * i));
+            if (t < L::VCH) fv = *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t);
+        };
+        auto stage = [&](char *half) {
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
+                lds_st(half, L::K0 + TL::piece(row, cc), fk[i]);
+                lds_st(half, L::Q0 + TL::piece(row, cc), fq[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < OPT; ++i) {
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
+                if (OCH % TH == 0 || ci < OCH) lds_st(half, L::O0 + row * L::OS + cc * 16, fo[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                // 16 bytes of a fragment: two runs of four columns of one row
+                const int id = t + TH * i, plane = id / 384, f = id % 384 >> 6, ln = id & 63;
+                const int mt = f < 2 ? f : (f + 2) / 2, j = f < 2 ? 0 : f & 1, r = 16 * mt + (ln & 15), c4 = 8 * j + (ln >> 4);
+                char *dst = half + L::R0 + plane * PlaneTile::BYTES;
+                const bf16x8 x = __builtin_bit_cast(bf16x8, fr[i]);
+                lds_st(dst, PlaneTile::quad(r, c4), __builtin_shufflevector(x, x, 0, 1, 2, 3));
+                lds_st(dst, PlaneTile::quad(r, c4 + 4), __builtin_shufflevector(x, x, 4, 5, 6, 7));
+            }
+            if (t < L::VCH) lds_st(half, L::G0 + 16 * t, fv);
+        };
+        // dV of chunk c, left where its dO tile was (read and later overwritten by the same thread)
+        auto flush = [&](int64_t c) {
+            const char *half = sm + (c & 1) * L::HALF;
+            const int64_t t0 = rng.b + c * CHUNK;
+            const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
+#pragma unroll
+            for (int i = 0; i < OPT; ++i) {
+                const int ci = t + TH * i, row = ci / (COLS / 8), cc = ci % (COLS / 8);
+                if (ci < OCH && row < len)
+                    *reinterpret_cast<i32x4 *>(p.dv + (t0 + row) * p.sv + hv * p.hsv + vb * COLS + cc * 8) =
+                        lds_ld<i32x4>(half, L::O0 + row * L::OS + cc * 16);
+            }
+        };
+        if (nch > 0) {
+            fetch(nch - 1);
+            stage(sm + ((nch - 1) & 1) * L::HALF);
+            if (nch > 1) fetch(nch - 2);
+        }
+        __syncthreads();
+        for (int64_t c = nch - 1; c >= 0; --c) {
+            if (c + 1 < nch) flush(c + 1);
+            if (c > 0) stage(sm + ((c - 1) & 1) * L::HALF);
+            if (c > 1) fetch(c - 2);
+            __syncthreads();
+        }
+        if (nch > 0) flush(0);
+        return;
+    }
+
+    const int q4 = lane >> 4, l16 = lane & 15;
+    const int col = (vb * NC + wave) * 16 + l16;
+    const int64_t shead = ((int64_t)n * p.HV + hv) * K * p.V;
     f32x4 dS[KT];
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dS[i][e] = p.dht ? p.dht[shead + (int64_t)(16 * i + 4 * q4 + e) * p.V + col] : 0.0f;
-
-    constexpr int CPT = 64 * K / 8 / NT;
-    constexpr int RCH = 4 * DeltaRecord::PLANE / 16, RPT = (RCH + NT - 1) / NT;
-    constexpr int VCH = DeltaRecord::NVEC * 16 + 1;
-    static_assert(NT >= VCH, "one vector chunk per thread");
-    i32x4 fk[CPT], fq[CPT], fr[RPT], fv;
-    uint16_t vv[16], oo[16];
-
-    auto fetch = [&](int64_t c) {
-        const int64_t t0 = rng.b + c * CHUNK;
-        const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
-        const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
-        const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + K) * 2));
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-            fk[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
-            fq[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
-        }
-        const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int id = t + NT * i;
-            if (RCH % NT == 0 || id < RCH) fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id);
-        }
-        if (t < VCH) fv = *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t);
-        const int bytes = (int)(((len - 1) * p.sv + p.V) * 2);
-        const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, bytes);
-        const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.dout + t0 * p.sv + hv * p.hsv, bytes);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t off = (uint32_t)((16 * (i >> 2) + 4 * q4 + (i & 3)) * (int)p.sv + col) * 2;
-            vv[i] = __builtin_amdgcn_raw_buffer_load_b16(rv, off, 0, 0);
-            oo[i] = __builtin_amdgcn_raw_buffer_load_b16(ro, off, 0, 0);
-        }
-    };
-    auto stage = [&]() {
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (K / 8), cc = ci % (K / 8);
-            st_parts<NP>(sm + L::K0, L::TILE, row * L::RS + cc * 16, fk[i]);
-            st_parts<NP>(sm + L::Q0, L::TILE, row * L::RS + cc * 16, fq[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int id = t + NT * i;
-            if (RCH % NT == 0 || id < RCH) {
-                lds_st(sm, L::P0 + 16 * id, fr[i]);
-            }
-        }
-        if (t < VCH) lds_st(sm, L::V0 + 16 * t, fv);
-    };
-
-    if (nch > 0) fetch(nch - 1);
+        for (int e = 0; e < 4; ++e) dS[i][e] = p.dht ? p.dht[shead + (int64_t)(state_row(i, q4) + e) * p.V + col] : 0.0f;
+    RightOp<IO, KS> So;
+    So.set(dS);
+    __syncthreads();
     for (int64_t c = nch - 1; c >= 0; --c) {
-        const int64_t t0 = rng.b + c * CHUNK;
-        const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
-        float v32[16];
-        f32x4 dO[4];
+        char *half = sm + (c & 1) * L::HALF;
+        const char *KL = half + L::K0, *QL = half + L::Q0;
+        const char *TH = half + L::R0, *PH = TH + 2 * PlaneTile::BYTES;
+        const int64_t frag = delta_item(p, slot0 + c, hv) * (p.V / 16) + (vb * NC + wave);
+        auto vec = [&](int which, f32x4 (&x)[4]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v32[i] = io_f32<IO>(vv[i]);
-            dO[i >> 2][i & 3] = io_f32<IO>(oo[i]);
-        }
-        stage();
-        __syncthreads();
-        if (c > 0) fetch(c - 1);
-
-        const int64_t frag = delta_item(p, slot0 + c, hv) * (p.V / 16) + (vb * NW + wave);
-        auto vec4 = [&](int which, int mt) { return lds_ld<f32x4>(sm, L::V0 + which * 256 + (16 * mt + 4 * q4) * 4); };
-        const float gamma = lds_ld<float>(sm, L::V0 + DeltaRecord::NVEC * 256);
+            for (int mt = 0; mt < 4; ++mt) x[mt] = lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4);
+        };
+        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
         {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.ds_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = dS[i];
         }
-        bf16x8 Sh[KS], Sl[KS];
+        constexpr f32x4 zero = {0, 0, 0, 0};
+        // dU = e^(G_C - G) (K dS) + P^T dO
+        f32x4 U[4] = {zero, zero, zero, zero}, x4[4];
+        bf16x8 a[4], b[4], Uh[2], Ul[2];
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-            bf16x4 h0, l0, h1, l1;
-            split4(dS[2 * j], h0, l0);
-            split4(dS[2 * j + 1], h1, l1);
-            Sh[j] = cat4(h0, h1);
-            Sl[j] = cat4(l0, l1);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) a[mt] = TL::row(KL, mt, j, q4, l16);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) U[mt] = So.mul1(a[mt], j, part, U[mt]);
         }
-        bf16x8 Oh[2], Ol[2];  // dO as a right operand (one part when it is bf16)
+        vec(DeltaRecord::ED, x4);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bf16x4 h0, l0, h1, l1;
-            split4(dO[2 * j], h0, l0);
-            split4(dO[2 * j + 1], h1, l1);
-            Oh[j] = cat4(h0, h1);
-            Ol[j] = cat4(l0, l1);
+        for (int mt = 0; mt < 4; ++mt) U[mt] = So.scaled(U[mt]) * x4[mt];
+        bf16x4 raw[4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+            raw[mt] = lds_tr(half, L::O0 + (16 * mt + 4 * q4 + (l16 >> 2)) * L::OS + 2 * (16 * wave + 4 * (l16 & 3)));
+        f32x4 dO[4];
+        bf16x8 Oh[2], Ol[2];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) dO[mt] = io4_f32<IO>(raw[mt]);
+        if constexpr (IO == IO_F16) {
+            split_rows(dO, Oh, Ol);
+        } else {
+            Oh[0] = cat4(raw[0], raw[1]);
+            Oh[1] = cat4(raw[2], raw[3]);
         }
-        // dU = P^T dO + e^(G_C - G) (K dS)
-        bf16x8 Uh[2], Ul[2];
+        // y += (plane pair)^T (h + l); two: l is there
+        auto upper = [&](const char *plane, const bf16x8 (&h)[2], const bf16x8 (&l)[2], auto two, f32x4 (&y)[4]) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bf16x4 h[2], l[2];
+            for (int jj = 0; jj < 2; ++jj) {
+                const int top = jj ? 4 : 2;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int mt = 2 * j + i;
-                f32x4 u = {0, 0, 0, 0};
-#pragma unroll
-                for (int jj = 0; jj < KS; ++jj) {
-                    const bf16x8 a = ld_row(sm + L::K0, L::RS, 16 * mt + l16, 32 * jj, q4);
-                    bf16x8 al = a;
-                    if constexpr (NP == 2) al = ld_row(sm + L::K0 + L::TILE, L::RS, 16 * mt + l16, 32 * jj, q4);
-                    u = mfma_split<NP == 2>(a, al, Sh[jj], Sl[jj], u);
+                for (int mt = 0; mt < top; ++mt) {
+                    a[mt] = PlaneTile::col(plane, mt, jj, q4, l16);
+                    b[mt] = PlaneTile::col(plane + PlaneTile::BYTES, mt, jj, q4, l16);
                 }
-                u *= vec4(DeltaRecord::ED, mt);
 #pragma unroll
-                for (int jj = j; jj < 2; ++jj) {
-                    const bf16x8 ph = ld_frag_t(sm + L::P0 + 2 * L::PLANE, mt, jj, q4, l16);
-                    const bf16x8 pl = ld_frag_t(sm + L::P0 + 3 * L::PLANE, mt, jj, q4, l16);
-                    u = mfma_bf16(ph, Oh[jj], u);
-                    if constexpr (NP == 2) u = mfma_bf16(ph, Ol[jj], u);
-                    u = mfma_bf16(pl, Oh[jj], u);
-                }
-                split4(u, h[i], l[i]);
+                for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(a[mt], h[jj], y[mt]);
+#pragma unroll
+                for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(b[mt], h[jj], y[mt]);
+                if constexpr (decltype(two)::value)
+#pragma unroll
+                    for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(a[mt], l[jj], y[mt]);
             }
-            Uh[j] = cat4(h[0], h[1]);
-            Ul[j] = cat4(l[0], l[1]);
-        }
-        // dY = T^T dU, dV = beta dY; the right operands e^G dV (negated) and scale e^G dO
-        bf16x8 Eh[2], El[2], Fh[2], Fl[2];
-        const __amdgpu_buffer_rsrc_t rdv = buf_rsrc(p.dv + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
+        };
+        upper(PH, Oh, Ol, std::integral_constant<bool, IO == IO_F16>{}, U);
+        split_rows(U, Uh, Ul);
+        // dY = T^T dU
+        f32x4 Y[4] = {zero, zero, zero, zero};
+        upper(TH, Uh, Ul, std::true_type{}, Y);
+        // dV = beta dY; the right operands e^G dV (negated) and scale e^G dO
+        RightOp<IO, 2> E, F;
+        {
+            f32x4 dv[4];
+            vec(DeltaRecord::BT, x4);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bf16x4 h[2], l[2], fh[2], fl[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int mt = 2 * j + i;
-                f32x4 y = {0, 0, 0, 0};
-#pragma unroll
-                for (int jj = j; jj < 2; ++jj)
-                    y = mfma_split<true>(ld_frag_t(sm + L::P0, mt, jj, q4, l16),
-                                         ld_frag_t(sm + L::P0 + L::PLANE, mt, jj, q4, l16), Uh[jj], Ul[jj], y);
-                reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = y;
-                const f32x4 dv = y * vec4(DeltaRecord::BT, mt), eg = vec4(DeltaRecord::EG, mt), eq = vec4(DeltaRecord::EQ, mt);
-                f32x4 yv;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    __builtin_amdgcn_raw_buffer_store_b16(f32_io<IO>(dv[e]), rdv, (uint32_t)((16 * mt + 4 * q4 + e) * (int)p.sv + col) * 2, 0, 0);
-                    yv[e] = sum16(y[e] * v32[4 * mt + e]);
-                }
-                if (l16 == 0) *reinterpret_cast<f32x4 *>(p.yv + frag * 64 + 16 * mt + 4 * q4) = yv;
-                split4(-(eg * dv), h[i], l[i]);
-                split4(eq * dO[mt], fh[i], fl[i]);
+            for (int mt = 0; mt < 4; ++mt) {
+                reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = Y[mt];
+                dv[mt] = Y[mt] * x4[mt];
+                st_rows16<IO>(half + L::O0 + (16 * mt + 4 * q4) * L::OS + 32 * wave, L::OS, dv[mt], l16);
             }
-            Eh[j] = cat4(h[0], h[1]);
-            El[j] = cat4(l[0], l[1]);
-            Fh[j] = cat4(fh[0], fh[1]);
-            Fl[j] = cat4(fl[0], fl[1]);
+            vec(DeltaRecord::EG, x4);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) dv[mt] *= -x4[mt];
+            E.set(dv);
+            vec(DeltaRecord::EQ, x4);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) dO[mt] *= x4[mt];
+            F.set(dO);
         }
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            f32x4 s = dS[i] * gamma;
+        for (int i0 = 0; i0 < KT; i0 += 4) {
+            f32x4 s[4], w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i] = IO == IO_F16 ? zero : dS[i0 + i] * gamma;
+                w[i] = zero;
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bf16x8 a = ld_col(sm + L::K0, L::RS, 32 * j, 16 * i, q4, l16);
-                const bf16x8 b = ld_col(sm + L::Q0, L::RS, 32 * j, 16 * i, q4, l16);
-                bf16x8 al = a, bl = b;
-                if constexpr (NP == 2) {
-                    al = ld_col(sm + L::K0 + L::TILE, L::RS, 32 * j, 16 * i, q4, l16);
-                    bl = ld_col(sm + L::Q0 + L::TILE, L::RS, 32 * j, 16 * i, q4, l16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = TL::col(KL, i0 + i, j, q4, l16);
+                    b[i] = TL::col(QL, i0 + i, j, q4, l16);
                 }
-                s = mfma_split<NP == 2>(a, al, Eh[j], El[j], s);
-                s = mfma_split<NP == 2>(b, bl, Fh[j], Fl[j], s);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = E.mul1(a[i], j, part, s[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (IO == IO_F16) w[i] = F.mul1(b[i], j, part, w[i]);
+                        else s[i] = F.mul1(b[i], j, part, s[i]);
+                    }
+                }
             }
-            dS[i] = s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dS[i0 + i] = IO == IO_F16 ? dS[i0 + i] * gamma + s[i] * E.inv + w[i] * F.inv : s[i];
         }
+        So.set(dS);
         __syncthreads();
     }
     if (p.dh0)
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p.dh0[shead + (int64_t)(16 * i + 4 * q4 + e) * p.V + col] = dS[i][e];
+            for (int e = 0; e < 4; ++e) p.dh0[shead + (int64_t)(state_row(i, q4) + e) * p.V + col] = dS[i][e];
 }
 
 // --------------------------------------------------------- all gradients --
@@ -262,9 +327,9 @@ struct GradLds {
     static constexpr int W0 = 2 * NP * TILE;  // the block of 32 value columns
     static constexpr int OS = 80;             // row stride of the dO block (bytes)
     static constexpr int OT = 64 * OS;
-    static constexpr int O0 = W0;
+    static constexpr int O0 = W0, VT0 = O0 + NP * OT;  // dO and V: [token][32]
     static constexpr int VP = 32 * PSTR;      // a plane of U or dY: [v][64 tokens]
-    static constexpr int U0 = O0 + NP * OT, Y0 = U0 + 2 * VP;
+    static constexpr int U0 = VT0 + NP * OT, Y0 = U0 + 2 * VP;
     static constexpr int SP = 32 * RS;        // a plane of S or dS: [v][D]
     static constexpr int S0 = Y0 + 2 * VP, DS0 = S0 + 2 * SP;
     static constexpr int WEND = DS0 + 2 * SP;
@@ -279,7 +344,8 @@ struct GradLds {
     static constexpr int VEC = R0;
     static constexpr int RED = VEC + DeltaRecord::NVEC * 256 + 16;  // [wave][3][64]
     static constexpr int ROW = RED + NWV * 3 * 256;                 // [4][64]
-    static constexpr int DOT = ROW + 4 * 256;                       // [wave]
+    static constexpr int YV = ROW + 4 * 256;                        // [64]
+    static constexpr int DOT = YV + 256;                            // [wave]
     static constexpr int SIZE = DOT + 16 * NWV;
 };
 
@@ -325,6 +391,7 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
     if (t < VCH) lds_st(sm, L::VEC + 16 * t, *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t));
 
     const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.dout + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + D) * 2));
+    const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + D) * 2));
     const f32x4 *s_ck = reinterpret_cast<const f32x4 *>(p.s_ck) + item * (D / 16) * (D / 16 * 64);
     const f32x4 *ds_ck = reinterpret_cast<const f32x4 *>(p.ds_ck) + item * (D / 16) * (D / 16 * 64);
     const f32x4 *u_ck = reinterpret_cast<const f32x4 *>(p.u_ck) + item * (D / 16) * 256;
@@ -334,7 +401,7 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
     constexpr int SPT = 2 * (D / 16) * 64 / NT;  // 2
     constexpr int UPT = 512 / NT;                // 1 (D = 128), 2 (D = 64)
     f32x4 fs[SPT], fd[SPT], fu[UPT], fy[UPT];
-    i32x4 fo;
+    i32x4 fo, fv;
     auto fetch = [&](int vb) {
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
@@ -346,11 +413,16 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
             fu[i] = u_ck[vb * 512 + t + NT * i];
             fy[i] = y_ck[vb * 512 + t + NT * i];
         }
-        if (t < 256) fo = buf_ld16<i32x4>(ro, (uint32_t)((t >> 2) * (int)p.sv + vb * 32 + (t & 3) * 8) * 2);
+        if (t < 256) {
+            const uint32_t off = (uint32_t)((t >> 2) * (int)p.sv + vb * 32 + (t & 3) * 8) * 2;
+            fo = buf_ld16<i32x4>(ro, off);
+            fv = buf_ld16<i32x4>(rv, off);
+        }
     };
-    auto st_frag = [&](int base, int plane, int stride, f32x4 x, int id, int tiles) {
+    auto st_frag = [&](int base, int plane, int stride, f32x4 x, int id, int tiles, bool state) {
         // fragment id -> (16 columns, tile, lane): 4 consecutive rows of one value column
-        const int ln = id & 63, tile = (id >> 6) % tiles, v = (id >> 6) / tiles * 16 + (ln & 15), r = 16 * tile + 4 * (ln >> 4);
+        const int ln = id & 63, tile = (id >> 6) % tiles, v = (id >> 6) / tiles * 16 + (ln & 15);
+        const int r = state ? state_row(tile, ln >> 4) : 16 * tile + 4 * (ln >> 4);
         bf16x4 h, l;
         split4(x, h, l);
         lds_st(sm, base + v * stride + 2 * r, h);
@@ -369,22 +441,26 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
         br = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3;
         bc = id - br * (br + 1) / 2;
     };
+    f32x4 yv = {0, 0, 0, 0};
     float dot = 0.0f;  // <S, dS>
     fetch(0);
     for (int vb = 0; vb < D / 32; ++vb) {
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
-            st_frag(L::S0, L::SP, L::RS, fs[i], t + NT * i, D / 16);
-            st_frag(L::DS0, L::SP, L::RS, fd[i], t + NT * i, D / 16);
+            st_frag(L::S0, L::SP, L::RS, fs[i], t + NT * i, D / 16, true);
+            st_frag(L::DS0, L::SP, L::RS, fd[i], t + NT * i, D / 16, true);
 #pragma unroll
             for (int e = 0; e < 4; ++e) dot = fmaf(fs[i][e], fd[i][e], dot);
         }
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            st_frag(L::U0, L::VP, PSTR, fu[i], t + NT * i, 4);
-            st_frag(L::Y0, L::VP, PSTR, fy[i], t + NT * i, 4);
+            st_frag(L::U0, L::VP, PSTR, fu[i], t + NT * i, 4, false);
+            st_frag(L::Y0, L::VP, PSTR, fy[i], t + NT * i, 4, false);
         }
-        if (t < 256) st_parts<NP>(sm + L::O0, L::OT, (t >> 2) * L::OS + (t & 3) * 16, fo);
+        if (t < 256) {
+            st_parts<NP>(sm + L::O0, L::OT, (t >> 2) * L::OS + (t & 3) * 16, fo);
+            st_parts<NP>(sm + L::VT0, L::OT, (t >> 2) * L::OS + (t & 3) * 16, fv);
+        }
         __syncthreads();
         if (vb + 1 < D / 32) fetch(vb + 1);
         const bf16x8 sh = ld_col_plain(sm + L::S0, L::RS, 0, 16 * wave, q4, l16);
@@ -415,8 +491,17 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
                 yu[i] = mfma_split<true>(v_col(L::Y0, 0, br), v_col(L::Y0, 1, br), uh, ul, yu[i]);
             }
         }
+        if (wave < 4) {  // the diagonal of dY V^T, block `wave`
+            const bf16x8 vh = ld_row_plain(sm + L::VT0, L::OS, 16 * wave + l16, 0, q4);
+            const bf16x8 yh = v_col(L::Y0, 0, wave), yl = v_col(L::Y0, 1, wave);
+            yv = mfma_bf16(yh, vh, yv);
+            yv = mfma_bf16(yl, vh, yv);
+            if constexpr (NP == 2) yv = mfma_bf16(yh, ld_row_plain(sm + L::VT0 + L::OT, L::OS, 16 * wave + l16, 0, q4), yv);
+        }
         __syncthreads();
     }
+    if (wave < 4 && l16 >> 2 == q4)  // row 4 q4 + e = column l16
+        *reinterpret_cast<float *>(sm + L::YV + 4 * (16 * wave + l16)) = l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0]);
 
     // score gradients: the same tiles of Q K^T and K K^T, decayed
     const float *vec = reinterpret_cast<const float *>(sm + L::VEC);
@@ -552,7 +637,7 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
     if (wave != 0) return;
 
     // the scalars: lane = token
-    float I = 0.0f, Y = 0.0f, X = 0.0f, sd = 0.0f, yv = 0.0f, rs = 0.0f;
+    float I = 0.0f, Y = 0.0f, X = 0.0f, sd = 0.0f, rs = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         const float *r = reinterpret_cast<const float *>(sm + L::RED) + w * 192;
@@ -560,11 +645,10 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
         Y += r[64 + lane];
         X += r[128 + lane];
         sd += lds_ld<float>(sm, L::DOT + 4 * w);
-        yv += p.yv[(item * NW + w) * 64 + lane];
     }
     for (int b = 0; b <= lane >> 4; ++b) rs += rowsum[b * 64 + lane];
     const float bt = vec[DeltaRecord::BT * 64 + lane];
-    const float dbeta = yv - Y - rs;
+    const float dbeta = lds_ld<float>(sm, L::YV + 4 * lane) - Y - rs;
     I -= bt * Y;
     // row `lane` of E to sums over the columns before each
     float run = 0.0f;
@@ -597,16 +681,29 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
 
 }  // namespace
 
+template <int K, int IO>
+static void launch_bwd_state_cols(const DeltaParams &p, int cols, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / cols)));
+    if (cols == 128) {
+        // (K = V: 128 columns only with 128 key rows)
+        if constexpr (K == 128) hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 8>), grid, dim3(64 * (8 + LW)), 0, stream, p);
+    } else if (cols == 64) {
+        hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 4>), grid, dim3(64 * (4 + LW)), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 2>), grid, dim3(64 * (2 + LW)), 0, stream, p);
+    }
+}
+
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream)
 {
-    (void)ncu;
-    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / 64)));
+    const int cols = delta_columns(p, ncu);
     if (p.K == 128) {
-        if (p.io == IO_F16) hipLaunchKernelGGL((delta_bwd_state_kernel<128, IO_F16, 4>), grid, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL((delta_bwd_state_kernel<128, IO_BF16, 4>), grid, dim3(256), 0, stream, p);
+        if (p.io == IO_F16) launch_bwd_state_cols<128, IO_F16>(p, cols, stream);
+        else launch_bwd_state_cols<128, IO_BF16>(p, cols, stream);
     } else {
-        if (p.io == IO_F16) hipLaunchKernelGGL((delta_bwd_state_kernel<64, IO_F16, 4>), grid, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL((delta_bwd_state_kernel<64, IO_BF16, 4>), grid, dim3(256), 0, stream, p);
+        if (p.io == IO_F16) launch_bwd_state_cols<64, IO_F16>(p, cols, stream);
+        else launch_bwd_state_cols<64, IO_BF16>(p, cols, stream);
     }
     return hipGetLastError();
 }

@@ -91,39 +91,38 @@ __device__ __forceinline__ bf16x8 ld_col_plain(const char *base, int stride, int
     return cat4(lds_tr(base, a), lds_tr(base, a + 4 * stride));
 }
 
-// A staged tile of 64 rows of K 16-bit values: the two halves of the columns
-// as sub-tiles of 64 rows of K bytes. It is read in two ways: 16 rows at two
-// runs of 4 columns K / 2 apart (left operands of K S: one run per sub-tile),
-// and 8 rows at 16 columns (transposed, of K^T U). The 16-byte pieces of a row
-// are permuted by the row's bits (swz) so that 32 lanes of either read touch
-// every bank once, and runs, rows 16 apart and tiles lie multiples of 512
-// bytes apart, so that one address per 32-wide step serves all of them.
+// The state's rows in accumulator tiles: rows 4 q4 .. of tile i are key rows
+// state_row(i, q4) .. + 3, so that two tiles (2 j, 2 j + 1) as a right operand
+// hold eight consecutive key rows per lane, and the left operand beside them
+// is one 16-byte read of a row of K or Q.
+__device__ __forceinline__ int state_row(int i, int q4) { return 32 * (i >> 1) + 8 * q4 + 4 * (i & 1); }
+
+// A staged tile of 64 rows of K 16-bit values, read in two ways: 16 rows at 8
+// columns (left operands of K S), and transposed, 8 rows at 4 runs of 4
+// columns (of K^T U). The 16-byte pieces of a row are permuted by the row's
+// bits (swz): the first read then touches every bank once, the second twice
+// at most (its runs all lie in one half of their pieces).
 template <int K>
 struct Tile {
-    static constexpr int SUB = 64 * K;
-    static constexpr int BYTES = 2 * SUB;
+    static constexpr int RS = 2 * K;
+    static constexpr int BYTES = 64 * RS;
     __device__ static __forceinline__ int swz(int r)
     {
-        return K == 128 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : (r >> 2 & 1) << 1 | (r >> 3 & 1);
+        return K == 128 ? (r >> 1 & 3) << 2 | (r & 1) << 1 | (r >> 3 & 1) : (r >> 1 & 1) << 2 | (r >> 2 & 3);
     }
     // byte offset of 16-byte piece c of row r
-    __device__ static __forceinline__ int piece(int r, int c)
-    {
-        return c / (K / 16) * SUB + r * K + (((c % (K / 16)) ^ swz(r)) << 4);
-    }
-    // rows 16 mt + l16, columns 16 j + 4 q4 .. and K / 2 + 16 j + 4 q4 ..
+    __device__ static __forceinline__ int piece(int r, int c) { return r * RS + ((c ^ swz(r)) << 4); }
+    // rows 16 mt + l16, columns 32 j + 8 q4 ..
     __device__ static __forceinline__ bf16x8 row(const char *tile, int mt, int j, int q4, int l16)
     {
-        const int a = l16 * K + (((2 * j + (q4 >> 1)) ^ swz(l16)) << 4) + 8 * (q4 & 1);
-        return cat4(lds_ld<bf16x4>(tile, a + 16 * K * mt), lds_ld<bf16x4>(tile, a + 16 * K * mt + SUB));
+        return lds_ld<bf16x8>(tile, l16 * RS + (((4 * j + q4) ^ swz(l16)) << 4) + 16 * RS * mt);
     }
-    // transposed: element (m, k) = tile[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns m = 16 i + l16
+    // transposed: element (m, k) = tile[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns those of state tile i
     __device__ static __forceinline__ bf16x8 col(const char *tile, int i, int j, int q4, int l16)
     {
         const int r = 4 * q4 + (l16 >> 2);
-        const int a = r * K + (((2 * (i % (K / 32)) + (l16 >> 1 & 1)) ^ swz(r)) << 4) + 8 * (l16 & 1);
-        const int o = i / (K / 32) * SUB + 32 * K * j;
-        return cat4(lds_tr(tile, a + o), lds_tr(tile, a + o + 16 * K));
+        const int a = r * RS + (((4 * (i >> 1) + (l16 & 3)) ^ swz(r)) << 4) + 8 * (i & 1) + 32 * RS * j;
+        return cat4(lds_tr(tile, a), lds_tr(tile, a + 16 * RS));
     }
 };
 
@@ -151,31 +150,21 @@ __device__ __forceinline__ void st_parts(char *base, int plane_bytes, int off, i
     }
 }
 
-// A record's fragment as a left operand, and the same plane transposed:
-// element (m, k) is plane[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 ..,
-// columns m = 16 mt + l16 (mt <= 2 j + 1).
+// A record's fragment as a left operand.
 __device__ __forceinline__ bf16x8 ld_frag(const char *plane, int mt, int j, int lane)
 {
     return *reinterpret_cast<const bf16x8 *>(plane + DeltaRecord::frag(mt, j) + 16 * lane);
-}
-__device__ __forceinline__ bf16x8 ld_frag_t(const char *plane, int mt, int j, int q4, int l16)
-{
-    const int a = ((l16 & 3) * 16 + 4 * q4 + (l16 >> 2)) * 16 + (mt & 1) * 8;
-    return cat4(lds_tr(plane, DeltaRecord::frag(2 * j, mt / 2) + a), lds_tr(plane, DeltaRecord::frag(2 * j + 1, mt / 2) + a));
 }
 
 __device__ __forceinline__ int64_t delta_item(const DeltaParams &p, int64_t slot, int hv) { return slot * p.HV + hv; }
 
 // A float32 right operand of N 32-row steps in two parts of the io type, for
-// products with q or k. Step j holds tiles j and j + N (FAR, as Tile::row
-// reads) or 2 j and 2 j + 1 (as Tile::col reads). bf16: as everywhere. fp16: the inputs are fp16
+// products with q or k (step j: tiles 2 j and 2 j + 1). bf16: as everywhere. fp16: the inputs are fp16
 // values as they stand, so the operand is taken in fp16 too, scaled per column
 // by a power of two that brings its largest value near 2^14: 22 significant
 // bits next to that value, and no value of the state out of fp16's range.
-template <int IO, int N, bool FAR>
+template <int IO, int N>
 struct RightOp {
-    __device__ static constexpr int first(int j) { return FAR ? j : 2 * j; }
-    __device__ static constexpr int second(int j) { return FAR ? j + N : 2 * j + 1; }
     i32x4 h[N], l[N];
     float inv = 1.0f;  // what a product is multiplied by
 
@@ -197,7 +186,7 @@ struct RightOp {
             inv = ldexpf(1.0f, -ex);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const f32x4 y0 = x[first(j)] * sc, y1 = x[second(j)] * sc;
+                const f32x4 y0 = x[2 * j] * sc, y1 = x[2 * j + 1] * sc;
                 const f16x4 h0 = __builtin_convertvector(y0, f16x4), h1 = __builtin_convertvector(y1, f16x4);
                 const f16x4 l0 = __builtin_convertvector(y0 - __builtin_convertvector(h0, f32x4), f16x4);
                 const f16x4 l1 = __builtin_convertvector(y1 - __builtin_convertvector(h1, f32x4), f16x4);
@@ -208,8 +197,8 @@ struct RightOp {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 bf16x4 h0, l0, h1, l1;
-                split4(x[first(j)], h0, l0);
-                split4(x[second(j)], h1, l1);
+                split4(x[2 * j], h0, l0);
+                split4(x[2 * j + 1], h1, l1);
                 h[j] = __builtin_bit_cast(i32x4, cat4(h0, h1));
                 l[j] = __builtin_bit_cast(i32x4, cat4(l0, l1));
             }

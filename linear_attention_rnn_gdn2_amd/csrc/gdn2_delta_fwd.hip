@@ -415,8 +415,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc) : 0.0f;
-    RightOp<IO, KS, true> So;
+            S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (state_row(i, q4) + e) * sr + col * sc) : 0.0f;
+    RightOp<IO, KS> So;
     So.set(S);
     __syncthreads();
     for (int64_t c = 0; c < nch; ++c) {
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
             W[mt] = U[mt] * ed[mt];
         }
-        RightOp<IO, 2, false> Wo;
+        RightOp<IO, 2> Wo;
         Wo.set(W);
         fence();
         // S <- e^(G_C) S + K^T (e^(G_C - G) U)
@@ -610,7 +610,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) state_st(p.ht, p.ht_bf16, shead + (16 * i + 4 * q4 + e) * sr + col * sc, S[i][e]);
+            for (int e = 0; e < 4; ++e) state_st(p.ht, p.ht_bf16, shead + (state_row(i, q4) + e) * sr + col * sc, S[i][e]);
 }
 
 template <int K, int IO>
