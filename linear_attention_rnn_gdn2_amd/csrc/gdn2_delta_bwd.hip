@@ -318,42 +318,90 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 // products that contract the value dimension run over 32 columns at a time,
 // staged value-major ([v][k] and [v][token], as the checkpoints' fragments
 // hold them); wave w owns key columns 16 w .. 16 w + 15 of dQ and dK and
-// every (D / 16)-th 16x16 tile of the two score gradients.
+// every (D / 16)-th 16x16 tile of the two score gradients, computed
+// transposed: a lane then holds four columns of one row r. Two workgroups
+// share a compute unit and hide each other's loads (with bf16 inputs, 128
+// registers; one with the next block's loads in registers was slower, 1.75 ms
+// against the figure below), so that nothing is fetched ahead.
+
+// 32 rows (v) of C 16-bit values, written 8 bytes at a time down 16 rows and
+// read transposed from 4 rows and the 4 rows 8 further on: pieces of 16 bytes
+// permuted by the row, their halves by the piece, both without conflicts.
+template <int C>
+struct ValueTile {
+    static constexpr int BYTES = 64 * C;
+    __device__ static __forceinline__ int swz(int r)
+    {
+        return C == 128 ? (r >> 3 & 1) << 3 | (r & 3) << 1 | (r >> 2 & 1) : (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1 | (r >> 2 & 1);
+    }
+    // byte offset of the four columns 4 c .. of row r
+    __device__ static __forceinline__ int quad(int r, int c)
+    {
+        return r * 2 * C + (((c >> 1) ^ swz(r)) << 4) + 8 * ((c ^ c >> 1) & 1);
+    }
+    // transposed: element (m, k) = tile[k][m], rows k = 8 q4 .., columns m = 16 w + l16
+    __device__ static __forceinline__ bf16x8 col(const char *tile, int w, int q4, int l16)
+    {
+        const int r = 8 * q4 + (l16 >> 2), c = 4 * w + (l16 & 3);
+        return cat4(lds_tr(tile, quad(r, c)), lds_tr(tile, quad(r + 4, c)));
+    }
+};
+// 64 rows (tokens) of 32 16-bit values: 16-byte piece c of row r.
+__device__ __forceinline__ int token_piece(int r, int c) { return r * 64 + ((c ^ (r >> 2 & 3)) << 4); }
+
 template <int D, int NP>
 struct GradLds {
-    static constexpr int RS = 2 * D + 16;
-    static constexpr int TILE = 64 * RS;
-    static constexpr int K0 = 0, Q0 = NP * TILE;
-    static constexpr int W0 = 2 * NP * TILE;  // the block of 32 value columns
-    static constexpr int OS = 80;             // row stride of the dO block (bytes)
-    static constexpr int OT = 64 * OS;
-    static constexpr int O0 = W0, VT0 = O0 + NP * OT;  // dO and V: [token][32]
-    static constexpr int VP = 32 * PSTR;      // a plane of U or dY: [v][64 tokens]
-    static constexpr int U0 = VT0 + NP * OT, Y0 = U0 + 2 * VP;
-    static constexpr int SP = 32 * RS;        // a plane of S or dS: [v][D]
+    // the block of 32 value columns
+    static constexpr int OT = 64 * 64;        // a part of dO or V
+    static constexpr int O0 = 0, VT0 = NP * OT;
+    static constexpr int VP = ValueTile<64>::BYTES;
+    static constexpr int U0 = 2 * NP * OT, Y0 = U0 + 2 * VP;
+    static constexpr int SP = ValueTile<D>::BYTES;
     static constexpr int S0 = Y0 + 2 * VP, DS0 = S0 + 2 * SP;
     static constexpr int WEND = DS0 + 2 * SP;
-    // over it, once all value columns are done: E, and the score gradients' planes
-    static constexpr int ES = 65;             // floats per row of E
-    static constexpr int E0 = W0;
-    static constexpr int PLANE = 64 * PSTR;
-    static constexpr int DP0 = (E0 + 64 * ES * 4 + 15) / 16 * 16, DA0 = DP0 + 2 * PLANE;
-    static constexpr int XEND = DA0 + 2 * PLANE;
-    static constexpr int R0 = WEND > XEND ? WEND : XEND;  // vectors, and sums to join over waves and tiles
+    // over it, once all value columns are done: K, Q, and the score gradients' planes
+    static constexpr int TILE = Tile<D>::BYTES;
+    static constexpr int K0 = 0, Q0 = NP * TILE;
+    static constexpr int DP0 = 2 * NP * TILE, DA0 = DP0 + 2 * PlaneTile::BYTES;
+    static constexpr int XEND = DA0 + 2 * PlaneTile::BYTES;
+    // vectors, and sums to join over waves and tiles
     static constexpr int NWV = D / 16;
-    static constexpr int VEC = R0;
+    static constexpr int VEC = WEND > XEND ? WEND : XEND;
     static constexpr int RED = VEC + DeltaRecord::NVEC * 256 + 16;  // [wave][3][64]
-    static constexpr int ROW = RED + NWV * 3 * 256;                 // [4][64]
-    static constexpr int YV = ROW + 4 * 256;                        // [64]
+    static constexpr int ES = 20;                                   // floats per row of a diagonal block of E
+    static constexpr int ED = RED + NWV * 3 * 256;                  // the four diagonal blocks: [64][ES]
+    static constexpr int ROW = ED + 64 * ES * 4;                    // row sums of the tiles of E, by block column: [3][64]
+    static constexpr int COL = ROW + 3 * 256;                       // column sums, by block row - 1: [3][64]
+    static constexpr int KKR = COL + 3 * 256;                       // row sums of D kk (dY U^T): [4][64]
+    static constexpr int YV = KKR + 4 * 256;                        // [64]
     static constexpr int DOT = YV + 256;                            // [wave]
     static constexpr int SIZE = DOT + 16 * NWV;
 };
 
+// The value again, as one the compiler knows nothing of: what is computed
+// from it stays where it is used (the lanes' LDS addresses, held over the
+// whole kernel, would take 30 registers more than there are).
+__device__ __forceinline__ int fresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Sum over the four lanes of a column (equal l16); every lane gets it.
+__device__ __forceinline__ float sum_q4(float x)
+{
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 template <int D, int IO>
-__global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
+__global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_bwd_grad_kernel(DeltaParams p)
 {
     constexpr int NP = IO == IO_F16 ? 2 : 1;
     using L = GradLds<D, NP>;
+    using TL = Tile<D>;
     constexpr int NW = D / 16, NT = 64 * NW;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int hv = (int)(blockIdx.x % (unsigned)p.HV);
@@ -365,73 +413,42 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
     const int64_t t0 = rng.b + c * CHUNK;
     const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
     const int hk = hv / (p.HV / p.H);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, q4 = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int t = threadIdx.x, lane = t & 63, q4 = lane >> 4, l16 = lane & 15;
+    auto again = [&]() {
+        lane = fresh(threadIdx.x & 63);
+        t = 64 * wave + lane;
+        q4 = lane >> 4;
+        l16 = lane & 15;
+    };
     const int64_t item = delta_item(p, slot, hv);
     const char *rec = p.rec + item * (int64_t)DeltaRecord::BYTES;
 
-    constexpr int CPT = 64 * D / 8 / NT;  // 2
-    {
-        const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + D) * 2));
-        const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + D) * 2));
-        i32x4 a[CPT], b[CPT];
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (D / 8), cc = ci % (D / 8);
-            a[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
-            b[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
-        }
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int ci = t + NT * i, row = ci / (D / 8), cc = ci % (D / 8);
-            st_parts<NP>(sm + L::K0, L::TILE, row * L::RS + cc * 16, a[i]);
-            st_parts<NP>(sm + L::Q0, L::TILE, row * L::RS + cc * 16, b[i]);
-        }
-    }
     constexpr int VCH = DeltaRecord::NVEC * 16 + 1;
     if (t < VCH) lds_st(sm, L::VEC + 16 * t, *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t));
 
-    const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.dout + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + D) * 2));
-    const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + D) * 2));
-    const f32x4 *s_ck = reinterpret_cast<const f32x4 *>(p.s_ck) + item * (D / 16) * (D / 16 * 64);
-    const f32x4 *ds_ck = reinterpret_cast<const f32x4 *>(p.ds_ck) + item * (D / 16) * (D / 16 * 64);
-    const f32x4 *u_ck = reinterpret_cast<const f32x4 *>(p.u_ck) + item * (D / 16) * 256;
-    const f32x4 *y_ck = reinterpret_cast<const f32x4 *>(p.y_ck) + item * (D / 16) * 256;
+    const int vbytes = (int)(((len - 1) * p.sv + D) * 2);
+    const __amdgpu_buffer_rsrc_t ro = buf_rsrc(p.dout + t0 * p.sv + hv * p.hsv, vbytes);
+    const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, vbytes);
+    // (buffers: one offset register per access, where a flat address takes two)
+    const __amdgpu_buffer_rsrc_t s_ck = buf_rsrc(p.s_ck + item * D * D, 4 * D * D), ds_ck = buf_rsrc(p.ds_ck + item * D * D, 4 * D * D);
+    const __amdgpu_buffer_rsrc_t u_ck = buf_rsrc(p.u_ck + item * 64 * D, 256 * D), y_ck = buf_rsrc(p.y_ck + item * 64 * D, 256 * D);
 
-    // fragments of a block of 32 value columns: 2 (D / 16) 64 of S and dS, 512 of U and dY
-    constexpr int SPT = 2 * (D / 16) * 64 / NT;  // 2
-    constexpr int UPT = 512 / NT;                // 1 (D = 128), 2 (D = 64)
-    f32x4 fs[SPT], fd[SPT], fu[UPT], fy[UPT];
-    i32x4 fo, fv;
-    auto fetch = [&](int vb) {
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            fs[i] = s_ck[vb * 2 * (D / 16) * 64 + t + NT * i];
-            fd[i] = ds_ck[vb * 2 * (D / 16) * 64 + t + NT * i];
-        }
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            fu[i] = u_ck[vb * 512 + t + NT * i];
-            fy[i] = y_ck[vb * 512 + t + NT * i];
-        }
-        if (t < 256) {
-            const uint32_t off = (uint32_t)((t >> 2) * (int)p.sv + vb * 32 + (t & 3) * 8) * 2;
-            fo = buf_ld16<i32x4>(ro, off);
-            fv = buf_ld16<i32x4>(rv, off);
-        }
-    };
-    auto st_frag = [&](int base, int plane, int stride, f32x4 x, int id, int tiles, bool state) {
-        // fragment id -> (16 columns, tile, lane): 4 consecutive rows of one value column
+    // fragment id -> (16 columns, tile, lane): 4 consecutive rows of one value column
+    auto st_frag = [&](int base, int plane, auto tile_of, f32x4 x, int id, int tiles, bool state) {
+        using VT = decltype(tile_of);
         const int ln = id & 63, tile = (id >> 6) % tiles, v = (id >> 6) / tiles * 16 + (ln & 15);
         const int r = state ? state_row(tile, ln >> 4) : 16 * tile + 4 * (ln >> 4);
         bf16x4 h, l;
         split4(x, h, l);
-        lds_st(sm, base + v * stride + 2 * r, h);
-        lds_st(sm, base + plane + v * stride + 2 * r, l);
+        lds_st(sm, base + VT::quad(v, r >> 2), h);
+        lds_st(sm, base + plane + VT::quad(v, r >> 2), l);
     };
 
     f32x4 aq[4], ay[4], au[4];  // dO S^T, dY S^T, U dS^T: rows 16 mt .., key columns 16 wave ..
     constexpr int TPW = (10 + NW - 1) / NW;
-    f32x4 ou[TPW], yu[TPW];     // dO U^T, dY U^T
+    f32x4 ou[TPW], yu[TPW];     // (dO U^T)^T, (dY U^T)^T
+    f32x4 yv = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) aq[i] = ay[i] = au[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -441,42 +458,60 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
         br = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3;
         bc = id - br * (br + 1) / 2;
     };
-    f32x4 yv = {0, 0, 0, 0};
     float dot = 0.0f;  // <S, dS>
-    fetch(0);
     for (int vb = 0; vb < D / 32; ++vb) {
+        again();
+        // fragments of 32 value columns: 2 (D / 16) 64 of S and dS, 512 of U and dY
+        constexpr int SPT = 2 * (D / 16) * 64 / NT;  // 2
+        constexpr int UPT = 512 / NT;                // 1 (D = 128), 2 (D = 64)
+        // (in two batches, which keeps the registers within the bound)
+        {
+            f32x4 fs[SPT], fu[UPT];
+            i32x4 fo = {};
 #pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            st_frag(L::S0, L::SP, L::RS, fs[i], t + NT * i, D / 16, true);
-            st_frag(L::DS0, L::SP, L::RS, fd[i], t + NT * i, D / 16, true);
+            for (int i = 0; i < SPT; ++i) fs[i] = buf_ld16<f32x4>(s_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dot = fmaf(fs[i][e], fd[i][e], dot);
-        }
+            for (int i = 0; i < UPT; ++i) fu[i] = buf_ld16<f32x4>(u_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
+            const uint32_t off = (uint32_t)((t >> 2) * (int)p.sv + vb * 32 + (t & 3) * 8) * 2;
+            if (t < 256) fo = buf_ld16<i32x4>(ro, off);
+            f32x4 fd[SPT];
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            st_frag(L::U0, L::VP, PSTR, fu[i], t + NT * i, 4, false);
-            st_frag(L::Y0, L::VP, PSTR, fy[i], t + NT * i, 4, false);
-        }
-        if (t < 256) {
-            st_parts<NP>(sm + L::O0, L::OT, (t >> 2) * L::OS + (t & 3) * 16, fo);
-            st_parts<NP>(sm + L::VT0, L::OT, (t >> 2) * L::OS + (t & 3) * 16, fv);
+            for (int i = 0; i < SPT; ++i) fd[i] = buf_ld16<f32x4>(ds_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
+            if (vb > 0) __syncthreads();  // the block before is done with
+#pragma unroll
+            for (int i = 0; i < SPT; ++i) st_frag(L::S0, L::SP, ValueTile<D>{}, fs[i], t + NT * i, D / 16, true);
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) st_frag(L::U0, L::VP, ValueTile<64>{}, fu[i], t + NT * i, 4, false);
+            if (t < 256) st_parts<NP>(sm + L::O0, L::OT, token_piece(t >> 2, t & 3), fo);
+#pragma unroll
+            for (int i = 0; i < SPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot = fmaf(fs[i][e], fd[i][e], dot);
+            region();
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) fu[i] = buf_ld16<f32x4>(y_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
+            if (t < 256) fo = buf_ld16<i32x4>(rv, off);
+#pragma unroll
+            for (int i = 0; i < SPT; ++i) st_frag(L::DS0, L::SP, ValueTile<D>{}, fd[i], t + NT * i, D / 16, true);
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) st_frag(L::Y0, L::VP, ValueTile<64>{}, fu[i], t + NT * i, 4, false);
+            if (t < 256) st_parts<NP>(sm + L::VT0, L::OT, token_piece(t >> 2, t & 3), fo);
         }
         __syncthreads();
-        if (vb + 1 < D / 32) fetch(vb + 1);
-        const bf16x8 sh = ld_col_plain(sm + L::S0, L::RS, 0, 16 * wave, q4, l16);
-        const bf16x8 sl = ld_col_plain(sm + L::S0 + L::SP, L::RS, 0, 16 * wave, q4, l16);
-        const bf16x8 dh = ld_col_plain(sm + L::DS0, L::RS, 0, 16 * wave, q4, l16);
-        const bf16x8 dl = ld_col_plain(sm + L::DS0 + L::SP, L::RS, 0, 16 * wave, q4, l16);
-        auto o_row = [&](int part, int mt) { return ld_row_plain(sm + L::O0 + part * L::OT, L::OS, 16 * mt + l16, 0, q4); };
-        auto v_col = [&](int base, int part, int mt) { return ld_col_plain(sm + base + part * L::VP, PSTR, 0, 16 * mt, q4, l16); };
+        again();
+        const bf16x8 sh = ValueTile<D>::col(sm + L::S0, wave, q4, l16), sl = ValueTile<D>::col(sm + L::S0 + L::SP, wave, q4, l16);
+        const bf16x8 dh = ValueTile<D>::col(sm + L::DS0, wave, q4, l16), dl = ValueTile<D>::col(sm + L::DS0 + L::SP, wave, q4, l16);
+        auto o_row = [&](int base, int part, int mt) { return lds_ld<bf16x8>(sm, base + part * L::OT + token_piece(16 * mt + l16, q4)); };
+        auto v_col = [&](int base, int part, int mt) { return ValueTile<64>::col(sm + base + part * L::VP, mt, q4, l16); };
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const bf16x8 o = o_row(0, mt);
+            const bf16x8 o = o_row(L::O0, 0, mt);
             bf16x8 o2 = o;
-            if constexpr (NP == 2) o2 = o_row(1, mt);
+            if constexpr (NP == 2) o2 = o_row(L::O0, 1, mt);
             aq[mt] = mfma_split<NP == 2>(o, o2, sh, sl, aq[mt]);
             ay[mt] = mfma_split<true>(v_col(L::Y0, 0, mt), v_col(L::Y0, 1, mt), sh, sl, ay[mt]);
             au[mt] = mfma_split<true>(v_col(L::U0, 0, mt), v_col(L::U0, 1, mt), dh, dl, au[mt]);
+            if (mt & 1) region();
         }
 #pragma unroll
         for (int i = 0; i < TPW; ++i) {
@@ -484,34 +519,49 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
             if (id < 10) {
                 int br, bc;
                 tri(id, br, bc);
-                const bf16x8 uh = v_col(L::U0, 0, bc), ul = v_col(L::U0, 1, bc), o = o_row(0, br);
-                bf16x8 o2 = o;
-                if constexpr (NP == 2) o2 = o_row(1, br);
-                ou[i] = mfma_split<NP == 2>(o, o2, uh, ul, ou[i]);
-                yu[i] = mfma_split<true>(v_col(L::Y0, 0, br), v_col(L::Y0, 1, br), uh, ul, yu[i]);
+                const bf16x8 uh = v_col(L::U0, 0, bc), ul = v_col(L::U0, 1, bc), o = o_row(L::O0, 0, br);
+                ou[i] = mfma_bf16(uh, o, ou[i]);
+                ou[i] = mfma_bf16(ul, o, ou[i]);
+                if constexpr (NP == 2) ou[i] = mfma_bf16(uh, o_row(L::O0, 1, br), ou[i]);
+                yu[i] = mfma_split<true>(uh, ul, v_col(L::Y0, 0, br), v_col(L::Y0, 1, br), yu[i]);
             }
+            region();
         }
         if (wave < 4) {  // the diagonal of dY V^T, block `wave`
-            const bf16x8 vh = ld_row_plain(sm + L::VT0, L::OS, 16 * wave + l16, 0, q4);
-            const bf16x8 yh = v_col(L::Y0, 0, wave), yl = v_col(L::Y0, 1, wave);
+            const bf16x8 vh = o_row(L::VT0, 0, wave), yh = v_col(L::Y0, 0, wave), yl = v_col(L::Y0, 1, wave);
             yv = mfma_bf16(yh, vh, yv);
             yv = mfma_bf16(yl, vh, yv);
-            if constexpr (NP == 2) yv = mfma_bf16(yh, ld_row_plain(sm + L::VT0 + L::OT, L::OS, 16 * wave + l16, 0, q4), yv);
+            if constexpr (NP == 2) yv = mfma_bf16(yh, o_row(L::VT0, 1, wave), yv);
         }
-        __syncthreads();
     }
+    again();
     if (wave < 4 && l16 >> 2 == q4)  // row 4 q4 + e = column l16
         *reinterpret_cast<float *>(sm + L::YV + 4 * (16 * wave + l16)) = l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0]);
+    {
+        constexpr int CPT = 64 * D / 8 / NT;  // 2
+        const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + D) * 2));
+        const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + D) * 2));
+        i32x4 a[CPT], b[CPT];
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int ci = t + NT * i, row = ci / (D / 8), cc = ci % (D / 8);
+            a[i] = buf_ld16<i32x4>(rk, (uint32_t)(row * (int)p.sk + cc * 8) * 2);
+            b[i] = buf_ld16<i32x4>(rq, (uint32_t)(row * (int)p.sq + cc * 8) * 2);
+        }
+        __syncthreads();  // the last block is done with
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int ci = t + NT * i, row = ci / (D / 8), cc = ci % (D / 8);
+            st_parts<NP>(sm + L::K0, L::TILE, TL::piece(row, cc), a[i]);
+            st_parts<NP>(sm + L::Q0, L::TILE, TL::piece(row, cc), b[i]);
+        }
+    }
+    __syncthreads();
 
-    // score gradients: the same tiles of Q K^T and K K^T, decayed
+    again();
+    // score gradients, rows r = 16 br + l16, columns s = 16 bc + 4 q4 + e: the same tiles of Q K^T and K K^T, decayed
     const float *vec = reinterpret_cast<const float *>(sm + L::VEC);
-    float *E = reinterpret_cast<float *>(sm + L::E0);
-    float *rowsum = reinterpret_cast<float *>(sm + L::ROW);
-    auto st_plane = [&](int base, int row, int col, float x) {
-        const __bf16 h = (__bf16)x, l = (__bf16)(x - (float)h);
-        lds_st(sm, base + row * PSTR + 2 * col, h);
-        lds_st(sm, base + L::PLANE + row * PSTR + 2 * col, l);
-    };
+    auto part = [&](int base, int which, int mt, int j) { return TL::row(sm + base + which * L::TILE, mt, j, q4, l16); };
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
         const int id = wave + NW * i;
@@ -521,39 +571,57 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
             f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                const bf16x8 b = ld_row_plain(sm + L::K0, L::RS, 16 * bc + l16, 32 * j, q4);
-                const bf16x8 ka = ld_row_plain(sm + L::K0, L::RS, 16 * br + l16, 32 * j, q4);
-                const bf16x8 qa = ld_row_plain(sm + L::Q0, L::RS, 16 * br + l16, 32 * j, q4);
-                kk = mfma_bf16(ka, b, kk);
-                qk = mfma_bf16(qa, b, qk);
+                const bf16x8 a = part(L::K0, 0, bc, j), kb = part(L::K0, 0, br, j), qb = part(L::Q0, 0, br, j);
+                kk = mfma_bf16(a, kb, kk);
+                qk = mfma_bf16(a, qb, qk);
                 if constexpr (NP == 2) {
-                    const bf16x8 b2 = ld_row_plain(sm + L::K0 + L::TILE, L::RS, 16 * bc + l16, 32 * j, q4);
-                    kk = mfma_bf16(ka, b2, kk);
-                    qk = mfma_bf16(qa, b2, qk);
-                    kk = mfma_bf16(ld_row_plain(sm + L::K0 + L::TILE, L::RS, 16 * br + l16, 32 * j, q4), b, kk);
-                    qk = mfma_bf16(ld_row_plain(sm + L::Q0 + L::TILE, L::RS, 16 * br + l16, 32 * j, q4), b, qk);
+                    const bf16x8 a2 = part(L::K0, 1, bc, j);
+                    kk = mfma_bf16(a2, kb, kk);
+                    qk = mfma_bf16(a2, qb, qk);
+                    kk = mfma_bf16(a, part(L::K0, 1, br, j), kk);
+                    qk = mfma_bf16(a, part(L::Q0, 1, br, j), qk);
                 }
+                if (j & 1) region();
             }
-            const int s = 16 * bc + l16;
-            const float gsh = vec[DeltaRecord::GH * 64 + s], gsl = vec[DeltaRecord::GL * 64 + s];
-            f32x4 rs;
+            const int r = 16 * br + l16, s0 = 16 * bc + 4 * q4;
+            const float gh = vec[DeltaRecord::GH * 64 + r], gl = vec[DeltaRecord::GL * 64 + r], bt = vec[DeltaRecord::BT * 64 + r];
+            const f32x4 sh = lds_ld<f32x4>(sm, L::VEC + DeltaRecord::GH * 256 + 4 * s0), sl = lds_ld<f32x4>(sm, L::VEC + DeltaRecord::GL * 256 + 4 * s0);
+            f32x4 dp, da, E;
+            float kkr = 0.0f, er = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int r = 16 * br + 4 * q4 + e;
-                const float d = ex2(fminf((vec[DeltaRecord::GH * 64 + r] - gsh) + (vec[DeltaRecord::GL * 64 + r] - gsl), 0.0f));
-                const float dp = s <= r ? p.scale * d * ou[i][e] : 0.0f;
-                const float yd = s < r ? d * yu[i][e] : 0.0f;
-                const float da = -vec[DeltaRecord::BT * 64 + r] * yd;
-                rs[e] = sum16(yd * kk[e]);
-                E[r * L::ES + s] = s < r ? dp * qk[e] + da * kk[e] : 0.0f;
-                st_plane(L::DP0, r, s, dp);
-                if (s <= r) st_plane(L::DA0, r, s, da);  // zero on the diagonal
-                if (s < r) st_plane(L::DA0, s, r, da);
+                const float d = ex2(fminf((gh - sh[e]) + (gl - sl[e]), 0.0f));
+                const bool below = s0 + e < r;
+                const float yd = below ? d * yu[i][e] : 0.0f;
+                dp[e] = s0 + e <= r ? p.scale * d * ou[i][e] : 0.0f;
+                da[e] = -bt * yd;
+                E[e] = below ? dp[e] * qk[e] + da[e] * kk[e] : 0.0f;
+                kkr = fmaf(yd, kk[e], kkr);
+                er += E[e];
             }
-            if (l16 == 0) *reinterpret_cast<f32x4 *>(rowsum + bc * 64 + 16 * br + 4 * q4) = rs;
-            if (br == bc && !(br & 1)) {  // the zero block right of it
+            kkr = sum_q4(kkr);
+            if (q4 == 0) *reinterpret_cast<float *>(sm + L::KKR + 256 * bc + 4 * r) = kkr;
+            if (br == bc) {
+                lds_st(sm, L::ED + (r * L::ES + 4 * q4) * 4, E);
+            } else {
+                er = sum_q4(er);
+                if (q4 == 0) *reinterpret_cast<float *>(sm + L::ROW + 256 * bc + 4 * r) = er;
+                f32x4 ec;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) st_plane(L::DP0, 16 * br + 4 * q4 + e, 16 * (br + 1) + l16, 0.0f);
+                for (int e = 0; e < 4; ++e) ec[e] = sum16(E[e]);
+                if (l16 == 0) lds_st(sm, L::COL + 256 * (br - 1) + 4 * s0, ec);
+            }
+            auto st_plane = [&](int base, int col4, f32x4 x) {
+                bf16x4 h, l;
+                split4(x, h, l);
+                lds_st(sm, base + PlaneTile::quad(r, col4), h);
+                lds_st(sm, base + PlaneTile::BYTES + PlaneTile::quad(r, col4), l);
+            };
+            st_plane(L::DP0, s0 >> 2, dp);
+            st_plane(L::DA0, s0 >> 2, da);
+            if (br == bc && !(br & 1)) {  // the zero block right of it
+                st_plane(L::DP0, (s0 >> 2) + 4, f32x4{0, 0, 0, 0});
+                st_plane(L::DA0, (s0 >> 2) + 4, f32x4{0, 0, 0, 0});
             }
         }
     }
@@ -562,26 +630,43 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
     if (lane == 0) *reinterpret_cast<float *>(sm + L::DOT + 4 * wave) = dot;
     __syncthreads();
 
+    again();
     // dQ and dK of this wave's key columns, and their rows' products with q and k
-    const int kc = 16 * wave + l16;
-    const int64_t w0 = (t0 * p.HV + hv) * D + kc;                     // per value head (float32)
-    const int64_t o0 = (t0 * p.H + hk) * D + kc;
     const bool grouped = p.H != p.HV;
+    __amdgpu_buffer_rsrc_t rdq, rdk;  // per value head in float32, or the gradients themselves
+    if (grouped) {
+        const int64_t o = (t0 * p.HV + hv) * D;
+        const int bytes = (int)(uint32_t)(((int64_t)(len - 1) * p.HV * D + D) * 4);
+        rdq = buf_rsrc(p.dq_ws + o, bytes);
+        rdk = buf_rsrc(p.dk_ws + o, bytes);
+    } else {
+        const int64_t o = (t0 * p.H + hk) * D;
+        const int bytes = ((len - 1) * p.H * D + D) * 2;
+        rdq = buf_rsrc(p.dq + o, bytes);
+        rdk = buf_rsrc(p.dk + o, bytes);
+    }
     float *red = reinterpret_cast<float *>(sm + L::RED) + wave * 192;
+    // right operands: rows 32 j .. of K and Q, the wave's columns
+    bf16x8 kc[NP][2], qc[NP][2];
+#pragma unroll
+    for (int w = 0; w < NP; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            kc[w][j] = cat4(TL::quad(sm + L::K0 + w * L::TILE, 2 * j, wave, q4, l16), TL::quad(sm + L::K0 + w * L::TILE, 2 * j + 1, wave, q4, l16));
+            qc[w][j] = cat4(TL::quad(sm + L::Q0 + w * L::TILE, 2 * j, wave, q4, l16), TL::quad(sm + L::Q0 + w * L::TILE, 2 * j + 1, wave, q4, l16));
+        }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
         auto vec4 = [&](int which) { return lds_ld<f32x4>(sm, L::VEC + which * 256 + (16 * mt + 4 * q4) * 4); };
-        const f32x4 eg = vec4(DeltaRecord::EG), bt = vec4(DeltaRecord::BT);
-        f32x4 dq = aq[mt] * vec4(DeltaRecord::EQ), y = ay[mt] * eg, x = au[mt] * vec4(DeltaRecord::ED);
-        f32x4 si, sy, sx;
+        f32x4 dq = aq[mt] * vec4(DeltaRecord::EQ), y = ay[mt] * vec4(DeltaRecord::EG), x = au[mt] * vec4(DeltaRecord::ED);
+        f32x4 si, sy, sx, dk = x - vec4(DeltaRecord::BT) * y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 16 * mt + 4 * q4 + e;
-            const int o = r * L::RS + 2 * kc;
-            float qv = bf16_bits_to_f32(lds_ld<uint16_t>(sm, L::Q0 + o)), kv = bf16_bits_to_f32(lds_ld<uint16_t>(sm, L::K0 + o));
+            // q and k of row 16 mt + 4 q4 + e, column 16 wave + l16
+            float qv = (float)qc[0][mt / 2][4 * (mt & 1) + e], kv = (float)kc[0][mt / 2][4 * (mt & 1) + e];
             if constexpr (NP == 2) {
-                qv += bf16_bits_to_f32(lds_ld<uint16_t>(sm, L::Q0 + L::TILE + o));
-                kv += bf16_bits_to_f32(lds_ld<uint16_t>(sm, L::K0 + L::TILE + o));
+                qv += (float)qc[NP - 1][mt / 2][4 * (mt & 1) + e];
+                kv += (float)kc[NP - 1][mt / 2][4 * (mt & 1) + e];
             }
             si[e] = sum16(qv * dq[e]);
             sy[e] = sum16(kv * y[e]);
@@ -592,76 +677,112 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
             *reinterpret_cast<f32x4 *>(red + 64 + 16 * mt + 4 * q4) = sy;
             *reinterpret_cast<f32x4 *>(red + 128 + 16 * mt + 4 * q4) = sx;
         }
-        f32x4 dk = x - bt * y;
-        auto part2 = [&](int base, int j, int which) {  // right operand: rows 32 j .. of K or Q, the wave's columns
-            return ld_col(sm + base + which * L::TILE, L::RS, 32 * j, 16 * wave, q4, l16);
+        auto add = [&](bf16x8 ah, bf16x8 al, const bf16x8 (&b)[NP][2], int j, f32x4 acc) {
+            acc = mfma_bf16(ah, b[0][j], acc);
+            acc = mfma_bf16(al, b[0][j], acc);
+            if constexpr (NP == 2) acc = mfma_bf16(ah, b[NP - 1][j], acc);
+            return acc;
         };
+        auto prow = [&](int base, int j) {
+            const int a = base + 64 * 16 * mt;
+            return cat4(lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, q4) + 2048 * j), lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, 4 + q4) + 2048 * j));
+        };
+        auto pcol = [&](int base, int j) { return PlaneTile::col(sm + base, mt, j, q4, l16); };
+        constexpr int PB = PlaneTile::BYTES;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const bf16x8 k0 = part2(L::K0, j, 0), q0 = part2(L::Q0, j, 0);
-            bf16x8 k1 = k0, q1 = q0;
-            if constexpr (NP == 2) {
-                k1 = part2(L::K0, j, 1);
-                q1 = part2(L::Q0, j, 1);
+            if (j <= mt / 2) {
+                dq = add(prow(L::DP0, j), prow(L::DP0 + PB, j), kc, j, dq);
+                dk = add(prow(L::DA0, j), prow(L::DA0 + PB, j), kc, j, dk);
             }
-            auto add = [&](bf16x8 ah, bf16x8 al, bf16x8 bh, bf16x8 bl, f32x4 acc) {
-                acc = mfma_bf16(ah, bh, acc);
-                acc = mfma_bf16(al, bh, acc);
-                if constexpr (NP == 2) acc = mfma_bf16(ah, bl, acc);
-                return acc;
-            };
-            if (j <= mt / 2)
-                dq = add(ld_row(sm + L::DP0, PSTR, 16 * mt + l16, 32 * j, q4),
-                         ld_row(sm + L::DP0 + L::PLANE, PSTR, 16 * mt + l16, 32 * j, q4), k0, k1, dq);
-            if (j >= mt / 2)
-                dk = add(ld_col(sm + L::DP0, PSTR, 32 * j, 16 * mt, q4, l16),
-                         ld_col(sm + L::DP0 + L::PLANE, PSTR, 32 * j, 16 * mt, q4, l16), q0, q1, dk);
-            dk = add(ld_row(sm + L::DA0, PSTR, 16 * mt + l16, 32 * j, q4),
-                     ld_row(sm + L::DA0 + L::PLANE, PSTR, 16 * mt + l16, 32 * j, q4), k0, k1, dk);
+            if (j >= mt / 2) {
+                dk = add(pcol(L::DP0, j), pcol(L::DP0 + PB, j), qc, j, dk);
+                dk = add(pcol(L::DA0, j), pcol(L::DA0 + PB, j), kc, j, dk);
+            }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 16 * mt + 4 * q4 + e;
-            if (r < len) {
-                if (grouped) {
-                    p.dq_ws[w0 + (int64_t)r * p.HV * D] = dq[e];
-                    p.dk_ws[w0 + (int64_t)r * p.HV * D] = dk[e];
-                } else {
-                    p.dq[o0 + (int64_t)r * p.H * D] = f32_io<IO>(dq[e]);
-                    p.dk[o0 + (int64_t)r * p.H * D] = f32_io<IO>(dk[e]);
-                }
+            // (rows past the chunk's end lie past the buffers' range)
+            const uint32_t r = 16 * mt + 4 * q4 + e;
+            if (grouped) {
+                const uint32_t o = 4 * (r * (uint32_t)(p.HV * D) + 16 * wave + l16);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dq[e]), rdq, o, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dk[e]), rdk, o, 0, 0);
+            } else {
+                const uint32_t o = 2 * (r * (uint32_t)(p.H * D) + 16 * wave + l16);
+                __builtin_amdgcn_raw_buffer_store_b16(f32_io<IO>(dq[e]), rdq, o, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b16(f32_io<IO>(dk[e]), rdk, o, 0, 0);
             }
         }
+        region();
     }
     __syncthreads();
     if (wave != 0) return;
 
     // the scalars: lane = token
-    float I = 0.0f, Y = 0.0f, X = 0.0f, sd = 0.0f, rs = 0.0f;
+    float I = 0.0f, Y = 0.0f, X = 0.0f, sd = 0.0f, kkr = 0.0f;
+    auto f32_at = [&](int base, int i) { return lds_ld<float>(sm, base + 4 * i); };
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const float *r = reinterpret_cast<const float *>(sm + L::RED) + w * 192;
-        I += r[lane];
-        Y += r[64 + lane];
-        X += r[128 + lane];
-        sd += lds_ld<float>(sm, L::DOT + 4 * w);
+        I += f32_at(L::RED + w * 768, lane);
+        Y += f32_at(L::RED + w * 768 + 256, lane);
+        X += f32_at(L::RED + w * 768 + 512, lane);
+        sd += f32_at(L::DOT, w);
     }
-    for (int b = 0; b <= lane >> 4; ++b) rs += rowsum[b * 64 + lane];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (b <= q4) kkr += f32_at(L::KKR + 256 * b, lane);
     const float bt = vec[DeltaRecord::BT * 64 + lane];
-    const float dbeta = lds_ld<float>(sm, L::YV + 4 * lane) - Y - rs;
+    const float dbeta = f32_at(L::YV, lane) - Y - kkr;
     I -= bt * Y;
-    // row `lane` of E to sums over the columns before each
+    // sum of E over r >= t > s, t = lane = 16 q4 + l16: whole tiles left of
+    // and below t's block, the rows from t on of the tiles left of the
+    // diagonal, the columns before t of the tiles under it, and the diagonal
+    float rows_left = 0.0f, cols_under = 0.0f, tiles = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+        if (b < q4) rows_left += f32_at(L::ROW + 256 * b, lane);
+        if (b >= q4) cols_under += f32_at(L::COL + 256 * b, lane);
+    }
+    // (row sums of the blocks further down, columns left of t's block)
+    float below[3];
+#pragma unroll
+    for (int br = 1; br < 4; ++br) {
+        float s = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+            if (b < br && b < q4 && br > q4) s += f32_at(L::ROW + 256 * b, 16 * br + l16);
+        below[br - 1] = sum16(s);
+    }
+    tiles = below[0] + below[1] + below[2];
+    // suffix sum of rows_left and exclusive prefix of cols_under within the 16 lanes of the block
+    float suf = rows_left, pre = cols_under;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+        const float a = __shfl_down(suf, d, 16), b = __shfl_up(pre, d, 16);
+        if (l16 + d < 16) suf += a;
+        if (l16 >= d) pre += b;
+    }
+    pre -= cols_under;
+    // the diagonal block: this lane's row summed up to each column, then down the columns
+    f32x4 row[4];
     float run = 0.0f;
-    for (int s = 0; s <= lane; ++s) {
-        const float x = E[lane * L::ES + s];
-        E[lane * L::ES + s] = run;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i] = lds_ld<f32x4>(sm, L::ED + (lane * L::ES + 4 * i) * 4);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float x = row[i / 4][i % 4];
+        row[i / 4][i % 4] = run;
         run += x;
     }
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds_st(sm, L::ED + (lane * L::ES + 4 * i) * 4, row[i]);
     float pairs = 0.0f;
-    for (int r = 0; r < 64; ++r)
-        if (r >= lane) pairs += E[r * L::ES + lane];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const float x = f32_at(L::ED, (16 * q4 + r) * L::ES + l16);
+        if (r >= l16) pairs += x;
+    }
     float Isum = I, Xsum = X;  // suffix sum of I, inclusive prefix of X
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -670,7 +791,7 @@ __global__ __launch_bounds__(4 * D) void delta_bwd_grad_kernel(DeltaParams p)
         if (lane >= d) Xsum += b;
     }
     const float xb = __shfl_up(Xsum, 1);
-    const float dg = pairs + Isum + (lane > 0 ? xb : 0.0f) + vec[DeltaRecord::NVEC * 64] * sd;
+    const float dg = pairs + suf + pre + tiles + Isum + (lane > 0 ? xb : 0.0f) + vec[DeltaRecord::NVEC * 64] * sd;
     if (lane < len) {
         const int64_t o = (t0 + lane) * p.HV + hv;
         p.dbeta[o] = f32_io<IO>(dbeta);

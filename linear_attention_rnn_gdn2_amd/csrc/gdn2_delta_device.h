@@ -117,6 +117,12 @@ struct Tile {
     {
         return lds_ld<bf16x8>(tile, l16 * RS + (((4 * j + q4) ^ swz(l16)) << 4) + 16 * RS * mt);
     }
+    // 4 rows 16 mt + 4 q4 .. of column 16 w + l16
+    __device__ static __forceinline__ bf16x4 quad(const char *tile, int mt, int w, int q4, int l16)
+    {
+        const int r = 4 * q4 + (l16 >> 2);
+        return lds_tr(tile, r * RS + (((2 * w + (l16 >> 1 & 1)) ^ swz(r)) << 4) + 8 * (l16 & 1) + 16 * RS * mt);
+    }
     // transposed: element (m, k) = tile[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns those of state tile i
     __device__ static __forceinline__ bf16x8 col(const char *tile, int i, int j, int q4, int l16)
     {

@@ -279,9 +279,6 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
 // registers, tiles a chunk ahead in the other half of LDS) and store the
 // outputs of the chunk before. One barrier per chunk; the computing waves
 // touch no global memory but for the states.
-#ifndef MAX64
-#define MAX64 0
-#endif
 constexpr int LW = 4;  // staging waves
 
 template <int K, int COLS, bool CKPT>
@@ -402,10 +399,6 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         return;
     }
 
-    // The computing waves that share a SIMD start every chunk together; with
-    // one ahead of the other, its matrix products run beside the other's
-    // vector work instead of both waiting for the same unit.
-    if (wave >= 4) __builtin_amdgcn_s_setprio(1);
     const int q4 = lane >> 4, l16 = lane & 15;
     const int col = (vb * NC + wave) * 16 + l16;
     const int64_t shead = ((int64_t)n * p.HV + hv) * K * p.V;
@@ -631,8 +624,8 @@ void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
 template <int K, int IO>
 void launch_state_cols(const DeltaParams &p, bool ckpt, int cols, hipStream_t stream)
 {
-    if (cols == 128 && !MAX64) launch_state_ck<K, IO, 8>(p, ckpt, stream);
-    else if (cols >= 64) launch_state_ck<K, IO, 4>(p, ckpt, stream);
+    if (cols == 128) launch_state_ck<K, IO, 8>(p, ckpt, stream);
+    else if (cols == 64) launch_state_ck<K, IO, 4>(p, ckpt, stream);
     else launch_state_ck<K, IO, 2>(p, ckpt, stream);
 }
 
