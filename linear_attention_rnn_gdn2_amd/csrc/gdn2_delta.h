@@ -34,8 +34,9 @@ struct DeltaParams {
     int32_t state_vmajor;
     int32_t qk_l2norm;
     int32_t nslots;         // slot_count(T, N)
-    // workspace (chunked calls): every chunk's record, DeltaRecord::bytes per (slot, value head)
+    // workspace (chunked calls): every chunk's record, DeltaRecord::BYTES per (slot, value head)
     char *rec;
+    int32_t low_p;          // the record's low plane of P is used
     // backward only. The checkpoints are in accumulator order: per (slot,
     // value head, 16 value columns) the float32 fragments f32x4[tile][lane]
     // of a wave: lane 16 q4 + l16 holds four rows of column l16, key rows
@@ -52,23 +53,27 @@ struct DeltaParams {
     float *dq_ws, *dk_ws;   // [T, HV, K] per value head (grouped heads only)
 };
 
-// One chunk's record, K-independent: the lower triangles of T and P as bf16
-// planes (high and low part: T = Th + Tl to 2^-18), then float32 vectors over
-// the chunk's 64 tokens. A plane is a sequence of left-operand fragments of
-// 1 KiB, one per 16 rows and 32 columns on or below the diagonal (the upper
-// block of a pair on the diagonal is zero): lane 16 q4 + l16 holds row l16,
-// columns 4 q4 .. + 3 and 16 + 4 q4 .. + 3 in 16 bytes.
+// One chunk's record, K-independent: the lower triangles of T and P as fp16
+// planes (high and low part: 22 significant bits next to the largest value,
+// scaled for that by a power of two of the chunk's own), then float32 vectors
+// over the chunk's 64 tokens. A plane is a sequence of left-operand fragments
+// of 1 KiB, one per 16 rows and 32 columns on or below the diagonal (the
+// upper block of a pair on the diagonal is zero): lane 16 q4 + l16 holds row
+// l16, columns 4 q4 .. + 3 and 16 + 4 q4 .. + 3 in 16 bytes.
 struct DeltaRecord {
     // fragment of rows 16 mt .., columns 32 j .. (j <= mt / 2)
     __host__ __device__ static constexpr int frag(int mt, int j) { return (mt < 2 ? mt : 2 * mt - 2 + j) * 1024; }
     static constexpr int PLANE = 6 * 1024;  // bytes
     static constexpr int TH = 0, TL = PLANE, PH = 2 * PLANE, PL = 3 * PLANE;
     static constexpr int VEC = 4 * PLANE;
-    // vectors: e^G rk, scale e^G rq, e^(G_C - G) rk, beta, G log2(e) in two parts
-    // (rk, rq: the reciprocal norms with in-kernel normalisation, else 1)
-    enum { EG = 0, EQ = 1, ED = 2, BT = 3, GH = 4, GL = 5, NVEC = 6 };
-    static constexpr int GAMMA = VEC + NVEC * 256;  // e^(G_C), one float
-    static constexpr int BYTES = GAMMA + 256;
+    // vectors: e^G rk / ck, scale e^G rq / cq, e^(G_C - G) rk / ck, beta (rk,
+    // rq: the reciprocal norms with in-kernel normalisation, else 1; ck, cq:
+    // the powers of two that bring a bf16 row of k or q into fp16's range)
+    enum { EG = 0, EQ = 1, ED = 2, BT = 3 };
+    static constexpr int SCAL = VEC + 4 * 256;  // e^(G_C), and what T and P are multiplied by to undo their scales
+    static constexpr int VEC2 = SCAL + 256;
+    enum { GH = 0, GL = 1, CK = 2, CQ = 3 };    // G log2(e) in two parts, ck, cq
+    static constexpr int BYTES = VEC2 + 4 * 256;
 };
 
 // Arguments of the q/k preparation (forward and backward).

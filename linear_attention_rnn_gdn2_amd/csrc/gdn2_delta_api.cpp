@@ -179,6 +179,7 @@ int validate(const DeltaFwd &a, bool chunked, void *ws, int64_t ws_bytes, DeltaP
     p->qk_l2norm = o.l2norm;
     p->nslots = (int32_t)gdn2::slot_count(T, N);
     p->rec = static_cast<char *>(ws);
+    p->low_p = p->io == gdn2::IO_F16;
     return GDN2_OK;
 }
 
@@ -292,6 +293,7 @@ int validate(const DeltaBwd &a, void *ws, int64_t ws_bytes, DeltaParams *p)
     p->dbeta = static_cast<uint16_t *>(a.dbeta->data);
     char *b = static_cast<char *>(ws);
     p->rec = b + w.rec;
+    p->low_p = 1;
     p->s_ck = reinterpret_cast<float *>(b + w.s);
     p->ds_ck = reinterpret_cast<float *>(b + w.ds);
     p->u_ck = reinterpret_cast<float *>(b + w.u);

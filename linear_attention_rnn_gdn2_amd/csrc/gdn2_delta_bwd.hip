@@ -50,10 +50,10 @@ struct PlaneTile {
         return c / 8 * 2048 + r * 64 + (((c % 8 >> 1) ^ swz(r)) << 4) + 8 * (c & 1);
     }
     // transposed: element (m, k) = plane[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns m = 16 i + l16, i <= 2 j + 1
-    __device__ static __forceinline__ bf16x8 col(const char *plane, int i, int j, int q4, int l16)
+    __device__ static __forceinline__ i32x4 col(const char *plane, int i, int j, int q4, int l16)
     {
         const int a = quad(4 * q4 + (l16 >> 2), 4 * (i & 1) + (l16 & 3)) + i / 2 * 2048 + 32 * 64 * j;
-        return cat4(lds_tr(plane, a), lds_tr(plane, a + 16 * 64));
+        return __builtin_bit_cast(i32x4, cat4(lds_tr(plane, a), lds_tr(plane, a + 16 * 64)));
     }
 };
 
@@ -65,7 +65,7 @@ struct BwdStateLds {
     static constexpr int O0 = 2 * TILE;
     static constexpr int R0 = O0 + 64 * OS;   // planes of T and P
     static constexpr int G0 = R0 + 4 * PlaneTile::BYTES;
-    static constexpr int VCH = (DeltaRecord::GAMMA + 16 - DeltaRecord::VEC) / 16;
+    static constexpr int VCH = (DeltaRecord::SCAL + 16 - DeltaRecord::VEC) / 16;
     static constexpr int HALF = (G0 + 16 * VCH + 511) / 512 * 512;
     static constexpr int SIZE = 2 * HALF;
 };
@@ -97,6 +97,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         constexpr int RPT = 4 * DeltaRecord::PLANE / 16 / TH;  // 6
         static_assert(L::VCH <= TH && 4 * DeltaRecord::PLANE == 16 * RPT * TH, "pieces per thread");
         i32x4 fk[CPT], fq[CPT], fo[OPT], fr[RPT], fv;
+        float ck[CPT], cq[CPT];  // the rows' powers of two
         auto fetch = [&](int64_t c) {
             const int64_t t0 = rng.b + c * CHUNK;
             const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
@@ -116,6 +117,14 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
                     fo[i] = buf_ld16<i32x4>(ro, (uint32_t)(row * (int)p.sv + vb * COLS + cc * 8) * 2);
             }
             const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
+            if constexpr (IO == IO_BF16) {
+                const float *v2 = reinterpret_cast<const float *>(rec + DeltaRecord::VEC2);
+#pragma unroll
+                for (int i = 0; i < CPT; ++i) {
+                    ck[i] = v2[DeltaRecord::CK * 64 + (t + TH * i) / (K / 8)];
+                    cq[i] = v2[DeltaRecord::CQ * 64 + (t + TH * i) / (K / 8)];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < RPT; ++i) fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * (t + TH * i));
             if (t < L::VCH) fv = *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t);
@@ -124,8 +133,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
                 const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
-                lds_st(half, L::K0 + TL::piece(row, cc), fk[i]);
-                lds_st(half, L::Q0 + TL::piece(row, cc), fq[i]);
+                lds_st(half, L::K0 + TL::piece(row, cc), row_f16<IO>(fk[i], ck[i]));
+                lds_st(half, L::Q0 + TL::piece(row, cc), row_f16<IO>(fq[i], cq[i]));
             }
 #pragma unroll
             for (int i = 0; i < OPT; ++i) {
@@ -181,7 +190,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dS[i][e] = p.dht ? p.dht[shead + (int64_t)(state_row(i, q4) + e) * p.V + col] : 0.0f;
-    RightOp<IO, KS> So;
+    RightOp<KS> So;
     So.set(dS);
     __syncthreads();
     for (int64_t c = nch - 1; c >= 0; --c) {
@@ -193,7 +202,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) x[mt] = lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4);
         };
-        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
+        const f32x4 scal = lds_ld<f32x4>(half, L::G0 + DeltaRecord::SCAL - DeltaRecord::VEC);  // e^(G_C), 1 / scales of T and P
+        const float gamma = scal[0];
         {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.ds_ck) + frag * (KT * 64) + lane;
 #pragma unroll
@@ -201,8 +211,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         }
         constexpr f32x4 zero = {0, 0, 0, 0};
         // dU = e^(G_C - G) (K dS) + P^T dO
-        f32x4 U[4] = {zero, zero, zero, zero}, x4[4];
-        bf16x8 a[4], b[4], Uh[2], Ul[2];
+        f32x4 U[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero}, x4[4], dO[4];
+        i32x4 a[4], b[4];
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
 #pragma unroll
@@ -212,25 +222,13 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) U[mt] = So.mul1(a[mt], j, part, U[mt]);
         }
-        vec(DeltaRecord::ED, x4);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) U[mt] = So.scaled(U[mt]) * x4[mt];
-        bf16x4 raw[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-            raw[mt] = lds_tr(half, L::O0 + (16 * mt + 4 * q4 + (l16 >> 2)) * L::OS + 2 * (16 * wave + 4 * (l16 & 3)));
-        f32x4 dO[4];
-        bf16x8 Oh[2], Ol[2];
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) dO[mt] = io4_f32<IO>(raw[mt]);
-        if constexpr (IO == IO_F16) {
-            split_rows(dO, Oh, Ol);
-        } else {
-            Oh[0] = cat4(raw[0], raw[1]);
-            Oh[1] = cat4(raw[2], raw[3]);
-        }
-        // y += (plane pair)^T (h + l); two: l is there
-        auto upper = [&](const char *plane, const bf16x8 (&h)[2], const bf16x8 (&l)[2], auto two, f32x4 (&y)[4]) {
+            dO[mt] = io4_f32<IO>(lds_tr(half, L::O0 + (16 * mt + 4 * q4 + (l16 >> 2)) * L::OS + 2 * (16 * wave + 4 * (l16 & 3))));
+        RightOp<2, 1> Oo;  // (16-bit values: one part is all of them)
+        Oo.set(dO);
+        // y += (plane pair)^T op
+        auto upper = [&](const char *plane, const auto &op, int parts, f32x4 (&y)[4]) {
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
                 const int top = jj ? 4 : 2;
@@ -240,21 +238,33 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
                     b[mt] = PlaneTile::col(plane + PlaneTile::BYTES, mt, jj, q4, l16);
                 }
 #pragma unroll
-                for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(a[mt], h[jj], y[mt]);
+                for (int mt = 0; mt < top; ++mt) y[mt] = op.mul1(a[mt], jj, 0, y[mt]);
 #pragma unroll
-                for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(b[mt], h[jj], y[mt]);
-                if constexpr (decltype(two)::value)
+                for (int mt = 0; mt < top; ++mt) y[mt] = op.mul1(b[mt], jj, 0, y[mt]);
+                if (parts == 2)
 #pragma unroll
-                    for (int mt = 0; mt < top; ++mt) y[mt] = mfma_bf16(a[mt], l[jj], y[mt]);
+                    for (int mt = 0; mt < top; ++mt) y[mt] = op.mul1(a[mt], jj, 1, y[mt]);
             }
         };
-        upper(PH, Oh, Ol, std::integral_constant<bool, IO == IO_F16>{}, U);
-        split_rows(U, Uh, Ul);
+        upper(PH, Oo, 1, Y);
+        vec(DeltaRecord::ED, x4);
+        const float pinv = Oo.inv * scal[2];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            U[mt] = U[mt] * (x4[mt] * So.inv) + Y[mt] * pinv;
+            Y[mt] = zero;
+        }
         // dY = T^T dU
-        f32x4 Y[4] = {zero, zero, zero, zero};
-        upper(TH, Uh, Ul, std::true_type{}, Y);
+        {
+            RightOp<2> Uo;
+            Uo.set(U);
+            upper(TH, Uo, 2, Y);
+            const float tinv = Uo.inv * scal[1];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) Y[mt] *= tinv;
+        }
         // dV = beta dY; the right operands e^G dV (negated) and scale e^G dO
-        RightOp<IO, 2> E, F;
+        RightOp<2> E, F;
         {
             f32x4 dv[4];
             vec(DeltaRecord::BT, x4);
@@ -275,12 +285,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         }
 #pragma unroll
         for (int i0 = 0; i0 < KT; i0 += 4) {
-            f32x4 s[4], w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[i] = IO == IO_F16 ? zero : dS[i0 + i] * gamma;
-                w[i] = zero;
-            }
+            f32x4 s[4] = {zero, zero, zero, zero}, w[4] = {zero, zero, zero, zero};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -293,15 +298,11 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[i] = E.mul1(a[i], j, part, s[i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (IO == IO_F16) w[i] = F.mul1(b[i], j, part, w[i]);
-                        else s[i] = F.mul1(b[i], j, part, s[i]);
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = F.mul1(b[i], j, part, w[i]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dS[i0 + i] = IO == IO_F16 ? dS[i0 + i] * gamma + s[i] * E.inv + w[i] * F.inv : s[i];
+            for (int i = 0; i < 4; ++i) dS[i0 + i] = dS[i0 + i] * gamma + s[i] * E.inv + w[i] * F.inv;
         }
         So.set(dS);
         __syncthreads();
@@ -367,7 +368,7 @@ struct GradLds {
     // vectors, and sums to join over waves and tiles
     static constexpr int NWV = D / 16;
     static constexpr int VEC = WEND > XEND ? WEND : XEND;
-    static constexpr int RED = VEC + DeltaRecord::NVEC * 256 + 16;  // [wave][3][64]
+    static constexpr int RED = VEC + DeltaRecord::BYTES - DeltaRecord::VEC;  // [wave][3][64]
     static constexpr int ES = 20;                                   // floats per row of a diagonal block of E
     static constexpr int ED = RED + NWV * 3 * 256;                  // the four diagonal blocks: [64][ES]
     static constexpr int ROW = ED + 64 * ES * 4;                    // row sums of the tiles of E, by block column: [3][64]
@@ -424,7 +425,8 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
     const int64_t item = delta_item(p, slot, hv);
     const char *rec = p.rec + item * (int64_t)DeltaRecord::BYTES;
 
-    constexpr int VCH = DeltaRecord::NVEC * 16 + 1;
+    constexpr int VCH = (DeltaRecord::BYTES - DeltaRecord::VEC) / 16;
+    static_assert(VCH <= NT, "one piece per thread");
     if (t < VCH) lds_st(sm, L::VEC + 16 * t, *reinterpret_cast<const i32x4 *>(rec + DeltaRecord::VEC + 16 * t));
 
     const int vbytes = (int)(((len - 1) * p.sv + D) * 2);
@@ -560,8 +562,8 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
 
     again();
     // score gradients, rows r = 16 br + l16, columns s = 16 bc + 4 q4 + e: the same tiles of Q K^T and K K^T, decayed
-    const float *vec = reinterpret_cast<const float *>(sm + L::VEC);
-    auto part = [&](int base, int which, int mt, int j) { return TL::row(sm + base + which * L::TILE, mt, j, q4, l16); };
+    const float *vec = reinterpret_cast<const float *>(sm + L::VEC), *vec2 = vec + (DeltaRecord::VEC2 - DeltaRecord::VEC) / 4;
+    auto part = [&](int base, int which, int mt, int j) { return __builtin_bit_cast(bf16x8, TL::row(sm + base + which * L::TILE, mt, j, q4, l16)); };
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
         const int id = wave + NW * i;
@@ -584,8 +586,8 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
                 if (j & 1) region();
             }
             const int r = 16 * br + l16, s0 = 16 * bc + 4 * q4;
-            const float gh = vec[DeltaRecord::GH * 64 + r], gl = vec[DeltaRecord::GL * 64 + r], bt = vec[DeltaRecord::BT * 64 + r];
-            const f32x4 sh = lds_ld<f32x4>(sm, L::VEC + DeltaRecord::GH * 256 + 4 * s0), sl = lds_ld<f32x4>(sm, L::VEC + DeltaRecord::GL * 256 + 4 * s0);
+            const float gh = vec2[DeltaRecord::GH * 64 + r], gl = vec2[DeltaRecord::GL * 64 + r], bt = vec[DeltaRecord::BT * 64 + r];
+            const f32x4 sh = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GH * 64 + s0), sl = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GL * 64 + s0);
             f32x4 dp, da, E;
             float kkr = 0.0f, er = 0.0f;
 #pragma unroll
@@ -658,7 +660,11 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
         auto vec4 = [&](int which) { return lds_ld<f32x4>(sm, L::VEC + which * 256 + (16 * mt + 4 * q4) * 4); };
-        f32x4 dq = aq[mt] * vec4(DeltaRecord::EQ), y = ay[mt] * vec4(DeltaRecord::EG), x = au[mt] * vec4(DeltaRecord::ED);
+        auto pow2 = [&](int which) { return *reinterpret_cast<const f32x4 *>(vec2 + which * 64 + 16 * mt + 4 * q4); };
+        // (the vectors without the powers of two: the rows here are as they came)
+        const f32x4 ck = pow2(DeltaRecord::CK);
+        f32x4 dq = aq[mt] * (vec4(DeltaRecord::EQ) * pow2(DeltaRecord::CQ)), y = ay[mt] * (vec4(DeltaRecord::EG) * ck);
+        f32x4 x = au[mt] * (vec4(DeltaRecord::ED) * ck);
         f32x4 si, sy, sx, dk = x - vec4(DeltaRecord::BT) * y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -687,7 +693,7 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
             const int a = base + 64 * 16 * mt;
             return cat4(lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, q4) + 2048 * j), lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, 4 + q4) + 2048 * j));
         };
-        auto pcol = [&](int base, int j) { return PlaneTile::col(sm + base, mt, j, q4, l16); };
+        auto pcol = [&](int base, int j) { return __builtin_bit_cast(bf16x8, PlaneTile::col(sm + base, mt, j, q4, l16)); };
         constexpr int PB = PlaneTile::BYTES;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -791,7 +797,7 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
         if (lane >= d) Xsum += b;
     }
     const float xb = __shfl_up(Xsum, 1);
-    const float dg = pairs + suf + pre + tiles + Isum + (lane > 0 ? xb : 0.0f) + vec[DeltaRecord::NVEC * 64] * sd;
+    const float dg = pairs + suf + pre + tiles + Isum + (lane > 0 ? xb : 0.0f) + vec[(DeltaRecord::SCAL - DeltaRecord::VEC) / 4] * sd;
     if (lane < len) {
         const int64_t o = (t0 + lane) * p.HV + hv;
         p.dbeta[o] = f32_io<IO>(dbeta);

@@ -1,12 +1,16 @@
 // Device helpers of the scalar-gated delta rule's kernels: two-part bf16
 // operands, staged tiles and MFMA fragments. Not part of the ABI.
 //
-// Precision. Every product of the rule runs on bf16 MFMA with float32
-// accumulation, and a float32 operand is taken as two bf16 parts, x = h + l
-// with h = bf16(x), l = bf16(x - h): 16 significant bits, 2^-18 relative.
-// Products of two such operands drop l l (2^-18 of the product). bf16 inputs
-// are one part, fp16 inputs are exactly two. The state, the chunk's WY
-// solution and all sums are float32.
+// Precision. The sequential passes run on fp16 MFMA with float32 accumulation
+// and take a float32 operand as two fp16 parts, x = h + l, after a power of
+// two has brought the largest value of its column (or chunk) near 2^14: 21
+// significant bits next to that value, 2^-38 of it at the bottom. Products of
+// two such operands drop l l. Rows of q and k that are fp16 values are used
+// as they are; bf16 rows are brought into fp16's range by a power of two per
+// row (exactly, but for values under 2^-38 of the row's largest). The gradient
+// pass uses two bf16 parts (16 bits, no scales), bf16 inputs as one part and
+// fp16 inputs exactly as two. The state, the chunk's WY solution and all sums
+// are float32.
 //
 // Fragments (lane = 16 q4 + l16). A 16x16 accumulator tile holds rows
 // 4 q4 + e (e = 0..3) of column l16. As the right operand of the next product
@@ -113,9 +117,9 @@ struct Tile {
     // byte offset of 16-byte piece c of row r
     __device__ static __forceinline__ int piece(int r, int c) { return r * RS + ((c ^ swz(r)) << 4); }
     // rows 16 mt + l16, columns 32 j + 8 q4 ..
-    __device__ static __forceinline__ bf16x8 row(const char *tile, int mt, int j, int q4, int l16)
+    __device__ static __forceinline__ i32x4 row(const char *tile, int mt, int j, int q4, int l16)
     {
-        return lds_ld<bf16x8>(tile, l16 * RS + (((4 * j + q4) ^ swz(l16)) << 4) + 16 * RS * mt);
+        return lds_ld<i32x4>(tile, l16 * RS + (((4 * j + q4) ^ swz(l16)) << 4) + 16 * RS * mt);
     }
     // 4 rows 16 mt + 4 q4 .. of column 16 w + l16
     __device__ static __forceinline__ bf16x4 quad(const char *tile, int mt, int w, int q4, int l16)
@@ -124,11 +128,11 @@ struct Tile {
         return lds_tr(tile, r * RS + (((2 * w + (l16 >> 1 & 1)) ^ swz(r)) << 4) + 8 * (l16 & 1) + 16 * RS * mt);
     }
     // transposed: element (m, k) = tile[k][m], rows k = 32 j + 4 q4 .. and 32 j + 16 + 4 q4 .., columns those of state tile i
-    __device__ static __forceinline__ bf16x8 col(const char *tile, int i, int j, int q4, int l16)
+    __device__ static __forceinline__ i32x4 col(const char *tile, int i, int j, int q4, int l16)
     {
         const int r = 4 * q4 + (l16 >> 2);
         const int a = r * RS + (((4 * (i >> 1) + (l16 & 3)) ^ swz(r)) << 4) + 8 * (i & 1) + 32 * RS * j;
-        return cat4(lds_tr(tile, a), lds_tr(tile, a + 16 * RS));
+        return __builtin_bit_cast(i32x4, cat4(lds_tr(tile, a), lds_tr(tile, a + 16 * RS)));
     }
 };
 
@@ -157,74 +161,110 @@ __device__ __forceinline__ void st_parts(char *base, int plane_bytes, int off, i
 }
 
 // A record's fragment as a left operand.
-__device__ __forceinline__ bf16x8 ld_frag(const char *plane, int mt, int j, int lane)
+__device__ __forceinline__ i32x4 ld_frag(const char *plane, int mt, int j, int lane)
 {
-    return *reinterpret_cast<const bf16x8 *>(plane + DeltaRecord::frag(mt, j) + 16 * lane);
+    return *reinterpret_cast<const i32x4 *>(plane + DeltaRecord::frag(mt, j) + 16 * lane);
 }
 
 __device__ __forceinline__ int64_t delta_item(const DeltaParams &p, int64_t slot, int hv) { return slot * p.HV + hv; }
 
-// A float32 right operand of N 32-row steps in two parts of the io type, for
-// products with q or k (step j: tiles 2 j and 2 j + 1). bf16: as everywhere. fp16: the inputs are fp16
-// values as they stand, so the operand is taken in fp16 too, scaled per column
-// by a power of two that brings its largest value near 2^14: 22 significant
-// bits next to that value, and no value of the state out of fp16's range.
-template <int IO, int N>
+__device__ __forceinline__ f32x4 mfma_f16(i32x4 a, i32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// The exponent of the power of two that brings m near 2^14 (2^13 <= m 2^e <
+// 2^14; zero, infinity and NaN count as values near 1).
+__device__ __forceinline__ int scale_exp(float m)
+{
+    const int e = 14 - __builtin_amdgcn_frexp_expf(m);
+    return e > 120 ? 120 : e;
+}
+
+// y0, y1 in fp16, packed, and what is left of them. (Rounded towards zero:
+// one instruction for the pair, and the low part takes up what is lost.)
+__device__ __forceinline__ uint32_t pack_f16(float y0, float y1)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(y0, y1));
+}
+__device__ __forceinline__ void split2_f16(float y0, float y1, uint32_t &h, uint32_t &l)
+{
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    h = pack_f16(y0, y1);
+    const f16x2 f = __builtin_bit_cast(f16x2, h);
+    l = pack_f16(fmaf((float)f[0], -1.0f, y0), fmaf((float)f[1], -1.0f, y1));
+}
+// Two tiles of a column as an operand: parts of x0 and x1 times sc.
+__device__ __forceinline__ void split8_f16(f32x4 x0, f32x4 x1, float sc, i32x4 &h, i32x4 &l)
+{
+    uint32_t a[4], b[4];
+    x0 *= sc;
+    x1 *= sc;
+    split2_f16(x0[0], x0[1], a[0], b[0]);
+    split2_f16(x0[2], x0[3], a[1], b[1]);
+    split2_f16(x1[0], x1[1], a[2], b[2]);
+    split2_f16(x1[2], x1[3], a[3], b[3]);
+    h = i32x4{(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
+    l = i32x4{(int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// The largest magnitude of 4 M values per lane over the lane's column (the
+// four lanes of equal l16).
+template <int M>
+__device__ __forceinline__ float col_max(const f32x4 (&x)[M])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) m = fmaxf(m, fmaxf(fabsf(x[i][e]), fabsf(x[i][e + 1])));
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// A float32 right operand of N 32-row steps (step j: tiles 2 j and 2 j + 1) in
+// PARTS fp16 parts, scaled per column.
+template <int N, int PARTS = 2>
 struct RightOp {
-    i32x4 h[N], l[N];
-    float inv = 1.0f;  // what a product is multiplied by
+    i32x4 h[N], l[PARTS == 2 ? N : 1];
+    float inv;  // what a product is multiplied by
 
     __device__ __forceinline__ void set(const f32x4 (&x)[2 * N])
     {
-        if constexpr (IO == IO_F16) {
-            float m = 0.0f;
+        const int ex = scale_exp(col_max(x));
+        const float sc = ldexpf(1.0f, ex);
+        inv = ldexpf(1.0f, -ex);
 #pragma unroll
-            for (int i = 0; i < 2 * N; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[i][e]));
-            const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-            m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-            const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-            m = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-            int ex = 14 - __builtin_amdgcn_frexp_expf(m);
-            ex = ex > 120 ? 120 : ex;  // (an exponent of zero, infinity or NaN is 0)
-            const float sc = ldexpf(1.0f, ex);
-            inv = ldexpf(1.0f, -ex);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < N; ++j) {
+            if constexpr (PARTS == 2) {
+                split8_f16(x[2 * j], x[2 * j + 1], sc, h[j], l[j]);
+            } else {
                 const f32x4 y0 = x[2 * j] * sc, y1 = x[2 * j + 1] * sc;
-                const f16x4 h0 = __builtin_convertvector(y0, f16x4), h1 = __builtin_convertvector(y1, f16x4);
-                const f16x4 l0 = __builtin_convertvector(y0 - __builtin_convertvector(h0, f32x4), f16x4);
-                const f16x4 l1 = __builtin_convertvector(y1 - __builtin_convertvector(h1, f32x4), f16x4);
-                h[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
-                l[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                bf16x4 h0, l0, h1, l1;
-                split4(x[2 * j], h0, l0);
-                split4(x[2 * j + 1], h1, l1);
-                h[j] = __builtin_bit_cast(i32x4, cat4(h0, h1));
-                l[j] = __builtin_bit_cast(i32x4, cat4(l0, l1));
+                const f16x4 a = __builtin_convertvector(y0, f16x4), b = __builtin_convertvector(y1, f16x4);  // to nearest
+                h[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
             }
         }
     }
-    // acc + a times the high (part 0) or low part of step j, a left operand of the io type
-    __device__ __forceinline__ f32x4 mul1(bf16x8 a, int j, int part, f32x4 acc) const
+    // acc + a times the high (part 0) or low part of step j
+    __device__ __forceinline__ f32x4 mul1(i32x4 a, int j, int part, f32x4 acc) const
     {
-        const i32x4 b = part ? l[j] : h[j];
-        if constexpr (IO == IO_F16)
-            return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
-        else return mfma_bf16(a, __builtin_bit_cast(bf16x8, b), acc);
-    }
-    // a sum of such products in the operand's own scale
-    __device__ __forceinline__ f32x4 scaled(f32x4 acc) const
-    {
-        if constexpr (IO == IO_F16) return acc * inv;
-        else return acc;
+        return mfma_f16(a, PARTS == 2 && part ? l[j] : h[j], acc);
     }
 };
+
+// 16 bytes of a row of q or k as fp16: as they are, or bf16 times the row's power of two.
+template <int IO>
+__device__ __forceinline__ i32x4 row_f16(i32x4 raw, float c)
+{
+    if constexpr (IO == IO_F16) return raw;
+    i32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = (int)pack_f16(__uint_as_float((uint32_t)raw[i] << 16) * c, __uint_as_float((uint32_t)raw[i] & 0xffff0000u) * c);
+    return y;
+}
 
 // Four 16-bit io values as float32.
 template <int IO>
@@ -232,19 +272,6 @@ __device__ __forceinline__ f32x4 io4_f32(bf16x4 x)
 {
     if constexpr (IO == IO_F16) return __builtin_convertvector(__builtin_bit_cast(f16x4, x), f32x4);
     else return __builtin_convertvector(x, f32x4);
-}
-
-// 64 tokens of a right operand in two bf16 parts (steps of tiles 0, 1 and 2, 3).
-__device__ __forceinline__ void split_rows(const f32x4 (&x)[4], bf16x8 (&h)[2], bf16x8 (&l)[2])
-{
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        bf16x4 h0, l0, h1, l1;
-        split4(x[2 * j], h0, l0);
-        split4(x[2 * j + 1], h1, l1);
-        h[j] = cat4(h0, h1);
-        l[j] = cat4(l0, l1);
-    }
 }
 
 // Four rows (4 q4 ..) of a wave's 16 columns, rounded to the io type, into a

@@ -53,7 +53,7 @@ struct WyLds {
     static constexpr int T0 = A0 + 64 * AS * 4;
     static constexpr int TEND = T0 + 64 * TS * 4;
     static constexpr int V0 = 2 * TILE > TEND ? 2 * TILE : TEND;
-    static constexpr int SIZE = V0 + 5 * 256;
+    static constexpr int SIZE = V0 + 8 * 256;  // G in two parts, beta, rk, rq, ck, cq; the waves' maxima
 };
 
 template <int K, int IO, bool L2N>
@@ -89,9 +89,29 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
             const int ci = t + 256 * i, row = ci / (K / 8), col = ci % (K / 8);
             lds_st(sm, L::K0 + row * L::RS + col * 16, a[i]);
             lds_st(sm, L::Q0 + row * L::RS + col * 16, b[i]);
+            if constexpr (IO == IO_BF16) {
+                // the powers of two for the sequential passes' fp16 rows, from the largest magnitude
+                // (as integers: bf16 magnitudes order like their bits)
+                auto row_max = [](i32x4 x) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = (uint32_t)x[e] & 0x7fffu, hi = (uint32_t)x[e] >> 16 & 0x7fffu;
+                        m = max(m, max(lo, hi));
+                    }
+#pragma unroll
+                    for (int d = 1; d < K / 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+                    return ldexpf(1.0f, scale_exp(__uint_as_float(m << 16)));
+                };
+                const float ck = row_max(a[i]), cq = row_max(b[i]);
+                if (col == 0) {
+                    lds_st(sm, L::V0 + 5 * 256 + 4 * row, ck);
+                    lds_st(sm, L::V0 + 6 * 256 + 4 * row, cq);
+                }
+            }
         }
     }
-    float *vec = reinterpret_cast<float *>(sm + L::V0);  // G in two parts, beta, rk, rq
+    float *vec = reinterpret_cast<float *>(sm + L::V0);
     char *rec = p.rec + delta_item(p, slot, hv) * (int64_t)DeltaRecord::BYTES;
     float *rvec = reinterpret_cast<float *>(rec + DeltaRecord::VEC);
     double G = 0.0, GC = 0.0;
@@ -150,15 +170,19 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
         __syncthreads();
     }
     if (wave == 0) {
-        const float rk = L2N ? vec[192 + lane] : 1.0f, rq = L2N ? vec[256 + lane] : 1.0f;
+        const float ck = IO == IO_BF16 ? vec[320 + lane] : 1.0f, cq = IO == IO_BF16 ? vec[384 + lane] : 1.0f;
+        const float rk = (L2N ? vec[192 + lane] : 1.0f) / ck, rq = (L2N ? vec[256 + lane] : 1.0f) / cq;  // (exact)
         const float eg = ex2((float)G), gh = (float)G;
         rvec[DeltaRecord::EG * 64 + lane] = eg * rk;
         rvec[DeltaRecord::EQ * 64 + lane] = eg * rq * p.scale;
         rvec[DeltaRecord::ED * 64 + lane] = ex2((float)(GC - G)) * rk;
         rvec[DeltaRecord::BT * 64 + lane] = bt;
-        rvec[DeltaRecord::GH * 64 + lane] = gh;
-        rvec[DeltaRecord::GL * 64 + lane] = (float)(G - (double)gh);
-        if (lane == 0) *reinterpret_cast<float *>(rec + DeltaRecord::GAMMA) = ex2((float)GC);
+        float *rvec2 = reinterpret_cast<float *>(rec + DeltaRecord::VEC2);
+        rvec2[DeltaRecord::GH * 64 + lane] = gh;
+        rvec2[DeltaRecord::GL * 64 + lane] = (float)(G - (double)gh);
+        rvec2[DeltaRecord::CK * 64 + lane] = ck;
+        rvec2[DeltaRecord::CQ * 64 + lane] = cq;
+        if (lane == 0) *reinterpret_cast<float *>(rec + DeltaRecord::SCAL) = ex2((float)GC);
     }
 
     // rows r = 16 wave + l16 of A and P, columns 16 s + 4 q4 + e
@@ -203,18 +227,34 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
             }
         }
     }
-    // blocks 2 j and 2 j + 1 of block row `wave` to the record's planes
-    auto st_pair = [&](int plane, int j, f32x4 x0, f32x4 x1) {
-        bf16x4 h0, l0, h1, l1;
-        split4(x0, h0, l0);
-        split4(x1, h1, l1);
+    // blocks 2 j and 2 j + 1 of block row `wave`, times sc, to the record's planes
+    auto st_pair = [&](int plane, int j, f32x4 x0, f32x4 x1, float sc, bool low) {
+        i32x4 h, l;
+        split8_f16(x0, x1, sc, h, l);
         char *dst = rec + plane + DeltaRecord::frag(wave, j) + 16 * lane;
-        *reinterpret_cast<bf16x8 *>(dst) = cat4(h0, h1);
-        *reinterpret_cast<bf16x8 *>(dst + DeltaRecord::PLANE) = cat4(l0, l1);
+        *reinterpret_cast<i32x4 *>(dst) = h;
+        if (low) *reinterpret_cast<i32x4 *>(dst + DeltaRecord::PLANE) = l;
     };
-    st_pair(DeltaRecord::PH, 0, Pt[0], Pt[1]);
-    if (wave >= 2) st_pair(DeltaRecord::PH, 1, Pt[2], Pt[3]);
+    // the waves' largest magnitudes, at vec[448 + 4 which + wave]
+    auto put_max = [&](int which, const f32x4 (&x)[4]) {
+        float m = col_max(x);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        if (lane == 0) vec[448 + 4 * which + wave] = m;
+    };
+    auto chunk_exp = [&](int which) {
+        const f32x4 m = lds_ld<f32x4>(sm, L::V0 + (448 + 4 * which) * 4);
+        return scale_exp(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+    };
+    put_max(0, Pt);
     __syncthreads();  // the tiles are done with
+    {
+        const int ex = chunk_exp(0);
+        const float sc = ldexpf(1.0f, ex);
+        st_pair(DeltaRecord::PH, 0, Pt[0], Pt[1], sc, p.low_p);
+        if (wave >= 2) st_pair(DeltaRecord::PH, 1, Pt[2], Pt[3], sc, p.low_p);
+        if (t == 0) *reinterpret_cast<float *>(rec + DeltaRecord::SCAL + 8) = ldexpf(1.0f, -ex);
+    }
 
     float *A = reinterpret_cast<float *>(sm + L::A0), *TD = reinterpret_cast<float *>(sm + L::T0);
 #pragma unroll
@@ -268,8 +308,13 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
             Tt[s] = -res;
         }
     }
-    st_pair(DeltaRecord::TH, 0, Tt[0], Tt[1]);
-    if (wave >= 2) st_pair(DeltaRecord::TH, 1, Tt[2], Tt[3]);
+    put_max(1, Tt);
+    __syncthreads();
+    const int ex = chunk_exp(1);
+    const float sc = ldexpf(1.0f, ex);
+    st_pair(DeltaRecord::TH, 0, Tt[0], Tt[1], sc, true);
+    if (wave >= 2) st_pair(DeltaRecord::TH, 1, Tt[2], Tt[3], sc, true);
+    if (t == 0) *reinterpret_cast<float *>(rec + DeltaRecord::SCAL + 4) = ldexpf(1.0f, -ex);
 }
 
 // -------------------------------------------------------- sequential pass --
@@ -281,7 +326,9 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
 // touch no global memory but for the states.
 constexpr int LW = 4;  // staging waves
 
-template <int K, int COLS, bool CKPT>
+// For 16-bit outputs next to bf16 rounding (2^-9) the high parts of S, P and U
+// do (2^-12); next to fp16 rounding they do not.
+template <int K, int IO, int COLS, bool CKPT>
 struct StateLds {
     static constexpr int TILE = Tile<K>::BYTES;
     static constexpr int VS = 2 * COLS + 16;  // row stride of the V tile (later the chunk's outputs)
@@ -289,8 +336,8 @@ struct StateLds {
     static constexpr int Q0 = TILE;           // (outputs only)
     static constexpr int V0 = CKPT ? TILE : 2 * TILE;
     static constexpr int R0 = V0 + 64 * VS;   // the record: planes of T (and P), vectors
-    static constexpr int RP = CKPT ? DeltaRecord::PH : DeltaRecord::VEC;  // bytes of planes
-    static constexpr int RCH = (RP + DeltaRecord::GAMMA + 16 - DeltaRecord::VEC) / 16;
+    static constexpr int RP = CKPT ? DeltaRecord::PH : IO == IO_BF16 ? DeltaRecord::PL : DeltaRecord::VEC;  // bytes of planes
+    static constexpr int RCH = (RP + DeltaRecord::SCAL + 16 - DeltaRecord::VEC) / 16;
     static constexpr int G0 = R0 + RP;        // its vectors
     static constexpr int HALF = (R0 + 16 * RCH + 511) / 512 * 512;
     static constexpr int SIZE = 2 * HALF;
@@ -300,7 +347,7 @@ template <int K, int IO, int NC, bool CKPT>
 __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams p)
 {
     constexpr int COLS = 16 * NC;
-    using L = StateLds<K, COLS, CKPT>;
+    using L = StateLds<K, IO, COLS, CKPT>;
     using TL = Tile<K>;
     constexpr int KT = K / 16, KS = K / 32;
     constexpr bool AHEAD = NC < 8;
@@ -324,6 +371,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         constexpr int VPT = (VCH + TH - 1) / TH;
         constexpr int RPT = (L::RCH + TH - 1) / TH;
         i32x4 fk[CPT], fq[CPT], fv[VPT], fr[RPT];
+        float ck[CPT], cq[CPT];  // the rows' powers of two
         auto fetch = [&](int64_t c) {
             const int64_t t0 = rng.b + c * CHUNK;
             const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
@@ -343,19 +391,28 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
                     fv[i] = buf_ld16<i32x4>(rv, (uint32_t)(row * (int)p.sv + vb * COLS + cc * 8) * 2);
             }
             const char *rec = p.rec + delta_item(p, slot0 + c, hv) * (int64_t)DeltaRecord::BYTES;
+            if constexpr (IO == IO_BF16) {
+                const float *v2 = reinterpret_cast<const float *>(rec + DeltaRecord::VEC2);
+#pragma unroll
+                for (int i = 0; i < CPT; ++i) {
+                    const int row = (t + TH * i) / (K / 8);
+                    ck[i] = v2[DeltaRecord::CK * 64 + row];
+                    if constexpr (!CKPT) cq[i] = v2[DeltaRecord::CQ * 64 + row];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                const int id = t + TH * i;  // planes first, then (past P without outputs) the vectors
+                const int id = t + TH * i;  // the planes that are used, then the vectors
                 if (id < L::RCH)
-                    fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id + (CKPT && 16 * id >= L::RP ? DeltaRecord::VEC - L::RP : 0));
+                    fr[i] = *reinterpret_cast<const i32x4 *>(rec + 16 * id + (16 * id >= L::RP ? DeltaRecord::VEC - L::RP : 0));
             }
         };
         auto stage = [&](char *half) {
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
                 const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
-                lds_st(half, L::K0 + TL::piece(row, cc), fk[i]);
-                if constexpr (!CKPT) lds_st(half, L::Q0 + TL::piece(row, cc), fq[i]);
+                lds_st(half, L::K0 + TL::piece(row, cc), row_f16<IO>(fk[i], ck[i]));
+                if constexpr (!CKPT) lds_st(half, L::Q0 + TL::piece(row, cc), row_f16<IO>(fq[i], cq[i]));
             }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -409,7 +466,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (state_row(i, q4) + e) * sr + col * sc) : 0.0f;
-    RightOp<IO, KS> So;
+    constexpr int OP = IO == IO_BF16 ? 1 : 2;  // parts of what only the outputs need
+    RightOp<KS> So;
     So.set(S);
     __syncthreads();
     for (int64_t c = 0; c < nch; ++c) {
@@ -422,37 +480,39 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             for (int mt = 0; mt < 4; ++mt) x[mt] = lds_ld<f32x4>(half, L::G0 + which * 256 + (16 * mt + 4 * q4) * 4);
         };
         // the left operands of four independent products, and the products
-        auto rows = [&](const char *tile, int j, bf16x8 (&a)[4]) {
+        auto rows = [&](const char *tile, int j, i32x4 (&a)[4]) {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) a[mt] = TL::row(tile, mt, j, q4, l16);
         };
-        auto cols = [&](int i0, int j, bf16x8 (&a)[4]) {
+        auto cols = [&](int i0, int j, i32x4 (&a)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = TL::col(KL, i0 + i, j, q4, l16);
         };
-        auto times = [&](const auto &op, const bf16x8 (&a)[4], int j, f32x4 (&y)[4]) {
+        auto times = [&](const auto &op, int parts, const i32x4 (&a)[4], int j, f32x4 (&y)[4]) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < parts; ++part)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = op.mul1(a[i], j, part, y[i]);
         };
-        auto frags = [&](const char *plane, int j, bf16x8 (&a)[4]) {
+        auto frags = [&](const char *plane, int j, i32x4 (&a)[4]) {
 #pragma unroll
             for (int mt = 2 * j; mt < 4; ++mt) a[mt] = ld_frag(plane, mt, j, lane);
         };
-        auto lower = [&](const bf16x8 (&ah)[4], const bf16x8 (&al)[4], bf16x8 h, bf16x8 l, int j, f32x4 (&y)[4]) {
+        // (parts of the plane and of the operand: 2, or 1 of each)
+        auto lower = [&](const i32x4 (&ah)[4], const i32x4 (&al)[4], const auto &op, int parts, int j, f32x4 (&y)[4]) {
 #pragma unroll
-            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(ah[mt], h, y[mt]);
+            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = op.mul1(ah[mt], j, 0, y[mt]);
+            if (parts == 2) {
 #pragma unroll
-            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(ah[mt], l, y[mt]);
+                for (int mt = 2 * j; mt < 4; ++mt) y[mt] = op.mul1(ah[mt], j, 1, y[mt]);
 #pragma unroll
-            for (int mt = 2 * j; mt < 4; ++mt) y[mt] = mfma_bf16(al[mt], h, y[mt]);
+                for (int mt = 2 * j; mt < 4; ++mt) y[mt] = op.mul1(al[mt], j, 0, y[mt]);
+            }
         };
         constexpr f32x4 zero = {0, 0, 0, 0};
         f32x4 R[4] = {zero, zero, zero, zero}, o[4] = {zero, zero, zero, zero}, U[4] = {zero, zero, zero, zero};
-        f32x4 v[4], bt[4], eg[4];
-        bf16x8 a0[4], a1[4], b0[4], b1[4], h2[2], l2[2];
-
+        f32x4 v[4], bt[4], eg[4], ed[4], eq[4];
+        i32x4 a0[4], a1[4], b0[4], b1[4];
         // Every block of loads stands where the products two regions before
         // its use begin (AHEAD), or at its use: two computing waves per SIMD
         // hide each other's waits, and have a third fewer registers.
@@ -472,7 +532,12 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             vec(DeltaRecord::EG, eg);
             vec(DeltaRecord::BT, bt);
         };
-        const float gamma = lds_ld<float>(half, L::G0 + DeltaRecord::NVEC * 256);
+        auto planes = [&](const char *plane, int parts, int j, i32x4 (&a)[4], i32x4 (&b)[4]) {
+            frags(plane, j, a);
+            if (parts == 2) frags(plane + DeltaRecord::PLANE, j, b);
+        };
+        const f32x4 scal = lds_ld<f32x4>(half, L::G0 + DeltaRecord::SCAL - DeltaRecord::VEC);  // e^(G_C), 1 / scales of T and P
+        const float gamma = scal[0];
 
         // K S
         early([&] { rows(KL, 0, a0), rows(KL, 1, a1); });
@@ -485,14 +550,14 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
             late([&] { rows(KL, j, a0); });
-            times(So, a0, j, R);
+            times(So, 2, a0, j, R);
             early([&] {
                 if (j + 2 < KS) rows(KL, j + 2, a0);
                 else if (!CKPT) rows(QL, 0, a0);
             });
             fence();
             late([&] { rows(KL, j + 1, a1); });
-            times(So, a1, j + 1, R);
+            times(So, 2, a1, j + 1, R);
             early([&] {
                 if (j + 2 < KS) rows(KL, j + 3, a1);
                 else rv();
@@ -502,32 +567,47 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         }
         // R = beta (V - e^G K S) as a right operand, beside half of Q S
         late(rv);
-        early([&] { frags(TH, 0, b0), frags(TH + DeltaRecord::PLANE, 0, b1); });
+        early([&] { planes(TH, 2, 0, b0, b1); });
         if constexpr (!CKPT && AHEAD) {
-            times(So, a0, 0, o);
+            times(So, OP, a0, 0, o);
             if (KS > 2) rows(QL, 2, a0);
-            times(So, a1, 1, o);
+            times(So, OP, a1, 1, o);
             if (KS > 2) rows(QL, 3, a1);
         }
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) R[mt] = bt[mt] * (v[mt] - eg[mt] * So.scaled(R[mt]));
-        split_rows(R, h2, l2);
+        for (int mt = 0; mt < 4; ++mt) R[mt] = bt[mt] * (v[mt] - eg[mt] * So.inv * R[mt]);
+        RightOp<2> Ro;
+        Ro.set(R);
         fence();
         // U = T R, and e^(G_C - G) U, beside the other half
-        late([&] { frags(TH, 0, b0), frags(TH + DeltaRecord::PLANE, 0, b1); });
-        lower(b0, b1, h2[0], l2[0], 0, U);
-        f32x4 ed[4], W[4];
-        early([&] { frags(TH, 1, b0), frags(TH + DeltaRecord::PLANE, 1, b1), vec(DeltaRecord::ED, ed); });
+        late([&] { planes(TH, 2, 0, b0, b1); });
+        lower(b0, b1, Ro, 2, 0, U);
+        early([&] { planes(TH, 2, 1, b0, b1), vec(DeltaRecord::ED, ed); });
         fence();
-        late([&] { frags(TH, 1, b0), frags(TH + DeltaRecord::PLANE, 1, b1); });
-        lower(b0, b1, h2[1], l2[1], 1, U);
+        late([&] { planes(TH, 2, 1, b0, b1); });
+        lower(b0, b1, Ro, 2, 1, U);
         early([&] { cols(0, 0, b0), cols(0, 1, b1); });
         fence();
         if constexpr (!CKPT && KS > 2 && AHEAD) {
-            times(So, a0, 2, o);
-            times(So, a1, 3, o);
+            times(So, OP, a0, 2, o);
+            times(So, OP, a1, 3, o);
         }
+        const float tinv = Ro.inv * scal[1];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) U[mt] *= tinv;
         // O = scale e^G Q S + P U, left where this wave's columns of V were
+        RightOp<2, OP> Uo;
+        auto outputs = [&](int j) {
+            if (j == 0) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) o[mt] = o[mt] * (eq[mt] * So.inv);
+            }
+            f32x4 y[4] = {zero, zero, zero, zero};
+            lower(j ? a0 : b0, j ? a1 : b1, Uo, OP, j, y);
+            const float s = Uo.inv * scal[2];
+#pragma unroll
+            for (int mt = 2 * j; mt < 4; ++mt) o[mt] += y[mt] * s;
+        };
         auto store_out = [&]() {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) st_rows16<IO>(half + L::V0 + (16 * mt + 4 * q4) * L::VS + 32 * wave, L::VS, o[mt], l16);
@@ -536,63 +616,60 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
                 rows(QL, j, a0);
-                times(So, a0, j, o);
+                times(So, OP, a0, j, o);
             }
-            vec(DeltaRecord::EQ, ed);
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * ed[mt];
-            split_rows(U, h2, l2);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                frags(PH, j, b0);
-                frags(PH + DeltaRecord::PLANE, j, b1);
-                lower(b0, b1, h2[j], l2[j], j, o);
-            }
+            vec(DeltaRecord::EQ, eq);
+            Uo.set(U);
+            planes(PH, OP, 0, b0, b1);
+            outputs(0);
+            planes(PH, OP, 1, a0, a1);
+            outputs(1);
             store_out();
         }
         late([&] { vec(DeltaRecord::ED, ed); });
+        RightOp<2> Wo;
+        {
+            f32x4 W[4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
-            W[mt] = U[mt] * ed[mt];
+            for (int mt = 0; mt < 4; ++mt) {
+                if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
+                W[mt] = U[mt] * ed[mt];
+            }
+            Wo.set(W);
         }
-        RightOp<IO, 2> Wo;
-        Wo.set(W);
         fence();
         // S <- e^(G_C) S + K^T (e^(G_C - G) U)
-        f32x4 eq[4];
 #pragma unroll
         for (int i0 = 0; i0 < KT; i0 += 4) {
-            f32x4 s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = IO == IO_F16 ? zero : S[i0 + i] * gamma;
+            f32x4 s[4] = {zero, zero, zero, zero};
             late([&] { cols(i0, 0, b0); });
-            times(Wo, b0, 0, s);
+            times(Wo, 2, b0, 0, s);
             early([&] {
                 if (i0 + 4 < KT) cols(i0 + 4, 0, b0);
-                else if (!CKPT) frags(PH, 0, b0);
+                else if (!CKPT) planes(PH, OP, 0, b0, a0);
             });
             fence();
             late([&] { cols(i0, 1, b1); });
-            times(Wo, b1, 1, s);
+            times(Wo, 2, b1, 1, s);
             early([&] {
                 if (i0 + 4 < KT) cols(i0 + 4, 1, b1);
-                else if (!CKPT) frags(PH + DeltaRecord::PLANE, 0, b1), vec(DeltaRecord::EQ, eq);
+                else if (!CKPT) vec(DeltaRecord::EQ, eq);
             });
-            if (!CKPT && AHEAD && i0 == 0) split_rows(U, h2, l2);
+            if (!CKPT && AHEAD && i0 == 0) Uo.set(U);
             fence();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[i0 + i] = IO == IO_F16 ? S[i0 + i] * gamma + s[i] * Wo.inv : s[i];
+            for (int i = 0; i < 4; ++i) S[i0 + i] = S[i0 + i] * gamma + s[i] * Wo.inv;
         }
         if constexpr (!CKPT && AHEAD) {
             // beside the next chunk's operand of S
-            frags(PH, 1, a0);
-            frags(PH + DeltaRecord::PLANE, 1, a1);
+            if constexpr (OP == 2) {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) o[mt] = So.scaled(o[mt]) * eq[mt];
-            lower(b0, b1, h2[0], l2[0], 0, o);
+                for (int mt = 0; mt < 4; ++mt) b1[mt] = a0[mt];
+            }
+            planes(PH, OP, 1, a0, a1);
+            outputs(0);
             So.set(S);
-            lower(a0, a1, h2[1], l2[1], 1, o);
+            outputs(1);
             store_out();
         } else {
             So.set(S);
