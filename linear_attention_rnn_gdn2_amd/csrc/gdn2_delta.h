@@ -50,6 +50,7 @@ struct DeltaParams {
     uint16_t *dbeta;        // [T, HV] io
     float *s_ck, *ds_ck;    // state entering / gradient of the state leaving each chunk: K x V per item
     float *u_ck, *y_ck;     // U and dY of each chunk: 64 x V per item
+    float *mx;              // [item][V / 16][8]: largest magnitudes of S, U, v, (0), dS, dY, dO, (0) in 16 columns of a chunk
     float *dq_ws, *dk_ws;   // [T, HV, K] per value head (grouped heads only)
 };
 

@@ -191,7 +191,7 @@ struct DeltaBwd {
 
 // Byte offsets of the backward's workspace.
 struct BwdSpace {
-    int64_t rec, s, ds, u, y, dq, dk, total;
+    int64_t rec, s, ds, u, y, mx, dq, dk, total;
     BwdSpace(int64_t T, int64_t N, int64_t H, int64_t HV, int64_t K, int64_t V)
     {
         const int64_t items = gdn2::slot_count(T, N) * HV;
@@ -206,6 +206,7 @@ struct BwdSpace {
         ds = take(T > 0 ? items * K * V * 4 : 0);
         u = take(T > 0 ? items * 64 * V * 4 : 0);
         y = take(T > 0 ? items * 64 * V * 4 : 0);
+        mx = take(T > 0 ? items * (V / 16) * 32 : 0);
         dq = take(H != HV ? T * HV * K * 4 : 0);
         dk = take(H != HV ? T * HV * K * 4 : 0);
         total = at;
@@ -298,6 +299,7 @@ int validate(const DeltaBwd &a, void *ws, int64_t ws_bytes, DeltaParams *p)
     p->ds_ck = reinterpret_cast<float *>(b + w.ds);
     p->u_ck = reinterpret_cast<float *>(b + w.u);
     p->y_ck = reinterpret_cast<float *>(b + w.y);
+    p->mx = reinterpret_cast<float *>(b + w.mx);
     p->dq_ws = reinterpret_cast<float *>(b + w.dq);
     p->dk_ws = reinterpret_cast<float *>(b + w.dk);
     return GDN2_OK;

@@ -209,6 +209,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = dS[i];
         }
+        const float smax = So.mx;
         constexpr f32x4 zero = {0, 0, 0, 0};
         // dU = e^(G_C - G) (K dS) + P^T dO
         f32x4 U[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero}, x4[4], dO[4];
@@ -262,6 +263,10 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
             const float tinv = Uo.inv * scal[1];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) Y[mt] *= tinv;
+        }
+        {
+            const f32x4 m = {max16(smax), max16(col_max(Y)), max16(Oo.mx), 0.0f};
+            if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8 + 4) = m;
         }
         // dV = beta dY; the right operands e^G dV (negated) and scale e^G dO
         RightOp<2> E, F;
@@ -320,10 +325,11 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 // staged value-major ([v][k] and [v][token], as the checkpoints' fragments
 // hold them); wave w owns key columns 16 w .. 16 w + 15 of dQ and dK and
 // every (D / 16)-th 16x16 tile of the two score gradients, computed
-// transposed: a lane then holds four columns of one row r. Two workgroups
-// share a compute unit and hide each other's loads (with bf16 inputs, 128
-// registers; one with the next block's loads in registers was slower, 1.75 ms
-// against the figure below), so that nothing is fetched ahead.
+// transposed: a lane then holds four columns of one row r. All operands are
+// fp16 parts under one power of two per operand and chunk (the sequential
+// passes leave the largest magnitudes). Two workgroups share a compute unit
+// and hide each other's loads; one with the next block's loads in registers
+// was slower (1.75 against 1.35 ms on 8 sequences, 37,517 tokens, 32 heads).
 
 // 32 rows (v) of C 16-bit values, written 8 bytes at a time down 16 rows and
 // read transposed from 4 rows and the 4 rows 8 further on: pieces of 16 bytes
@@ -341,29 +347,29 @@ struct ValueTile {
         return r * 2 * C + (((c >> 1) ^ swz(r)) << 4) + 8 * ((c ^ c >> 1) & 1);
     }
     // transposed: element (m, k) = tile[k][m], rows k = 8 q4 .., columns m = 16 w + l16
-    __device__ static __forceinline__ bf16x8 col(const char *tile, int w, int q4, int l16)
+    __device__ static __forceinline__ i32x4 col(const char *tile, int w, int q4, int l16)
     {
         const int r = 8 * q4 + (l16 >> 2), c = 4 * w + (l16 & 3);
-        return cat4(lds_tr(tile, quad(r, c)), lds_tr(tile, quad(r + 4, c)));
+        return __builtin_bit_cast(i32x4, cat4(lds_tr(tile, quad(r, c)), lds_tr(tile, quad(r + 4, c))));
     }
 };
 // 64 rows (tokens) of 32 16-bit values: 16-byte piece c of row r.
 __device__ __forceinline__ int token_piece(int r, int c) { return r * 64 + ((c ^ (r >> 2 & 3)) << 4); }
 
-template <int D, int NP>
+template <int D>
 struct GradLds {
     // the block of 32 value columns
-    static constexpr int OT = 64 * 64;        // a part of dO or V
-    static constexpr int O0 = 0, VT0 = NP * OT;
+    static constexpr int OT = 64 * 64;        // dO or V
+    static constexpr int O0 = 0, VT0 = OT;
     static constexpr int VP = ValueTile<64>::BYTES;
-    static constexpr int U0 = 2 * NP * OT, Y0 = U0 + 2 * VP;
+    static constexpr int U0 = 2 * OT, Y0 = U0 + 2 * VP;
     static constexpr int SP = ValueTile<D>::BYTES;
     static constexpr int S0 = Y0 + 2 * VP, DS0 = S0 + 2 * SP;
     static constexpr int WEND = DS0 + 2 * SP;
     // over it, once all value columns are done: K, Q, and the score gradients' planes
     static constexpr int TILE = Tile<D>::BYTES;
-    static constexpr int K0 = 0, Q0 = NP * TILE;
-    static constexpr int DP0 = 2 * NP * TILE, DA0 = DP0 + 2 * PlaneTile::BYTES;
+    static constexpr int K0 = 0, Q0 = TILE;
+    static constexpr int DP0 = 2 * TILE, DA0 = DP0 + 2 * PlaneTile::BYTES;
     static constexpr int XEND = DA0 + 2 * PlaneTile::BYTES;
     // vectors, and sums to join over waves and tiles
     static constexpr int NWV = D / 16;
@@ -376,7 +382,8 @@ struct GradLds {
     static constexpr int KKR = COL + 3 * 256;                       // row sums of D kk (dY U^T): [4][64]
     static constexpr int YV = KKR + 4 * 256;                        // [64]
     static constexpr int DOT = YV + 256;                            // [wave]
-    static constexpr int SIZE = DOT + 16 * NWV;
+    static constexpr int PMX = DOT + 32;                            // largest of dP, dA: [2][wave]
+    static constexpr int SIZE = PMX + 64;
 };
 
 // The value again, as one the compiler knows nothing of: what is computed
@@ -398,10 +405,9 @@ __device__ __forceinline__ float sum_q4(float x)
 }
 
 template <int D, int IO>
-__global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_bwd_grad_kernel(DeltaParams p)
+__global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(DeltaParams p)
 {
-    constexpr int NP = IO == IO_F16 ? 2 : 1;
-    using L = GradLds<D, NP>;
+    using L = GradLds<D>;
     using TL = Tile<D>;
     constexpr int NW = D / 16, NT = 64 * NW;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
@@ -436,15 +442,27 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
     const __amdgpu_buffer_rsrc_t s_ck = buf_rsrc(p.s_ck + item * D * D, 4 * D * D), ds_ck = buf_rsrc(p.ds_ck + item * D * D, 4 * D * D);
     const __amdgpu_buffer_rsrc_t u_ck = buf_rsrc(p.u_ck + item * 64 * D, 256 * D), y_ck = buf_rsrc(p.y_ck + item * 64 * D, 256 * D);
 
+    // the operands' powers of two and what undoes them, from the sequential passes' maxima
+    enum { MS = 0, MU = 1, MV = 2, MD = 4, MY = 5, MO = 6 };
+    float m8 = lane < D / 2 ? p.mx[item * (D / 2) + lane] : 0.0f;  // [D / 16][8]
+    m8 = fmaxf(m8, __shfl_xor(m8, 8));
+    m8 = fmaxf(m8, __shfl_xor(m8, 16));
+    m8 = fmaxf(m8, __shfl_xor(m8, 32));
+    const int ex8 = IO == IO_F16 && ((lane & 7) == MV || (lane & 7) == MO) ? 0 : scale_exp(m8);
+    auto exp_of = [&](int which) { return __builtin_amdgcn_readlane(ex8, which); };
+    const int eS = exp_of(MS), eU = exp_of(MU), eV = exp_of(MV), eD = exp_of(MD), eY = exp_of(MY), eO = exp_of(MO);
+    auto two = [](int e) { return ldexpf(1.0f, e); };
+
     // fragment id -> (16 columns, tile, lane): 4 consecutive rows of one value column
-    auto st_frag = [&](int base, int plane, auto tile_of, f32x4 x, int id, int tiles, bool state) {
+    auto st_frag = [&](int base, int plane, auto tile_of, f32x4 x, float sc, int id, int tiles, bool state) {
         using VT = decltype(tile_of);
         const int ln = id & 63, tile = (id >> 6) % tiles, v = (id >> 6) / tiles * 16 + (ln & 15);
         const int r = state ? state_row(tile, ln >> 4) : 16 * tile + 4 * (ln >> 4);
-        bf16x4 h, l;
-        split4(x, h, l);
-        lds_st(sm, base + VT::quad(v, r >> 2), h);
-        lds_st(sm, base + plane + VT::quad(v, r >> 2), l);
+        uint32_t h0, l0, h1, l1;
+        split2_f16(x[0] * sc, x[1] * sc, h0, l0);
+        split2_f16(x[2] * sc, x[3] * sc, h1, l1);
+        lds_st(sm, base + VT::quad(v, r >> 2), u32x2{h0, h1});
+        lds_st(sm, base + plane + VT::quad(v, r >> 2), u32x2{l0, l1});
     };
 
     f32x4 aq[4], ay[4], au[4];  // dO S^T, dY S^T, U dS^T: rows 16 mt .., key columns 16 wave ..
@@ -481,10 +499,10 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
             for (int i = 0; i < SPT; ++i) fd[i] = buf_ld16<f32x4>(ds_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
             if (vb > 0) __syncthreads();  // the block before is done with
 #pragma unroll
-            for (int i = 0; i < SPT; ++i) st_frag(L::S0, L::SP, ValueTile<D>{}, fs[i], t + NT * i, D / 16, true);
+            for (int i = 0; i < SPT; ++i) st_frag(L::S0, L::SP, ValueTile<D>{}, fs[i], two(eS), t + NT * i, D / 16, true);
 #pragma unroll
-            for (int i = 0; i < UPT; ++i) st_frag(L::U0, L::VP, ValueTile<64>{}, fu[i], t + NT * i, 4, false);
-            if (t < 256) st_parts<NP>(sm + L::O0, L::OT, token_piece(t >> 2, t & 3), fo);
+            for (int i = 0; i < UPT; ++i) st_frag(L::U0, L::VP, ValueTile<64>{}, fu[i], two(eU), t + NT * i, 4, false);
+            if (t < 256) lds_st(sm, L::O0 + token_piece(t >> 2, t & 3), row_f16<IO>(fo, two(eO)));
 #pragma unroll
             for (int i = 0; i < SPT; ++i)
 #pragma unroll
@@ -494,25 +512,27 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
             for (int i = 0; i < UPT; ++i) fu[i] = buf_ld16<f32x4>(y_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
             if (t < 256) fo = buf_ld16<i32x4>(rv, off);
 #pragma unroll
-            for (int i = 0; i < SPT; ++i) st_frag(L::DS0, L::SP, ValueTile<D>{}, fd[i], t + NT * i, D / 16, true);
+            for (int i = 0; i < SPT; ++i) st_frag(L::DS0, L::SP, ValueTile<D>{}, fd[i], two(eD), t + NT * i, D / 16, true);
 #pragma unroll
-            for (int i = 0; i < UPT; ++i) st_frag(L::Y0, L::VP, ValueTile<64>{}, fu[i], t + NT * i, 4, false);
-            if (t < 256) st_parts<NP>(sm + L::VT0, L::OT, token_piece(t >> 2, t & 3), fo);
+            for (int i = 0; i < UPT; ++i) st_frag(L::Y0, L::VP, ValueTile<64>{}, fu[i], two(eY), t + NT * i, 4, false);
+            if (t < 256) lds_st(sm, L::VT0 + token_piece(t >> 2, t & 3), row_f16<IO>(fo, two(eV)));
         }
         __syncthreads();
         again();
-        const bf16x8 sh = ValueTile<D>::col(sm + L::S0, wave, q4, l16), sl = ValueTile<D>::col(sm + L::S0 + L::SP, wave, q4, l16);
-        const bf16x8 dh = ValueTile<D>::col(sm + L::DS0, wave, q4, l16), dl = ValueTile<D>::col(sm + L::DS0 + L::SP, wave, q4, l16);
-        auto o_row = [&](int base, int part, int mt) { return lds_ld<bf16x8>(sm, base + part * L::OT + token_piece(16 * mt + l16, q4)); };
+        const i32x4 sh = ValueTile<D>::col(sm + L::S0, wave, q4, l16), sl = ValueTile<D>::col(sm + L::S0 + L::SP, wave, q4, l16);
+        const i32x4 dh = ValueTile<D>::col(sm + L::DS0, wave, q4, l16), dl = ValueTile<D>::col(sm + L::DS0 + L::SP, wave, q4, l16);
+        auto o_row = [&](int base, int mt) { return lds_ld<i32x4>(sm, base + token_piece(16 * mt + l16, q4)); };
         auto v_col = [&](int base, int part, int mt) { return ValueTile<64>::col(sm + base + part * L::VP, mt, q4, l16); };
+        // acc + (ah + al) (bh + bl), without al bl
+        auto split = [](i32x4 ah, i32x4 al, i32x4 bh, i32x4 bl, f32x4 acc) {
+            return mfma_f16(al, bh, mfma_f16(ah, bl, mfma_f16(ah, bh, acc)));
+        };
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const bf16x8 o = o_row(L::O0, 0, mt);
-            bf16x8 o2 = o;
-            if constexpr (NP == 2) o2 = o_row(L::O0, 1, mt);
-            aq[mt] = mfma_split<NP == 2>(o, o2, sh, sl, aq[mt]);
-            ay[mt] = mfma_split<true>(v_col(L::Y0, 0, mt), v_col(L::Y0, 1, mt), sh, sl, ay[mt]);
-            au[mt] = mfma_split<true>(v_col(L::U0, 0, mt), v_col(L::U0, 1, mt), dh, dl, au[mt]);
+            const i32x4 o = o_row(L::O0, mt);
+            aq[mt] = mfma_f16(o, sl, mfma_f16(o, sh, aq[mt]));
+            ay[mt] = split(v_col(L::Y0, 0, mt), v_col(L::Y0, 1, mt), sh, sl, ay[mt]);
+            au[mt] = split(v_col(L::U0, 0, mt), v_col(L::U0, 1, mt), dh, dl, au[mt]);
             if (mt & 1) region();
         }
 #pragma unroll
@@ -521,24 +541,34 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
             if (id < 10) {
                 int br, bc;
                 tri(id, br, bc);
-                const bf16x8 uh = v_col(L::U0, 0, bc), ul = v_col(L::U0, 1, bc), o = o_row(L::O0, 0, br);
-                ou[i] = mfma_bf16(uh, o, ou[i]);
-                ou[i] = mfma_bf16(ul, o, ou[i]);
-                if constexpr (NP == 2) ou[i] = mfma_bf16(uh, o_row(L::O0, 1, br), ou[i]);
-                yu[i] = mfma_split<true>(uh, ul, v_col(L::Y0, 0, br), v_col(L::Y0, 1, br), yu[i]);
+                const i32x4 uh = v_col(L::U0, 0, bc), ul = v_col(L::U0, 1, bc), o = o_row(L::O0, br);
+                ou[i] = mfma_f16(ul, o, mfma_f16(uh, o, ou[i]));
+                yu[i] = split(uh, ul, v_col(L::Y0, 0, br), v_col(L::Y0, 1, br), yu[i]);
             }
             region();
         }
         if (wave < 4) {  // the diagonal of dY V^T, block `wave`
-            const bf16x8 vh = o_row(L::VT0, 0, wave), yh = v_col(L::Y0, 0, wave), yl = v_col(L::Y0, 1, wave);
-            yv = mfma_bf16(yh, vh, yv);
-            yv = mfma_bf16(yl, vh, yv);
-            if constexpr (NP == 2) yv = mfma_bf16(yh, o_row(L::VT0, 1, wave), yv);
+            const i32x4 vh = o_row(L::VT0, wave);
+            yv = mfma_f16(v_col(L::Y0, 1, wave), vh, mfma_f16(v_col(L::Y0, 0, wave), vh, yv));
         }
     }
     again();
     if (wave < 4 && l16 >> 2 == q4)  // row 4 q4 + e = column l16
-        *reinterpret_cast<float *>(sm + L::YV + 4 * (16 * wave + l16)) = l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0]);
+        *reinterpret_cast<float *>(sm + L::YV + 4 * (16 * wave + l16)) =
+            (l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0])) * two(-eY - eV);
+    const float *vec = reinterpret_cast<const float *>(sm + L::VEC), *vec2 = vec + (DeltaRecord::VEC2 - DeltaRecord::VEC) / 4;
+    // one power of two for all rows of K, and one for Q's: the smallest of the rows'
+    float uk = 1.0f, uq = 1.0f;
+    if constexpr (IO == IO_BF16) {
+        uk = vec2[DeltaRecord::CK * 64 + lane];
+        uq = vec2[DeltaRecord::CQ * 64 + lane];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            uk = fminf(uk, __shfl_xor(uk, d));
+            uq = fminf(uq, __shfl_xor(uq, d));
+        }
+    }
+    const float ik = 1.0f / uk, iq = 1.0f / uq;  // (exact)
     {
         constexpr int CPT = 64 * D / 8 / NT;  // 2
         const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + D) * 2));
@@ -554,16 +584,15 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int ci = t + NT * i, row = ci / (D / 8), cc = ci % (D / 8);
-            st_parts<NP>(sm + L::K0, L::TILE, TL::piece(row, cc), a[i]);
-            st_parts<NP>(sm + L::Q0, L::TILE, TL::piece(row, cc), b[i]);
+            lds_st(sm, L::K0 + TL::piece(row, cc), row_f16<IO>(a[i], uk));
+            lds_st(sm, L::Q0 + TL::piece(row, cc), row_f16<IO>(b[i], uq));
         }
     }
     __syncthreads();
 
     again();
     // score gradients, rows r = 16 br + l16, columns s = 16 bc + 4 q4 + e: the same tiles of Q K^T and K K^T, decayed
-    const float *vec = reinterpret_cast<const float *>(sm + L::VEC), *vec2 = vec + (DeltaRecord::VEC2 - DeltaRecord::VEC) / 4;
-    auto part = [&](int base, int which, int mt, int j) { return __builtin_bit_cast(bf16x8, TL::row(sm + base + which * L::TILE, mt, j, q4, l16)); };
+    float pm = 0.0f, am = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
         const int id = wave + NW * i;
@@ -573,33 +602,31 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
             f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                const bf16x8 a = part(L::K0, 0, bc, j), kb = part(L::K0, 0, br, j), qb = part(L::Q0, 0, br, j);
-                kk = mfma_bf16(a, kb, kk);
-                qk = mfma_bf16(a, qb, qk);
-                if constexpr (NP == 2) {
-                    const bf16x8 a2 = part(L::K0, 1, bc, j);
-                    kk = mfma_bf16(a2, kb, kk);
-                    qk = mfma_bf16(a2, qb, qk);
-                    kk = mfma_bf16(a, part(L::K0, 1, br, j), kk);
-                    qk = mfma_bf16(a, part(L::Q0, 1, br, j), qk);
-                }
+                const i32x4 a = TL::row(sm + L::K0, bc, j, q4, l16);
+                kk = mfma_f16(a, TL::row(sm + L::K0, br, j, q4, l16), kk);
+                qk = mfma_f16(a, TL::row(sm + L::Q0, br, j, q4, l16), qk);
                 if (j & 1) region();
             }
+            kk *= ik * ik;
+            qk *= ik * iq;
             const int r = 16 * br + l16, s0 = 16 * bc + 4 * q4;
             const float gh = vec2[DeltaRecord::GH * 64 + r], gl = vec2[DeltaRecord::GL * 64 + r], bt = vec[DeltaRecord::BT * 64 + r];
             const f32x4 sh = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GH * 64 + s0), sl = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GL * 64 + s0);
+            const float fo = p.scale * two(-eO - eU), fy = two(-eY - eU);
             f32x4 dp, da, E;
             float kkr = 0.0f, er = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float d = ex2(fminf((gh - sh[e]) + (gl - sl[e]), 0.0f));
                 const bool below = s0 + e < r;
-                const float yd = below ? d * yu[i][e] : 0.0f;
-                dp[e] = s0 + e <= r ? p.scale * d * ou[i][e] : 0.0f;
+                const float yd = below ? d * fy * yu[i][e] : 0.0f;
+                dp[e] = s0 + e <= r ? d * fo * ou[i][e] : 0.0f;
                 da[e] = -bt * yd;
                 E[e] = below ? dp[e] * qk[e] + da[e] * kk[e] : 0.0f;
                 kkr = fmaf(yd, kk[e], kkr);
                 er += E[e];
+                pm = fmaxf(pm, fabsf(dp[e]));
+                am = fmaxf(am, fabsf(da[e]));
             }
             kkr = sum_q4(kkr);
             if (q4 == 0) *reinterpret_cast<float *>(sm + L::KKR + 256 * bc + 4 * r) = kkr;
@@ -613,17 +640,47 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
                 for (int e = 0; e < 4; ++e) ec[e] = sum16(E[e]);
                 if (l16 == 0) lds_st(sm, L::COL + 256 * (br - 1) + 4 * s0, ec);
             }
-            auto st_plane = [&](int base, int col4, f32x4 x) {
-                bf16x4 h, l;
-                split4(x, h, l);
-                lds_st(sm, base + PlaneTile::quad(r, col4), h);
-                lds_st(sm, base + PlaneTile::BYTES + PlaneTile::quad(r, col4), l);
+            ou[i] = dp;
+            yu[i] = da;
+        }
+        region();
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        pm = fmaxf(pm, __shfl_xor(pm, d));
+        am = fmaxf(am, __shfl_xor(am, d));
+    }
+    if (lane == 0) {
+        *reinterpret_cast<float *>(sm + L::PMX + 4 * wave) = pm;
+        *reinterpret_cast<float *>(sm + L::PMX + 32 + 4 * wave) = am;
+    }
+    __syncthreads();
+    pm = am = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        pm = fmaxf(pm, lds_ld<float>(sm, L::PMX + 4 * w));
+        am = fmaxf(am, lds_ld<float>(sm, L::PMX + 32 + 4 * w));
+    }
+    const int eP = scale_exp(pm), eA = scale_exp(am);
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+        const int id = wave + NW * i;
+        if (id < 10) {
+            int br, bc;
+            tri(id, br, bc);
+            const int r = 16 * br + l16, c4 = 4 * bc + q4;
+            auto st_plane = [&](int base, int col4, f32x4 x, float sc) {
+                uint32_t h0, l0, h1, l1;
+                split2_f16(x[0] * sc, x[1] * sc, h0, l0);
+                split2_f16(x[2] * sc, x[3] * sc, h1, l1);
+                lds_st(sm, base + PlaneTile::quad(r, col4), u32x2{h0, h1});
+                lds_st(sm, base + PlaneTile::BYTES + PlaneTile::quad(r, col4), u32x2{l0, l1});
             };
-            st_plane(L::DP0, s0 >> 2, dp);
-            st_plane(L::DA0, s0 >> 2, da);
+            st_plane(L::DP0, c4, ou[i], two(eP));
+            st_plane(L::DA0, c4, yu[i], two(eA));
             if (br == bc && !(br & 1)) {  // the zero block right of it
-                st_plane(L::DP0, (s0 >> 2) + 4, f32x4{0, 0, 0, 0});
-                st_plane(L::DA0, (s0 >> 2) + 4, f32x4{0, 0, 0, 0});
+                st_plane(L::DP0, c4 + 4, f32x4{0, 0, 0, 0}, 1.0f);
+                st_plane(L::DA0, c4 + 4, f32x4{0, 0, 0, 0}, 1.0f);
             }
         }
     }
@@ -649,63 +706,61 @@ __global__ __launch_bounds__(4 * D, IO == IO_F16 || D == 64 ? 2 : 4) void delta_
     }
     float *red = reinterpret_cast<float *>(sm + L::RED) + wave * 192;
     // right operands: rows 32 j .. of K and Q, the wave's columns
-    bf16x8 kc[NP][2], qc[NP][2];
+    bf16x4 kc[4], qc[4];
 #pragma unroll
-    for (int w = 0; w < NP; ++w)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            kc[w][j] = cat4(TL::quad(sm + L::K0 + w * L::TILE, 2 * j, wave, q4, l16), TL::quad(sm + L::K0 + w * L::TILE, 2 * j + 1, wave, q4, l16));
-            qc[w][j] = cat4(TL::quad(sm + L::Q0 + w * L::TILE, 2 * j, wave, q4, l16), TL::quad(sm + L::Q0 + w * L::TILE, 2 * j + 1, wave, q4, l16));
-        }
+    for (int mt = 0; mt < 4; ++mt) {
+        kc[mt] = TL::quad(sm + L::K0, mt, wave, q4, l16);
+        qc[mt] = TL::quad(sm + L::Q0, mt, wave, q4, l16);
+    }
+    const float fq = two(-eO - eS), fy = two(-eY - eS), fx = two(-eU - eD);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
         auto vec4 = [&](int which) { return lds_ld<f32x4>(sm, L::VEC + which * 256 + (16 * mt + 4 * q4) * 4); };
         auto pow2 = [&](int which) { return *reinterpret_cast<const f32x4 *>(vec2 + which * 64 + 16 * mt + 4 * q4); };
-        // (the vectors without the powers of two: the rows here are as they came)
+        // (the vectors without the rows' powers of two)
         const f32x4 ck = pow2(DeltaRecord::CK);
-        f32x4 dq = aq[mt] * (vec4(DeltaRecord::EQ) * pow2(DeltaRecord::CQ)), y = ay[mt] * (vec4(DeltaRecord::EG) * ck);
-        f32x4 x = au[mt] * (vec4(DeltaRecord::ED) * ck);
+        f32x4 dq = aq[mt] * (vec4(DeltaRecord::EQ) * pow2(DeltaRecord::CQ) * fq), y = ay[mt] * (vec4(DeltaRecord::EG) * ck * fy);
+        f32x4 x = au[mt] * (vec4(DeltaRecord::ED) * ck * fx);
         f32x4 si, sy, sx, dk = x - vec4(DeltaRecord::BT) * y;
+        // q and k of rows 16 mt + 4 q4 .., column 16 wave + l16
+        const f32x4 qv = __builtin_convertvector(__builtin_bit_cast(f16x4, qc[mt]), f32x4) * iq;
+        const f32x4 kv = __builtin_convertvector(__builtin_bit_cast(f16x4, kc[mt]), f32x4) * ik;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // q and k of row 16 mt + 4 q4 + e, column 16 wave + l16
-            float qv = (float)qc[0][mt / 2][4 * (mt & 1) + e], kv = (float)kc[0][mt / 2][4 * (mt & 1) + e];
-            if constexpr (NP == 2) {
-                qv += (float)qc[NP - 1][mt / 2][4 * (mt & 1) + e];
-                kv += (float)kc[NP - 1][mt / 2][4 * (mt & 1) + e];
-            }
-            si[e] = sum16(qv * dq[e]);
-            sy[e] = sum16(kv * y[e]);
-            sx[e] = sum16(kv * x[e]);
+            si[e] = sum16(qv[e] * dq[e]);
+            sy[e] = sum16(kv[e] * y[e]);
+            sx[e] = sum16(kv[e] * x[e]);
         }
         if (l16 == 0) {
             *reinterpret_cast<f32x4 *>(red + 16 * mt + 4 * q4) = si;
             *reinterpret_cast<f32x4 *>(red + 64 + 16 * mt + 4 * q4) = sy;
             *reinterpret_cast<f32x4 *>(red + 128 + 16 * mt + 4 * q4) = sx;
         }
-        auto add = [&](bf16x8 ah, bf16x8 al, const bf16x8 (&b)[NP][2], int j, f32x4 acc) {
-            acc = mfma_bf16(ah, b[0][j], acc);
-            acc = mfma_bf16(al, b[0][j], acc);
-            if constexpr (NP == 2) acc = mfma_bf16(ah, b[NP - 1][j], acc);
-            return acc;
-        };
         auto prow = [&](int base, int j) {
-            const int a = base + 64 * 16 * mt;
-            return cat4(lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, q4) + 2048 * j), lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, 4 + q4) + 2048 * j));
+            const int a = base + 64 * 16 * mt + 2048 * j;
+            return __builtin_bit_cast(i32x4, cat4(lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, q4)), lds_ld<bf16x4>(sm, a + PlaneTile::quad(l16, 4 + q4))));
         };
-        auto pcol = [&](int base, int j) { return __builtin_bit_cast(bf16x8, PlaneTile::col(sm + base, mt, j, q4, l16)); };
+        auto pcol = [&](int base, int j) { return PlaneTile::col(sm + base, mt, j, q4, l16); };
         constexpr int PB = PlaneTile::BYTES;
+        f32x4 pk = {0, 0, 0, 0}, pq = {0, 0, 0, 0}, ak = {0, 0, 0, 0};  // dP K, dP^T Q, (dA + dA^T) K
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+            const i32x4 k8 = __builtin_bit_cast(i32x4, cat4(kc[2 * j], kc[2 * j + 1])), q8 = __builtin_bit_cast(i32x4, cat4(qc[2 * j], qc[2 * j + 1]));
             if (j <= mt / 2) {
-                dq = add(prow(L::DP0, j), prow(L::DP0 + PB, j), kc, j, dq);
-                dk = add(prow(L::DA0, j), prow(L::DA0 + PB, j), kc, j, dk);
+                pk = mfma_f16(prow(L::DP0, j), k8, pk);
+                pk = mfma_f16(prow(L::DP0 + PB, j), k8, pk);
+                ak = mfma_f16(prow(L::DA0, j), k8, ak);
+                ak = mfma_f16(prow(L::DA0 + PB, j), k8, ak);
             }
             if (j >= mt / 2) {
-                dk = add(pcol(L::DP0, j), pcol(L::DP0 + PB, j), qc, j, dk);
-                dk = add(pcol(L::DA0, j), pcol(L::DA0 + PB, j), kc, j, dk);
+                pq = mfma_f16(pcol(L::DP0, j), q8, pq);
+                pq = mfma_f16(pcol(L::DP0 + PB, j), q8, pq);
+                ak = mfma_f16(pcol(L::DA0, j), k8, ak);
+                ak = mfma_f16(pcol(L::DA0 + PB, j), k8, ak);
             }
         }
+        dq += pk * (two(-eP) * ik);
+        dk += pq * (two(-eP) * iq) + ak * (two(-eA) * ik);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             // (rows past the chunk's end lie past the buffers' range)

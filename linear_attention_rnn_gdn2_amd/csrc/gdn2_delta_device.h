@@ -6,11 +6,9 @@
 // two has brought the largest value of its column (or chunk) near 2^14: 21
 // significant bits next to that value, 2^-38 of it at the bottom. Products of
 // two such operands drop l l. Rows of q and k that are fp16 values are used
-// as they are; bf16 rows are brought into fp16's range by a power of two per
-// row (exactly, but for values under 2^-38 of the row's largest). The gradient
-// pass uses two bf16 parts (16 bits, no scales), bf16 inputs as one part and
-// fp16 inputs exactly as two. The state, the chunk's WY solution and all sums
-// are float32.
+// as they are; bf16 rows are brought into fp16's range by a power of two
+// (exactly, but for values under 2^-38 of the largest). The state, the chunk's
+// WY solution and all sums are float32.
 //
 // Fragments (lane = 16 q4 + l16). A 16x16 accumulator tile holds rows
 // 4 q4 + e (e = 0..3) of column l16. As the right operand of the next product
@@ -27,35 +25,7 @@
 namespace gdn2 {
 namespace dev {
 
-constexpr float LOG2E = 1.44269504088896340736f;
-constexpr int PSTR = 144;  // LDS row stride of a 64-column bf16 plane (bytes): 16 rows apart in banks by 16 bytes
-
-// x = h + l. In pairs: a packed pair of high parts is widened by a shift and
-// a mask, where converting it back element by element costs twice as much.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &l)
-{
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x0, x1}, bf16x2));
-    l = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x0 - __uint_as_float(h << 16),
-                                                                    x1 - __uint_as_float(h & 0xffff0000u)}, bf16x2));
-}
-__device__ __forceinline__ void split4(f32x4 x, bf16x4 &h, bf16x4 &l)
-{
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    uint32_t h0, l0, h1, l1;
-    split2(x[0], x[1], h0, l0);
-    split2(x[2], x[3], h1, l1);
-    h = __builtin_bit_cast(bf16x4, u32x2{h0, h1});
-    l = __builtin_bit_cast(bf16x4, u32x2{l0, l1});
-}
-__device__ __forceinline__ void split8(f32x8 x, bf16x8 &h, bf16x8 &l)
-{
-    bf16x4 h0, l0, h1, l1;
-    split4(__builtin_shufflevector(x, x, 0, 1, 2, 3), h0, l0);
-    split4(__builtin_shufflevector(x, x, 4, 5, 6, 7), h1, l1);
-    h = cat4(h0, h1);
-    l = cat4(l0, l1);
-}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <int IO>
 __device__ __forceinline__ float io_f32(uint16_t b)
@@ -68,31 +38,6 @@ __device__ __forceinline__ uint16_t f32_io(float x)  // rounded to nearest even
 {
     if constexpr (IO == IO_F16) return __builtin_bit_cast(uint16_t, (_Float16)x);
     else return __builtin_bit_cast(uint16_t, (__bf16)x);
-}
-
-// The left operand of one 32-wide step from a row-major tile in LDS: row
-// `row`, columns c0 + 4 q4 .. + 3 and c0 + 16 + 4 q4 .. + 3.
-__device__ __forceinline__ bf16x8 ld_row(const char *base, int stride, int row, int c0, int q4)
-{
-    const char *a = base + row * stride + 2 * (c0 + 4 * q4);
-    return cat4(*reinterpret_cast<const bf16x4 *>(a), *reinterpret_cast<const bf16x4 *>(a + 32));
-}
-// The same operand of the transposed tile: element (m, k) is tile[k][m],
-// rows k = k0 + 4 q4 .. and k0 + 16 + 4 q4 .., columns m = c0 + l16.
-__device__ __forceinline__ bf16x8 ld_col(const char *base, int stride, int k0, int c0, int q4, int l16)
-{
-    const int a = (k0 + 4 * q4 + (l16 >> 2)) * stride + 2 * (c0 + 4 * (l16 & 3));
-    return cat4(lds_tr(base, a), lds_tr(base, a + 16 * stride));
-}
-// As ld_row and ld_col with the contraction in plain order (8 q4 .. 8 q4 + 7).
-__device__ __forceinline__ bf16x8 ld_row_plain(const char *base, int stride, int row, int c0, int q4)
-{
-    return *reinterpret_cast<const bf16x8 *>(base + row * stride + 2 * (c0 + 8 * q4));
-}
-__device__ __forceinline__ bf16x8 ld_col_plain(const char *base, int stride, int k0, int c0, int q4, int l16)
-{
-    const int a = (k0 + 8 * q4 + (l16 >> 2)) * stride + 2 * (c0 + 4 * (l16 & 3));
-    return cat4(lds_tr(base, a), lds_tr(base, a + 4 * stride));
 }
 
 // The state's rows in accumulator tiles: rows 4 q4 .. of tile i are key rows
@@ -135,30 +80,6 @@ struct Tile {
         return __builtin_bit_cast(i32x4, cat4(lds_tr(tile, a), lds_tr(tile, a + 16 * RS)));
     }
 };
-
-// acc + (ah [+ al]) (bh + bl), without al bl
-template <bool TWO>
-__device__ __forceinline__ f32x4 mfma_split(bf16x8 ah, bf16x8 al, bf16x8 bh, bf16x8 bl, f32x4 acc)
-{
-    acc = mfma_bf16(ah, bh, acc);
-    acc = mfma_bf16(ah, bl, acc);
-    if constexpr (TWO) acc = mfma_bf16(al, bh, acc);
-    return acc;
-}
-
-// 16 bytes of io values as one bf16 plane (bf16) or two (fp16: exact).
-template <int NP>
-__device__ __forceinline__ void st_parts(char *base, int plane_bytes, int off, i32x4 raw)
-{
-    if constexpr (NP == 1) {
-        *reinterpret_cast<i32x4 *>(base + off) = raw;
-    } else {
-        bf16x8 h, l;
-        split8(__builtin_convertvector(__builtin_bit_cast(f16x8, raw), f32x8), h, l);
-        *reinterpret_cast<bf16x8 *>(base + off) = h;
-        *reinterpret_cast<bf16x8 *>(base + plane_bytes + off) = l;
-    }
-}
 
 // A record's fragment as a left operand.
 __device__ __forceinline__ i32x4 ld_frag(const char *plane, int mt, int j, int lane)
@@ -224,16 +145,27 @@ __device__ __forceinline__ float col_max(const f32x4 (&x)[M])
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
+// The largest of the 16 lanes of a row; every lane gets it.
+__device__ __forceinline__ float max16(float x)
+{
+    x = fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x128, 0xf, 0xf, true)));  // row_ror:8
+    x = fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x124, 0xf, 0xf, true)));  // row_ror:4
+    x = fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x122, 0xf, 0xf, true)));  // row_ror:2
+    return fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x121, 0xf, 0xf, true)));  // row_ror:1
+}
+
 // A float32 right operand of N 32-row steps (step j: tiles 2 j and 2 j + 1) in
 // PARTS fp16 parts, scaled per column.
 template <int N, int PARTS = 2>
 struct RightOp {
     i32x4 h[N], l[PARTS == 2 ? N : 1];
     float inv;  // what a product is multiplied by
+    float mx;   // the column's largest magnitude
 
     __device__ __forceinline__ void set(const f32x4 (&x)[2 * N])
     {
-        const int ex = scale_exp(col_max(x));
+        mx = col_max(x);
+        const int ex = scale_exp(mx);
         const float sc = ldexpf(1.0f, ex);
         inv = ldexpf(1.0f, -ex);
 #pragma unroll

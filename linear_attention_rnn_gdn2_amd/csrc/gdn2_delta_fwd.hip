@@ -546,6 +546,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = S[i];
         }
+        const float smax = So.mx;
         fence();
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
@@ -636,6 +637,10 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
                 W[mt] = U[mt] * ed[mt];
             }
             Wo.set(W);
+            if constexpr (CKPT) {
+                const f32x4 m = {max16(smax), max16(col_max(U)), max16(col_max(v)), 0.0f};
+                if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8) = m;
+            }
         }
         fence();
         // S <- e^(G_C) S + K^T (e^(G_C - G) U)

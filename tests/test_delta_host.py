@@ -161,7 +161,7 @@ def test_workspace_sizes(gdn2):
     assert gdn2.delta_chunk_fwd_workspace(130, 2, 4) == (130 // 64 + 2) * 4 * 26880
     assert gdn2.delta_chunk_fwd_workspace(0, 2, 4) == 0
     items = (130 // 64 + 2) * 4
-    want = items * (26880 + 8 * 64 * 64 + 512 * 64) + 2 * 130 * 4 * 64 * 4
+    want = items * (26880 + 8 * 64 * 64 + 514 * 64) + 2 * 130 * 4 * 64 * 4
     got = gdn2.delta_chunk_bwd_workspace(130, 2, 2, 4, 64, 64)
     assert want <= got <= want + 8 * 256
     assert gdn2.delta_chunk_bwd_workspace(130, 2, 4, 4, 64, 64) < got
