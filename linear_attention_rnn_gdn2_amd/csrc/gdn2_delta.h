@@ -97,6 +97,7 @@ struct QkParams {
     int64_t sx[2], hsx[2], sy[2], hsy[2], sdy[2], hsdy[2];
     float *part;                 // backward with weights: [groups][2][K] partial sums
     int32_t groups;
+    int32_t split;               // log2 of the waves per token
 };
 
 // Value columns per workgroup of the sequential passes: the fewest (32, 64 or

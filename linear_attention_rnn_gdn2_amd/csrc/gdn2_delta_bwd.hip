@@ -268,47 +268,42 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
             const f32x4 m = {max16(smax), max16(col_max(Y)), max16(Oo.mx), 0.0f};
             if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8 + 4) = m;
         }
-        // dV = beta dY; the right operands e^G dV (negated) and scale e^G dO
-        RightOp<2> E, F;
-        {
-            f32x4 dv[4];
-            vec(DeltaRecord::BT, x4);
+        // dS <- e^(G_C) dS + tile^T x
+        auto add_outer = [&](const char *tile, const f32x4 (&x)[4], float g) {
+            RightOp<2> op;
+            op.set(x);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = Y[mt];
-                dv[mt] = Y[mt] * x4[mt];
-                st_rows16<IO>(half + L::O0 + (16 * mt + 4 * q4) * L::OS + 32 * wave, L::OS, dv[mt], l16);
-            }
-            vec(DeltaRecord::EG, x4);
+            for (int i0 = 0; i0 < KT; i0 += 4) {
+                f32x4 s[4] = {zero, zero, zero, zero};
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) dv[mt] *= -x4[mt];
-            E.set(dv);
-            vec(DeltaRecord::EQ, x4);
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) dO[mt] *= x4[mt];
-            F.set(dO);
-        }
+                    for (int i = 0; i < 4; ++i) a[i] = TL::col(tile, i0 + i, j, q4, l16);
 #pragma unroll
-        for (int i0 = 0; i0 < KT; i0 += 4) {
-            f32x4 s[4] = {zero, zero, zero, zero}, w[4] = {zero, zero, zero, zero};
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = TL::col(KL, i0 + i, j, q4, l16);
-                    b[i] = TL::col(QL, i0 + i, j, q4, l16);
+                        for (int i = 0; i < 4; ++i) s[i] = op.mul1(a[i], j, part, s[i]);
                 }
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = E.mul1(a[i], j, part, s[i]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = F.mul1(b[i], j, part, w[i]);
-                }
+                for (int i = 0; i < 4; ++i) dS[i0 + i] = dS[i0 + i] * g + s[i] * op.inv;
             }
+        };
+        vec(DeltaRecord::EQ, x4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dS[i0 + i] = dS[i0 + i] * gamma + s[i] * E.inv + w[i] * F.inv;
+        for (int mt = 0; mt < 4; ++mt) dO[mt] *= x4[mt];
+        add_outer(QL, dO, gamma);  // scale e^G dO
+        // dV = beta dY, left where this wave's columns of dO were, and -e^G dV
+        vec(DeltaRecord::BT, x4);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = Y[mt];
+            Y[mt] *= x4[mt];
+            st_rows16<IO>(half + L::O0 + (16 * mt + 4 * q4) * L::OS + 32 * wave, L::OS, Y[mt], l16);
         }
+        vec(DeltaRecord::EG, x4);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) Y[mt] *= -x4[mt];
+        add_outer(KL, Y, 1.0f);
         So.set(dS);
         __syncthreads();
     }
@@ -386,15 +381,6 @@ struct GradLds {
     static constexpr int SIZE = PMX + 64;
 };
 
-// The value again, as one the compiler knows nothing of: what is computed
-// from it stays where it is used (the lanes' LDS addresses, held over the
-// whole kernel, would take 30 registers more than there are).
-__device__ __forceinline__ int fresh(int x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 // Sum over the four lanes of a column (equal l16); every lane gets it.
 __device__ __forceinline__ float sum_q4(float x)
 {
@@ -451,7 +437,8 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
     const int ex8 = IO == IO_F16 && ((lane & 7) == MV || (lane & 7) == MO) ? 0 : scale_exp(m8);
     auto exp_of = [&](int which) { return __builtin_amdgcn_readlane(ex8, which); };
     const int eS = exp_of(MS), eU = exp_of(MU), eV = exp_of(MV), eD = exp_of(MD), eY = exp_of(MY), eO = exp_of(MO);
-    auto two = [](int e) { return ldexpf(1.0f, e); };
+    // (by its bits: a uniform value that takes no vector register; -114 <= e <= 120)
+    auto two = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
 
     // fragment id -> (16 columns, tile, lane): 4 consecutive rows of one value column
     auto st_frag = [&](int base, int plane, auto tile_of, f32x4 x, float sc, int id, int tiles, bool state) {
@@ -555,7 +542,7 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
     again();
     if (wave < 4 && l16 >> 2 == q4)  // row 4 q4 + e = column l16
         *reinterpret_cast<float *>(sm + L::YV + 4 * (16 * wave + l16)) =
-            (l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0])) * two(-eY - eV);
+            (l16 & 2 ? (l16 & 1 ? yv[3] : yv[2]) : (l16 & 1 ? yv[1] : yv[0])) * two(-eY) * two(-eV);
     const float *vec = reinterpret_cast<const float *>(sm + L::VEC), *vec2 = vec + (DeltaRecord::VEC2 - DeltaRecord::VEC) / 4;
     // one power of two for all rows of K, and one for Q's: the smallest of the rows'
     float uk = 1.0f, uq = 1.0f;
@@ -567,8 +554,11 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
             uk = fminf(uk, __shfl_xor(uk, d));
             uq = fminf(uq, __shfl_xor(uq, d));
         }
+        uk = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(uk)));
+        uq = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(uq)));
     }
-    const float ik = 1.0f / uk, iq = 1.0f / uq;  // (exact)
+    // (powers of two: the reciprocal has the exponent's complement)
+    const float ik = __uint_as_float((254u << 23) - __float_as_uint(uk)), iq = __uint_as_float((254u << 23) - __float_as_uint(uq));
     {
         constexpr int CPT = 64 * D / 8 / NT;  // 2
         const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + D) * 2));
@@ -607,20 +597,21 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
                 qk = mfma_f16(a, TL::row(sm + L::Q0, br, j, q4, l16), qk);
                 if (j & 1) region();
             }
-            kk *= ik * ik;
-            qk *= ik * iq;
+            kk = kk * ik * ik;
+            qk = qk * ik * iq;
             const int r = 16 * br + l16, s0 = 16 * bc + 4 * q4;
             const float gh = vec2[DeltaRecord::GH * 64 + r], gl = vec2[DeltaRecord::GL * 64 + r], bt = vec[DeltaRecord::BT * 64 + r];
             const f32x4 sh = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GH * 64 + s0), sl = *reinterpret_cast<const f32x4 *>(vec2 + DeltaRecord::GL * 64 + s0);
-            const float fo = p.scale * two(-eO - eU), fy = two(-eY - eU);
+            ou[i] = ou[i] * two(-eO) * two(-eU) * p.scale;
+            yu[i] = yu[i] * two(-eY) * two(-eU);
             f32x4 dp, da, E;
             float kkr = 0.0f, er = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float d = ex2(fminf((gh - sh[e]) + (gl - sl[e]), 0.0f));
                 const bool below = s0 + e < r;
-                const float yd = below ? d * fy * yu[i][e] : 0.0f;
-                dp[e] = s0 + e <= r ? d * fo * ou[i][e] : 0.0f;
+                const float yd = below ? d * yu[i][e] : 0.0f;
+                dp[e] = s0 + e <= r ? d * ou[i][e] : 0.0f;
                 da[e] = -bt * yd;
                 E[e] = below ? dp[e] * qk[e] + da[e] * kk[e] : 0.0f;
                 kkr = fmaf(yd, kk[e], kkr);
@@ -661,7 +652,7 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
         pm = fmaxf(pm, lds_ld<float>(sm, L::PMX + 4 * w));
         am = fmaxf(am, lds_ld<float>(sm, L::PMX + 32 + 4 * w));
     }
-    const int eP = scale_exp(pm), eA = scale_exp(am);
+    const int eP = __builtin_amdgcn_readfirstlane(scale_exp(pm)), eA = __builtin_amdgcn_readfirstlane(scale_exp(am));
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
         const int id = wave + NW * i;
@@ -712,15 +703,14 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
         kc[mt] = TL::quad(sm + L::K0, mt, wave, q4, l16);
         qc[mt] = TL::quad(sm + L::Q0, mt, wave, q4, l16);
     }
-    const float fq = two(-eO - eS), fy = two(-eY - eS), fx = two(-eU - eD);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
         auto vec4 = [&](int which) { return lds_ld<f32x4>(sm, L::VEC + which * 256 + (16 * mt + 4 * q4) * 4); };
         auto pow2 = [&](int which) { return *reinterpret_cast<const f32x4 *>(vec2 + which * 64 + 16 * mt + 4 * q4); };
         // (the vectors without the rows' powers of two)
         const f32x4 ck = pow2(DeltaRecord::CK);
-        f32x4 dq = aq[mt] * (vec4(DeltaRecord::EQ) * pow2(DeltaRecord::CQ) * fq), y = ay[mt] * (vec4(DeltaRecord::EG) * ck * fy);
-        f32x4 x = au[mt] * (vec4(DeltaRecord::ED) * ck * fx);
+        f32x4 dq = aq[mt] * two(-eO) * two(-eS) * (vec4(DeltaRecord::EQ) * pow2(DeltaRecord::CQ));
+        f32x4 y = ay[mt] * two(-eY) * two(-eS) * (vec4(DeltaRecord::EG) * ck), x = au[mt] * two(-eU) * two(-eD) * (vec4(DeltaRecord::ED) * ck);
         f32x4 si, sy, sx, dk = x - vec4(DeltaRecord::BT) * y;
         // q and k of rows 16 mt + 4 q4 .., column 16 wave + l16
         const f32x4 qv = __builtin_convertvector(__builtin_bit_cast(f16x4, qc[mt]), f32x4) * iq;
@@ -759,8 +749,8 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
                 ak = mfma_f16(pcol(L::DA0 + PB, j), k8, ak);
             }
         }
-        dq += pk * (two(-eP) * ik);
-        dk += pq * (two(-eP) * iq) + ak * (two(-eA) * ik);
+        dq += pk * two(-eP) * ik;
+        dk += pq * two(-eP) * iq + ak * two(-eA) * ik;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             // (rows past the chunk's end lie past the buffers' range)

@@ -225,6 +225,15 @@ __device__ __forceinline__ void st_rows16(char *at, int stride, f32x4 x, int l16
     *reinterpret_cast<uint32_t *>(a + stride) = __builtin_amdgcn_perm(second, first, 0x07060302u);
 }
 
+// The value again, as one the compiler knows nothing of: what is computed
+// from it stays where it is used (the lanes' LDS addresses, held over the
+// whole kernel, would take a quarter more registers than there are).
+__device__ __forceinline__ int fresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Nothing moves across: the sequential passes are latency-bound, and a
 // region's loads are those of the products two regions on.
 __device__ __forceinline__ void region() { __builtin_amdgcn_sched_barrier(0); }

@@ -57,7 +57,7 @@ struct WyLds {
 };
 
 template <int K, int IO, bool L2N>
-__global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
+__global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
 {
     using L = WyLds<K>;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
@@ -99,8 +99,11 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
                         const uint32_t lo = (uint32_t)x[e] & 0x7fffu, hi = (uint32_t)x[e] >> 16 & 0x7fffu;
                         m = max(m, max(lo, hi));
                     }
-#pragma unroll
-                    for (int d = 1; d < K / 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+                    // over the K / 8 lanes of the row
+                    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));   // lane ^ 1
+                    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));   // lane ^ 2
+                    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xf, 0xf, true));  // mirrored in 8
+                    if (K == 128) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xf, 0xf, true));  // in 16
                     return ldexpf(1.0f, scale_exp(__uint_as_float(m << 16)));
                 };
                 const float ck = row_max(a[i]), cq = row_max(b[i]);
@@ -237,9 +240,7 @@ __global__ __launch_bounds__(256) void delta_wy_kernel(DeltaParams p)
     };
     // the waves' largest magnitudes, at vec[448 + 4 which + wave]
     auto put_max = [&](int which, const f32x4 (&x)[4]) {
-        float m = col_max(x);
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        const float m = max16(col_max(x));
         if (lane == 0) vec[448 + 4 * which + wave] = m;
     };
     auto chunk_exp = [&](int which) {
