@@ -440,15 +440,20 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * and conditioning, and the same layouts; g and beta may have any
  * non-negative strides (elements) and need only their element's alignment.
  * opts: state_layout and qk_l2norm as for gdn2_chunk_fwd_opts (NULL:
- * defaults); the chunked entry runs whole sequences and refuses
- * seq_split_chunks > 0 (GDN2_ERR_UNSUPPORTED), the recurrent one ignores it.
+ * defaults); of seq_split_chunks the chunked entry takes 0 (few long
+ * sequences run as parallel segments, joined by their transitions; chosen
+ * from T, N, HV, K and V alone) and -1 (never split), and refuses > 0
+ * (GDN2_ERR_UNSUPPORTED); the recurrent one ignores it.
  * N * HV and (T / 64 + N) * HV may reach 8388607 (GDN2_ERR_SHAPE beyond).
  *
- * Accuracy: every product runs on bf16 MFMA with float32 accumulation and
- * float32 operands taken in two bf16 parts (16 significant bits), the state
- * and all sums in float32. Float32 results (final_state, dg,
- * d_initial_state) are within about 1e-5 of a float64 evaluation, relative
- * in the 2-norm, on unit-norm keys; 16-bit results are rounded once.
+ * Accuracy: products run on fp16 MFMA with float32 accumulation; float32
+ * operands are taken in two fp16 parts next to a power of two of their
+ * column's largest value (22 significant bits), bf16 rows next to one of
+ * their own; the state and all sums are float32. Float32 results
+ * (final_state, dg, d_initial_state) are within about 1e-6 of a float64
+ * evaluation, relative in the 2-norm, on unit-norm keys; 16-bit results are
+ * rounded once (a forward output of bf16 takes the state in one such part, 11
+ * bits next to its 8).
  *
  * Workspace: these entries allocate nothing and keep nothing between calls.
  * The caller passes device memory of at least the number of bytes that the
@@ -464,7 +469,8 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * without the workspace: no HIP call, no device memory.
  */
 
-/* Bytes of workspace of gdn2_delta_chunk_fwd: (T / 64 + N) * HV * 26880. */
+/* Bytes of workspace of gdn2_delta_chunk_fwd: (T / 64 + N) * HV * 26880, and
+ * at most 8 MiB for the segments where few long sequences are split. */
 int64_t gdn2_delta_chunk_fwd_workspace(int64_t T, int32_t N, int32_t HV);
 
 /* The chunked forward. final_state may not alias initial_state. */

@@ -92,6 +92,20 @@ int check_workspace(void *ws, int64_t have, int64_t need, const gdn2_tensor *con
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
+// The forward's workspace: the records, then a split run's segments (the
+// most that any K and V of this T, N and HV take).
+int64_t fwd_records(int64_t T, int64_t N, int64_t HV) { return gdn2::slot_count(T, N) * HV * DeltaRecord::BYTES; }
+int64_t fwd_segments(int64_t T, int64_t N, int64_t HV)
+{
+    int64_t most = 0;
+    for (int64_t K = 64; K <= 128; K += 64)
+        for (int64_t V = 64; V <= 128; V += 64) {
+            const int64_t b = gdn2::delta_segment_bytes(N, HV, K, V, gdn2::delta_segments(T, N, HV, K, V));
+            if (b > most) most = b;
+        }
+    return most;
+}
+
 struct DeltaFwd {
     const gdn2_tensor *q, *k, *v, *g, *beta;
     float scale;
@@ -106,7 +120,7 @@ int validate(const DeltaFwd &a, bool chunked, void *ws, int64_t ws_bytes, DeltaP
     int rc;
     if ((rc = read_options(a.opts, &o))) return rc;
     if (chunked && o.split > 0)
-        return fail(GDN2_ERR_UNSUPPORTED, "seq_split_chunks %d: the scalar-gated rule runs whole sequences", o.split);
+        return fail(GDN2_ERR_UNSUPPORTED, "seq_split_chunks %d: the scalar-gated rule takes 0 (automatic) or -1 (whole sequences)", o.split);
     if (!a.q) return fail(GDN2_ERR_NULL_ARG, "q is NULL");
     if (!a.k) return fail(GDN2_ERR_NULL_ARG, "k is NULL");
     if (!a.v) return fail(GDN2_ERR_NULL_ARG, "v is NULL");
@@ -180,6 +194,8 @@ int validate(const DeltaFwd &a, bool chunked, void *ws, int64_t ws_bytes, DeltaP
     p->nslots = (int32_t)gdn2::slot_count(T, N);
     p->rec = static_cast<char *>(ws);
     p->low_p = p->io == gdn2::IO_F16;
+    p->nseg = chunked && o.split == 0 && T > 0 ? gdn2::delta_segments(T, N, HV, K, V) : 1;
+    p->seg = p->nseg > 1 ? reinterpret_cast<float *>(p->rec + fwd_records(T, N, HV)) : nullptr;
     return GDN2_OK;
 }
 
@@ -295,6 +311,7 @@ int validate(const DeltaBwd &a, void *ws, int64_t ws_bytes, DeltaParams *p)
     char *b = static_cast<char *>(ws);
     p->rec = b + w.rec;
     p->low_p = 1;
+    p->nseg = 1;
     p->s_ck = reinterpret_cast<float *>(b + w.s);
     p->ds_ck = reinterpret_cast<float *>(b + w.ds);
     p->u_ck = reinterpret_cast<float *>(b + w.u);
@@ -441,7 +458,7 @@ extern "C" {
 int64_t gdn2_delta_chunk_fwd_workspace(int64_t T, int32_t N, int32_t HV)
 {
     if (T <= 0 || N <= 0 || HV <= 0) return 0;
-    return gdn2::slot_count(T, N) * HV * DeltaRecord::BYTES;
+    return fwd_records(T, N, HV) + fwd_segments(T, N, HV);
 }
 
 int64_t gdn2_delta_chunk_bwd_workspace(int64_t T, int32_t N, int32_t H, int32_t HV, int32_t K, int32_t V)

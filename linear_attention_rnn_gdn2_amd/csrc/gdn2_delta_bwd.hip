@@ -79,10 +79,8 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
     constexpr int KT = K / 16, KS = K / 32;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int nvb = p.V / COLS;
-    int item = blockIdx.x;
-    const int vb = item % nvb;
-    item /= nvb;
-    const int hv = item % p.HV, n = item / p.HV;
+    const Chain chain = chain_of(p, nvb);
+    const int vb = chain.part, hv = chain.hv, n = chain.n;
     const int hk = hv / (p.HV / p.H);
     const SeqRange rng = seq_of(p, n);
     const int64_t nch = chunks_of(rng);

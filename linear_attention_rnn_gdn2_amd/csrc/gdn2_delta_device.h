@@ -248,5 +248,43 @@ __device__ __forceinline__ float sum16(float x)
     return x;
 }
 
+// The chain (sequence, value head) of a workgroup of the sequential passes
+// and which of the chain's `per` workgroups it is. The workgroups that read the same tiles of k and q
+// (or of one chain) run on one XCD, whose L2 they share (consecutive
+// workgroups go to the 8 XCDs in turn), where that leaves every XCD the same
+// number; up to 64 sequences start longest first, so that with more chains
+// than compute units the short ones fill the end.
+struct Chain {
+    int part, hv, n;
+};
+__device__ __forceinline__ Chain chain_of(const DeltaParams &p, int per)
+{
+    const unsigned b = blockIdx.x;
+    const int rep = p.HV / p.H, same = per * rep, pairs = p.N * p.H;
+    int u, pair;
+    if (pairs % 8 == 0) {
+        u = (int)(b / 8 % (unsigned)same);
+        pair = (int)(b / 8 / (unsigned)same * 8 + b % 8);
+    } else {
+        u = (int)(b % (unsigned)same);
+        pair = (int)(b / (unsigned)same);
+    }
+    int n = pair / p.H;
+    if (p.N > 1 && p.N <= 64) {
+        const int lane = threadIdx.x & 63;
+        int len = -1, rank = 0;
+        if (lane < p.N) {
+            const SeqRange r = seq_of(p, lane);
+            len = (int)chunks_of(r);
+        }
+        for (int j = 0; j < p.N; ++j) {
+            const int x = __builtin_amdgcn_readlane(len, j);
+            rank += x > len || (x == len && j < lane);
+        }
+        n = __builtin_ctzll(__ballot(lane < p.N && rank == n));
+    }
+    return Chain{u % per, pair % p.H * rep + u / per, n};
+}
+
 }  // namespace dev
 }  // namespace gdn2

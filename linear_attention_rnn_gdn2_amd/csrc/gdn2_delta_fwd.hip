@@ -344,24 +344,43 @@ struct StateLds {
     static constexpr int SIZE = 2 * HALF;
 };
 
-template <int K, int IO, int NC, bool CKPT>
+// MODE: outputs; the backward's checkpoints (CKPT); a split run's segments
+// from zero, their end states and transitions (SEG, the K columns of the
+// transition after the V of the state); its outputs, each segment entered
+// with the joined state (JOIN).
+enum { OUT, CKPTS, SEG, JOIN };
+
+template <int K, int IO, int NC, int MODE>
 __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams p)
 {
     constexpr int COLS = 16 * NC;
+    constexpr bool CKPT = MODE == CKPTS || MODE == SEG;  // (no outputs)
     using L = StateLds<K, IO, COLS, CKPT>;
     using TL = Tile<K>;
     constexpr int KT = K / 16, KS = K / 32;
     constexpr bool AHEAD = NC < 8;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int nvb = p.V / COLS;
-    int item = blockIdx.x;
-    const int vb = item % nvb;
-    item /= nvb;
-    const int hv = item % p.HV, n = item / p.HV;
+    const int blocks = MODE == SEG ? nvb + K / COLS : nvb;
+    const int nseg = MODE == SEG ? p.nseg - 1 : MODE == JOIN ? p.nseg : 1;
+    const Chain chain = chain_of(p, blocks * nseg);
+    const int hv = chain.hv, n = chain.n, seg = chain.part / blocks, vb = chain.part % blocks;
+    const bool transition = MODE == SEG && vb >= nvb;
+    if (transition && seg == 0) return;  // (entered with the known initial state)
     const int hk = hv / (p.HV / p.H);
-    const SeqRange rng = seq_of(p, n);
-    const int64_t nch = chunks_of(rng);
-    const int64_t slot0 = chunk_slot(rng.b, n, 0);
+    SeqRange rng = seq_of(p, n);
+    int64_t nch = chunks_of(rng);
+    int64_t slot0 = chunk_slot(rng.b, n, 0);
+    if constexpr (MODE == SEG || MODE == JOIN) {
+        const int64_t per = (nch + p.nseg - 1) / p.nseg, c0 = seg * per < nch ? seg * per : nch;
+        nch = nch - c0 < per ? nch - c0 : per;
+        slot0 += c0;
+        rng.b += c0 * CHUNK;
+        if (rng.e > rng.b + nch * CHUNK) rng.e = rng.b + nch * CHUNK;
+    }
+    // where a split run keeps segment s of this chain
+    const int64_t seg_size = (int64_t)K * p.V + K * K;
+    float *segs = (MODE == SEG || MODE == JOIN) ? p.seg + ((int64_t)n * p.HV + hv) * (p.nseg - 1) * seg_size : nullptr;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 
     if (wave >= NC) {
@@ -378,7 +397,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
             const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
             const __amdgpu_buffer_rsrc_t rq = buf_rsrc(p.q + t0 * p.sq + hk * p.hsq, (int)(((len - 1) * p.sq + K) * 2));
-            const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, (int)(((len - 1) * p.sv + p.V) * 2));
+            const __amdgpu_buffer_rsrc_t rv = buf_rsrc(p.v + t0 * p.sv + hv * p.hsv, transition ? 0 : (int)(((len - 1) * p.sv + p.V) * 2));
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
                 const int ci = t + TH * i, row = ci / (K / 8), cc = ci % (K / 8);
@@ -466,7 +485,9 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            S[i][e] = p.h0 ? state_ld(p.h0, p.h0_bf16, shead + (state_row(i, q4) + e) * sr + col * sc) : 0.0f;
+            S[i][e] = transition ? (state_row(i, q4) + e == col - p.V ? 1.0f : 0.0f)
+                      : seg > 0  ? (MODE == JOIN ? segs[(seg - 1) * seg_size + (state_row(i, q4) + e) * (int64_t)p.V + col] : 0.0f)
+                      : p.h0     ? state_ld(p.h0, p.h0_bf16, shead + (state_row(i, q4) + e) * sr + col * sc) : 0.0f;
     constexpr int OP = IO == IO_BF16 ? 1 : 2;  // parts of what only the outputs need
     RightOp<KS> So;
     So.set(S);
@@ -542,7 +563,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 
         // K S
         early([&] { rows(KL, 0, a0), rows(KL, 1, a1); });
-        if constexpr (CKPT) {
+        if constexpr (MODE == CKPTS) {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.s_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = S[i];
@@ -634,11 +655,11 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             f32x4 W[4];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                if constexpr (CKPT) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
+                if constexpr (MODE == CKPTS) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
                 W[mt] = U[mt] * ed[mt];
             }
             Wo.set(W);
-            if constexpr (CKPT) {
+            if constexpr (MODE == CKPTS) {
                 const f32x4 m = {max16(smax), max16(col_max(U)), max16(col_max(v)), 0.0f};
                 if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8) = m;
             }
@@ -682,11 +703,66 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
         }
         __syncthreads();
     }
-    if (p.ht)
+    if constexpr (MODE == SEG) {
+        float *dst = segs + seg * seg_size + (transition ? (int64_t)K * p.V + col - p.V : col);
+        const int64_t row = transition ? K : p.V;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[(state_row(i, q4) + e) * row] = S[i][e];
+    } else if (p.ht && seg == nseg - 1)
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) state_st(p.ht, p.ht_bf16, shead + (state_row(i, q4) + e) * sr + col * sc, S[i][e]);
+}
+
+// A split run's segments joined: end state s <- end state s + transition s
+// times end state s - 1, one after the other, in float32 (16x16x4 MFMA).
+// Columns are independent: a workgroup takes 16 of a chain's, a wave 16 of
+// the rows; the state passes between the waves through LDS, transposed, so
+// that four rows of a column are one read. A step's wait is the transition
+// (64 KiB a chain), which is loaded a step ahead.
+template <int K>
+__global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
+{
+    constexpr int KT = K / 16, RS = K + 4;
+    __shared__ __attribute__((aligned(16))) float sm[2][16 * RS];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q4 = lane >> 4, l16 = lane & 15;
+    const int col = (int)(blockIdx.x % (unsigned)(p.V / 16)) * 16 + l16, row = 16 * wave + 4 * q4;
+    const int64_t size = (int64_t)K * p.V + K * K;
+    float *end = p.seg + (int64_t)(blockIdx.x / (unsigned)(p.V / 16)) * (p.nseg - 1) * size;
+    auto load = [&](const float *at) {
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = at[(row + e) * (int64_t)p.V + col];
+        return x;
+    };
+    auto fetch = [&](const float *at, f32x4 (&m)[KT]) {
+        const float *tr = at + (int64_t)K * p.V + (16 * wave + l16) * K + 4 * q4;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) m[i] = *reinterpret_cast<const f32x4 *>(tr + 16 * i);
+    };
+    f32x4 x = load(end), m[KT], ahead[KT];
+    *reinterpret_cast<f32x4 *>(&sm[0][l16 * RS + row]) = x;
+    if (p.nseg > 2) fetch(end + size, m);
+    for (int s = 1; s < p.nseg - 1; ++s) {
+        float *at = end + s * size;
+        x = load(at);
+        if (s + 1 < p.nseg - 1) fetch(at + size, ahead);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(&sm[(s - 1) & 1][l16 * RS + 16 * i + 4 * q4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_16x16x4f32(m[i][e], b[e], x, 0, 0, 0);
+        }
+        *reinterpret_cast<f32x4 *>(&sm[s & 1][l16 * RS + row]) = x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[(row + e) * (int64_t)p.V + col] = x[e];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) m[i] = ahead[i];
+    }
 }
 
 template <int K, int IO>
@@ -699,9 +775,19 @@ void launch_wy_l2(const DeltaParams &p, dim3 grid, hipStream_t stream)
 template <int K, int IO, int NC>
 void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / (16 * NC)))), block(64 * (NC + LW));
-    if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, false>), grid, block, 0, stream, p);
+    const int64_t chains = (int64_t)p.N * p.HV;
+    const dim3 grid((unsigned)(chains * (p.V / (16 * NC)))), block(64 * (NC + LW));
+    if constexpr (NC < 8) {
+        if (p.nseg > 1) {
+            const dim3 grid1((unsigned)(chains * ((p.V + p.K) / 64) * (p.nseg - 1)));
+            hipLaunchKernelGGL((delta_state_kernel<K, IO, 4, SEG>), grid1, dim3(64 * (4 + LW)), 0, stream, p);
+            hipLaunchKernelGGL((delta_join_kernel<K>), dim3((unsigned)(chains * (p.V / 16))), dim3(4 * K), 0, stream, p);
+            hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, JOIN>), dim3(grid.x * p.nseg), block, 0, stream, p);
+            return;
+        }
+    }
+    if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, CKPTS>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, OUT>), grid, block, 0, stream, p);
 }
 
 template <int K, int IO>
@@ -730,10 +816,21 @@ hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream)
 
 int delta_columns(const DeltaParams &p, int ncu)
 {
-    const int64_t chains = (int64_t)p.N * p.HV;
+    const int64_t chains = (int64_t)p.N * p.HV * p.nseg;
+    if (p.nseg > 1) return chains * (p.V / 32) <= ncu ? 32 : 64;
     for (int cols = 32; cols < p.V; cols *= 2)
-        if (chains * (p.V / cols) <= ncu) return cols;
+        if (chains * (p.V / cols) <= (cols == 64 ? 2 : 1) * (int64_t)ncu) return cols;
     return p.V;
+}
+
+int delta_segments(int64_t T, int64_t N, int64_t HV, int64_t K, int64_t V)
+{
+    if (T <= 0 || N <= 0 || HV <= 0) return 1;
+    const int64_t chunks = T / CHUNK / N;  // of a sequence of mean length
+    int64_t s = 1 + 256 / (N * HV * ((V + K) / 64));
+    if (s > 32) s = 32;
+    if (s > chunks / 8) s = chunks / 8;
+    return s < 3 ? 1 : (int)s;
 }
 
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream)

@@ -9,6 +9,7 @@ GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -182,7 +183,7 @@ def _prepare(q, k, v, initial_state, cu_seqlens, output_final_state, out, final_
     K = q.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     if out is None:
-        out = torch.empty((T, HV, V), dtype=q.dtype, device=v.device)
+        out = torch.empty_like(v, dtype=q.dtype, memory_format=torch.contiguous_format)
     if final_state is None and output_final_state:
         shape = (N, HV, V, K) if state_layout == "vk" else (N, HV, K, V)
         final_state = torch.empty(shape, dtype=torch.float32, device=v.device)
@@ -342,24 +343,32 @@ class Gdn2QkOptions(ctypes.Structure):
 def _describe_all(tensors):
     """The descriptors of a call's tensors in one buffer: (buffer, the
     address of each, None for None). A decode step is launch-bound, so the
-    descriptors are packed rather than built field by field."""
-    buf = ctypes.create_string_buffer(_DESC.size * len(tensors))
-    base, size, addrs = ctypes.addressof(buf), _DESC.size, []
-    for i, t in enumerate(tensors):
+    descriptors are packed at once rather than built field by field."""
+    vals = []
+    for t in tensors:
         if t is None:
-            addrs.append(None)
+            vals += _NO_DESC
             continue
-        n = t.dim()
+        shape = t.shape
+        n = len(shape)
         if n > 4:
             raise ValueError("at most 4 dimensions")
         pad = _ZEROS[n]
-        _DESC.pack_into(buf, i * size, t.data_ptr() if t.numel() else 0, _DTYPES.get(t.dtype, 0), n,
-                        *t.shape, *pad, *t.stride(), *pad)
-        addrs.append(base + i * size)
-    return buf, addrs
+        vals += (t.data_ptr(), _DTYPES.get(t.dtype, 0), n, *shape, *pad, *t.stride(), *pad)
+    packer = _packer(len(tensors))
+    buf = ctypes.create_string_buffer(packer.size)
+    packer.pack_into(buf, 0, *vals)
+    base = ctypes.addressof(buf)
+    return buf, [None if t is None else base + i * _DESC.size for i, t in enumerate(tensors)]
 
 
 _ZEROS = [(0,) * (4 - n) for n in range(5)]
+_NO_DESC = (0,) * 11
+
+
+@functools.lru_cache(maxsize=None)
+def _packer(n):
+    return struct.Struct("@" + _DESC.format[1:] * n)
 
 
 def _one_device(names, tensors):
@@ -379,11 +388,12 @@ def _one_device(names, tensors):
 
 def _launch(dev, call):
     """call(stream) with `dev` current, on its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream().cuda_stream without its object
     if torch.cuda.current_device() == dev.index:
-        rc = call(torch.cuda.current_stream(dev).cuda_stream)
+        rc = call(stream)
     else:
         with torch.cuda.device(dev):
-            rc = call(torch.cuda.current_stream(dev).cuda_stream)
+            rc = call(stream)
     if rc != 0:
         raise Gdn2Error(rc, last_error())
 
@@ -419,7 +429,7 @@ def _delta_outputs(q, k, v, cu_seqlens, output_final_state, out, final_state, st
     K = q.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     if out is None:
-        out = torch.empty((T, HV, V), dtype=q.dtype, device=v.device)
+        out = torch.empty_like(v, dtype=q.dtype, memory_format=torch.contiguous_format)
     if final_state is None and output_final_state and N >= 1:
         shape = (N, HV, V, K) if state_layout == "vk" else (N, HV, K, V)
         final_state = torch.empty(shape, dtype=torch.float32, device=v.device)
@@ -438,7 +448,7 @@ def delta_chunk_bwd_workspace(T, N, H, HV, K, V):
 
 def delta_chunk_fwd(q, k, v, g=None, beta=None, scale=None, initial_state=None, cu_seqlens=None,
                     output_final_state=True, out=None, final_state=None, state_layout="kv", qk_l2norm=False,
-                    workspace=None):
+                    workspace=None, seq_split=0):
     """The scalar-gated delta rule, chunked, on the current HIP stream.
 
     S = e^g S, u = beta (v - S^T k), S += k u^T, o = scale S^T q, with one g
@@ -448,7 +458,8 @@ def delta_chunk_fwd(q, k, v, g=None, beta=None, scale=None, initial_state=None, 
     states and cu_seqlens, scale, state_layout and qk_l2norm as in
     :func:`chunk_fwd`. Returns (out, final_state or None). ``workspace``: a
     contiguous device tensor of at least ``delta_chunk_fwd_workspace(T, N,
-    HV)`` bytes (None: taken from torch's allocator).
+    HV)`` bytes (None: taken from torch's allocator). ``seq_split``: 0 lets
+    few long sequences run as parallel segments, -1 walks each whole.
     """
     lib = load_library()
     tensors = [q, k, v, g, beta, initial_state, cu_seqlens, out, final_state]
@@ -457,8 +468,8 @@ def delta_chunk_fwd(q, k, v, g=None, beta=None, scale=None, initial_state=None, 
     ws = _workspace(lib.gdn2_delta_chunk_fwd_workspace(v.shape[0], N, v.shape[1]), workspace, dev)
     keep, d = _describe_all([q, k, v, g, beta, initial_state, cu_seqlens, out, final_state])
     opts = None
-    if state_layout != "kv" or qk_l2norm:
-        opts = make_options(0, state_layout, qk_l2norm)
+    if state_layout != "kv" or qk_l2norm or seq_split:
+        opts = make_options(seq_split, state_layout, qk_l2norm)
     _launch(dev, lambda stream: lib.gdn2_delta_chunk_fwd(*d[:5], _scale_arg(scale), *d[5:],
                                                          None if opts is None else ctypes.addressof(opts),
                                                          *_ws_args(ws), stream))
@@ -580,9 +591,9 @@ def qk_norm_rope(q, k, norm="l2", eps=None, q_weight=None, k_weight=None, rope=N
     lib = load_library()
     dev = _one_device(_QK_NAMES, [q, k, q_weight, k_weight, rope, positions, q_out, k_out])
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     keep, d = _describe_all([q, k, q_weight, k_weight, rope, positions, q_out, k_out])
     opts = _qk_options(norm, eps, interleaved)
     _launch(dev, lambda stream: lib.gdn2_qk_norm_rope_fwd(*d, ctypes.addressof(opts), stream))
@@ -606,7 +617,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, norm="l2", eps=None, q_weight=None, k
     _rank3(q=q, k=k)
     for n, t in (("dq", q), ("dk", k), ("dq_weight", q_weight), ("dk_weight", k_weight)):
         if out.get(n) is None:
-            out[n] = None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+            out[n] = None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
     dw = out["dq_weight"] is not None or out["dk_weight"] is not None
     nbytes = lib.gdn2_qk_norm_rope_bwd_workspace(q.shape[0], q.shape[1], k.shape[1], q.shape[2]) if dw else 0
     ws = _workspace(nbytes, workspace, dev)

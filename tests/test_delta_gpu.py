@@ -390,3 +390,26 @@ def test_many_short_sequences(lib):
     for recurrent in (False, True):
         check_fwd("short", fwd(lib, d, recurrent), ref)
     check_grads("short", grads(lib, d), backward64(d))
+
+
+@pytest.mark.parametrize("lens,H,HV,K,V,io,beta_max", [
+    ([2400], 1, 1, 64, 64, BF16, 2.0),
+    ([2304], 2, 4, 128, 128, BF16, 1.0),
+    ([2500], 3, 3, 128, 64, F16, 1.0),
+    ([9000, 0, 37, 600], 1, 2, 64, 128, BF16, 1.0),
+    ([7001], 8, 8, 128, 128, BF16, 2.0),
+])
+def test_split_run(lib, lens, H, HV, K, V, io, beta_max):
+    """Few long sequences run as parallel segments: the reference's results, with empty segments, short
+    neighbours and V-major states, and whole-sequence runs' within both runs' errors."""
+    assert lib.delta_chunk_fwd_workspace(sum(lens), len(lens), HV) > (sum(lens) // 64 + len(lens)) * HV * 26880, "not split"
+    d = make(lens, H, HV, K, V, seed=31, io=io, beta_max=beta_max)
+    got = fwd(lib, d, False)
+    check_fwd("split", got, forward64(d))
+    whole = fwd(lib, d, False, seq_split=-1)
+    close("state against a whole run's", got[1], whole[1].double().cpu(), 2 * F32_REL)
+    vk = dict(d, initial_state=d["initial_state"].transpose(2, 3).contiguous())
+    flip = fwd(lib, vk, False, state_layout="vk")
+    assert torch.equal(flip[0], got[0]) and torch.equal(flip[1].transpose(2, 3), got[1])
+    none = dict(d, initial_state=None)
+    check_fwd("no initial state", fwd(lib, none, False), forward64(none))
