@@ -129,7 +129,7 @@ hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream);
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream);
 hipError_t launch_delta_bwd_grad(const DeltaParams &p, hipStream_t stream);
-hipError_t launch_delta_step(const DeltaParams &p, int ncu, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_qk_fwd(const QkParams &p, hipStream_t stream);
 hipError_t launch_qk_bwd(const QkParams &p, hipStream_t stream);
 // Workgroups of the q/k backward (each leaves one row of partial weight gradients).

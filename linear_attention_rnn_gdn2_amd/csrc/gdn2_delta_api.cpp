@@ -498,7 +498,7 @@ int gdn2_delta_recurrent_fwd(const gdn2_tensor *q, const gdn2_tensor *k, const g
     DeltaParams p;
     if (int rc = validate(DeltaFwd{q, k, v, g, beta, scale, initial_state, cu_seqlens, out, final_state, opts}, false, nullptr, 0, &p))
         return rc;
-    return launched(gdn2::launch_delta_step(p, current_cus(), stream));
+    return launched(gdn2::launch_delta_step(p, stream));
 }
 
 int gdn2_delta_recurrent_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k, const gdn2_tensor *v, const gdn2_tensor *g,

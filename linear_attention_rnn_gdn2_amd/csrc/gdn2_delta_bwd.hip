@@ -35,6 +35,9 @@ using namespace dev;
 // As the forward's sequential pass: NC computing waves of 16 value columns
 // each, 4 staging waves. T and P are used transposed, through transpose reads
 // of their planes, which are staged row-major for that (PlaneTile).
+// Bound by HBM with many chains: 190 KiB per item, of which dS and dY, 96 KiB,
+// are left for the gradients (8 sequences, 37,517 tokens, 32 heads: 785 us,
+// 4.6 TB/s; the checkpoints of the forward's pass, 140 KiB per item, 530 us).
 constexpr int LW = 4;  // staging waves
 
 // A record's plane, row-major: columns 0 .. 31 of all rows, then columns
@@ -322,7 +325,9 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 // fp16 parts under one power of two per operand and chunk (the sequential
 // passes leave the largest magnitudes). Two workgroups share a compute unit
 // and hide each other's loads; one with the next block's loads in registers
-// was slower (1.75 against 1.35 ms on 8 sequences, 37,517 tokens, 32 heads).
+// was slower (1.75 against 1.35 ms on 8 sequences, 37,517 tokens, 32 heads;
+// 1.5 ms with the second fp16 parts). Bound by HBM, 290 KiB per item at
+// 3.8 TB/s, and by the loads' latency in what is left of the copy rate.
 
 // 32 rows (v) of C 16-bit values, written 8 bytes at a time down 16 rows and
 // read transposed from 4 rows and the 4 rows 8 further on: pieces of 16 bytes
@@ -469,38 +474,37 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
         // fragments of 32 value columns: 2 (D / 16) 64 of S and dS, 512 of U and dY
         constexpr int SPT = 2 * (D / 16) * 64 / NT;  // 2
         constexpr int UPT = 512 / NT;                // 1 (D = 128), 2 (D = 64)
-        // (in two batches, which keeps the registers within the bound)
+        // (dY and V follow once S has left its registers: all at once is no faster, after the stores 5% slower)
         {
-            f32x4 fs[SPT], fu[UPT];
-            i32x4 fo = {};
+            f32x4 fs[SPT], fd[SPT], fu[UPT], fy[UPT];
+            i32x4 fo = {}, fv = {};
 #pragma unroll
             for (int i = 0; i < SPT; ++i) fs[i] = buf_ld16<f32x4>(s_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
+#pragma unroll
+            for (int i = 0; i < SPT; ++i) fd[i] = buf_ld16<f32x4>(ds_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
 #pragma unroll
             for (int i = 0; i < UPT; ++i) fu[i] = buf_ld16<f32x4>(u_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
             const uint32_t off = (uint32_t)((t >> 2) * (int)p.sv + vb * 32 + (t & 3) * 8) * 2;
             if (t < 256) fo = buf_ld16<i32x4>(ro, off);
-            f32x4 fd[SPT];
-#pragma unroll
-            for (int i = 0; i < SPT; ++i) fd[i] = buf_ld16<f32x4>(ds_ck, 16 * (uint32_t)(vb * 2 * (D / 16) * 64 + t + NT * i));
             if (vb > 0) __syncthreads();  // the block before is done with
-#pragma unroll
-            for (int i = 0; i < SPT; ++i) st_frag(L::S0, L::SP, ValueTile<D>{}, fs[i], two(eS), t + NT * i, D / 16, true);
-#pragma unroll
-            for (int i = 0; i < UPT; ++i) st_frag(L::U0, L::VP, ValueTile<64>{}, fu[i], two(eU), t + NT * i, 4, false);
-            if (t < 256) lds_st(sm, L::O0 + token_piece(t >> 2, t & 3), row_f16<IO>(fo, two(eO)));
 #pragma unroll
             for (int i = 0; i < SPT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dot = fmaf(fs[i][e], fd[i][e], dot);
+#pragma unroll
+            for (int i = 0; i < SPT; ++i) st_frag(L::S0, L::SP, ValueTile<D>{}, fs[i], two(eS), t + NT * i, D / 16, true);
             region();
 #pragma unroll
-            for (int i = 0; i < UPT; ++i) fu[i] = buf_ld16<f32x4>(y_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
-            if (t < 256) fo = buf_ld16<i32x4>(rv, off);
+            for (int i = 0; i < UPT; ++i) fy[i] = buf_ld16<f32x4>(y_ck, 16 * (uint32_t)(vb * 512 + t + NT * i));
+            if (t < 256) fv = buf_ld16<i32x4>(rv, off);
 #pragma unroll
             for (int i = 0; i < SPT; ++i) st_frag(L::DS0, L::SP, ValueTile<D>{}, fd[i], two(eD), t + NT * i, D / 16, true);
 #pragma unroll
-            for (int i = 0; i < UPT; ++i) st_frag(L::Y0, L::VP, ValueTile<64>{}, fu[i], two(eY), t + NT * i, 4, false);
-            if (t < 256) lds_st(sm, L::VT0 + token_piece(t >> 2, t & 3), row_f16<IO>(fo, two(eV)));
+            for (int i = 0; i < UPT; ++i) st_frag(L::U0, L::VP, ValueTile<64>{}, fu[i], two(eU), t + NT * i, 4, false);
+            if (t < 256) lds_st(sm, L::O0 + token_piece(t >> 2, t & 3), row_f16<IO>(fo, two(eO)));
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) st_frag(L::Y0, L::VP, ValueTile<64>{}, fy[i], two(eY), t + NT * i, 4, false);
+            if (t < 256) lds_st(sm, L::VT0 + token_piece(t >> 2, t & 3), row_f16<IO>(fv, two(eV)));
         }
         __syncthreads();
         again();

@@ -1,4 +1,4 @@
-// Device helpers of the scalar-gated delta rule's kernels: two-part bf16
+// Device helpers of the scalar-gated delta rule's kernels: two-part fp16
 // operands, staged tiles and MFMA fragments. Not part of the ABI.
 //
 // Precision. The sequential passes run on fp16 MFMA with float32 accumulation
@@ -249,11 +249,11 @@ __device__ __forceinline__ float sum16(float x)
 }
 
 // The chain (sequence, value head) of a workgroup of the sequential passes
-// and which of the chain's `per` workgroups it is. The workgroups that read the same tiles of k and q
-// (or of one chain) run on one XCD, whose L2 they share (consecutive
+// and which of the chain's `per` workgroups it is. The workgroups that read
+// the same tiles of k and q run on one XCD, whose L2 they share (consecutive
 // workgroups go to the 8 XCDs in turn), where that leaves every XCD the same
-// number; up to 64 sequences start longest first, so that with more chains
-// than compute units the short ones fill the end.
+// number of them; up to 64 sequences start longest first, so that with more
+// workgroups than compute units the short ones fill the end.
 struct Chain {
     int part, hv, n;
 };

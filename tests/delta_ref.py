@@ -8,24 +8,27 @@ the channels' dbeta plus the sum of dw.
 
 Tolerances. A value rounded once to a 16-bit type is off by at most
 finfo.eps / 2 relative. Before that rounding, the kernels' products take
-float32 operands in two bf16 parts: each part leaves out at most 2^-18 of its
-operand, and the product of the two low parts, 2^-18 of the product, is
-dropped, so a product of two such operands is off by up to 3 * 2^-18, and by
-sqrt(3) * 2^-18 = 6.6e-6 in the 2-norm when the errors are independent. Five
-products follow each other from the inputs to a float32 result: sqrt(5) *
-6.6e-6 = 1.5e-5, and F32_REL = 2e-5 is asked. dg multiplies two such chains
-(S and dS): 2^0.5 times that, DG_REL = 3e-5. On single elements the same
-error is relative to the sum of the terms' magnitudes, about sqrt(128) times
-a typical value: ELEMENT = 5 * 3 * 2^-18 * sqrt(128) = 6.5e-4 of the largest
-value.
+float32 operands in two fp16 parts, each cut off below its 11 bits: a part
+leaves out at most 2^-10 of what it stands for, the pair 2^-20 of the operand,
+and the product of the two low parts, 2^-20 of the product, is dropped. A
+product of two such operands is off by up to 3 * 2^-20, and by sqrt(3) * 2^-20
+in the 2-norm when the errors are independent. Five products follow each
+other from the inputs to a float32 result: sqrt(15) * 2^-20 = 3.7e-6, and
+F32_REL = 4e-6 is asked. dg multiplies two such chains (S and dS): 2^0.5 times
+that, DG_REL = 6e-6. On single elements the same error is relative to the sum
+of the terms' magnitudes, about sqrt(128) times a typical value: ELEMENT = 5 *
+3 * 2^-20 * sqrt(128) = 1.6e-4 of the largest value. A forward output of bf16
+takes the state, P and U in one part rounded to nearest, 2^-12 of each: up to
+2^-11 = 4.9e-4 of the largest value more, ELEMENT16 = 6.5e-4.
 """
 
 import numpy as np
 import torch
 
-F32_REL = 2e-5
-DG_REL = 3e-5
-ELEMENT = 6.5e-4
+F32_REL = 4e-6
+DG_REL = 6e-6
+ELEMENT = 1.6e-4
+ELEMENT16 = 6.5e-4
 
 
 def make(lens, H, HV, K, V, seed, io=torch.bfloat16, gtype=torch.float32, init=True, beta_max=2.0, strong=False):
@@ -79,8 +82,10 @@ def backward64(d, scale=None):
 
 
 def close(tag, x, ref, rel):
-    """x against the float64 reference: `rel` in the 2-norm and ELEMENT on
-    single elements, plus half a step of x's type where it has 16 bits."""
+    """x against the float64 reference: `rel` in the 2-norm and ELEMENT (of a
+    bf16 result ELEMENT16) on single elements, plus half a step of x's type
+    where it has 16 bits."""
+    element = ELEMENT16 if x.dtype == torch.bfloat16 else ELEMENT
     half = torch.finfo(x.dtype).eps / 2 if x.dtype != torch.float32 else 0.0
     a, r = x.detach().cpu().double().numpy(), np.asarray(ref, dtype=np.float64)
     assert a.shape == r.shape, f"{tag}: {a.shape} {r.shape}"
@@ -91,4 +96,4 @@ def close(tag, x, ref, rel):
     got = np.linalg.norm(err) / norm if norm > 0 else np.linalg.norm(err)
     worst = (err - half * np.abs(r)).max() / max(np.abs(r).max(), 1e-30)
     print(f"{tag}: rel-L2 {got:.2e} (allowed {rel + half:.2e}), element {worst:.2e}", flush=True)
-    assert got <= rel + half and worst <= ELEMENT, f"{tag}: rel-L2 {got:.3e}, element {worst:.3e}"
+    assert got <= rel + half and worst <= element, f"{tag}: rel-L2 {got:.3e}, element {worst:.3e}"
