@@ -16,8 +16,9 @@ using gdn2::DeltaParams;
 using gdn2::DeltaRecord;
 using gdn2::QkParams;
 
-// One kernel launch holds up to 2^32 - 1 threads: 512 per (chunk, value head).
-constexpr int64_t kMaxItems = UINT32_MAX / 512;
+// One kernel launch holds up to 2^32 - 1 threads: 512 per (chunk, value head)
+// and 768 per (sequence, value head).
+constexpr int64_t kMaxItems = UINT32_MAX / 768;
 
 int check_io(const gdn2_tensor *t, const char *name, int32_t io, const int64_t *want, Layout layout)
 {

@@ -252,3 +252,23 @@ def test_host_tensors_are_refused(gdn2):
     b = bwd_case()
     with pytest.raises(ValueError):
         gdn2.delta_chunk_bwd(**b)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_chain_limit(gdn2, recurrent):
+    """768 threads per (sequence, value head): 5592405 chains are one launch, one more is refused."""
+    c = dict(case(T=64, H=1, HV=1), initial_state=None, final_state=None)
+    for n, want in ((5592405 - 1, "OK"), (5592406, "SHAPE")):
+        c["cu_seqlens"] = torch.zeros(n + 1, dtype=torch.int32)
+        assert status(gdn2, **c, recurrent=recurrent) == want
+
+
+def test_split_workspace(gdn2):
+    """Segments are added where few long sequences are split, 8 MiB at most, and nowhere else."""
+    def more(T, N, HV):
+        return gdn2.delta_chunk_fwd_workspace(T, N, HV) - (T // 64 + N) * HV * 26880
+    assert more(4096, 1, 16) == 4 * 16 * 131072 and more(37517, 8, 32) == 0 and more(1000, 1, 1) == 0
+    for T in (1536, 2304, 5000, 40000, 1 << 20):
+        for N in (1, 2, 3, 8):
+            for HV in range(1, 70):
+                assert 0 <= more(T, N, HV) <= 8 << 20
