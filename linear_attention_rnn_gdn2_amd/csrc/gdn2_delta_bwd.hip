@@ -853,6 +853,37 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
     }
 }
 
+// dq, dk of a q/k head with several value heads: the sums over them, in their
+// order, of the sequences' tokens (what lies behind the last one is left as
+// it is). Eight columns per thread.
+template <int IO>
+__global__ __launch_bounds__(256) void delta_bwd_reduce_kernel(DeltaParams p)
+{
+    const int m = p.HV / p.H, pieces = p.K / 8;
+    const int64_t b = seq_of(p, 0).b, e = seq_of(p, p.N - 1).e, total = (e - b) * p.H * pieces;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / pieces + b * p.H;  // (token, q/k head): its value heads' rows follow each other
+        const int c = (int)(i % pieces) * 8;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const float *src = (w ? p.dk_ws : p.dq_ws) + row * m * p.K + c;
+            f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+            for (int j = 0; j < m; ++j) {
+                lo += *reinterpret_cast<const f32x4 *>(src + (int64_t)j * p.K);
+                hi += *reinterpret_cast<const f32x4 *>(src + (int64_t)j * p.K + 4);
+            }
+            uint16_t *dst = (w ? p.dk : p.dq) + row * p.K + c;
+            u32x2 a, d;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                a[x] = (uint32_t)f32_io<IO>(lo[2 * x]) | (uint32_t)f32_io<IO>(lo[2 * x + 1]) << 16;
+                d[x] = (uint32_t)f32_io<IO>(hi[2 * x]) | (uint32_t)f32_io<IO>(hi[2 * x + 1]) << 16;
+            }
+            *reinterpret_cast<i32x4 *>(dst) = i32x4{(int)a[0], (int)a[1], (int)d[0], (int)d[1]};
+        }
+    }
+}
+
 }  // namespace
 
 template <int K, int IO>
@@ -895,17 +926,11 @@ hipError_t launch_delta_bwd_grad(const DeltaParams &p, hipStream_t stream)
     }
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (p.H == p.HV) return hipSuccess;
-    BwdParams r{};
-    r.T = p.T;
-    r.H = p.H;
-    r.HV = p.HV;
-    r.K = p.K;
-    r.io = p.io;
-    r.dq_ws = p.dq_ws;
-    r.dk_ws = p.dk_ws;
-    r.dq = p.dq;
-    r.dk = p.dk;
-    return launch_bwd_reduce(r, stream);
+    const int64_t blocks = (p.T * p.H * p.K / 8 + 255) / 256;
+    const dim3 rgrid((unsigned)(blocks < 65536 ? blocks : 65536));
+    if (p.io == IO_F16) hipLaunchKernelGGL((delta_bwd_reduce_kernel<IO_F16>), rgrid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((delta_bwd_reduce_kernel<IO_BF16>), rgrid, dim3(256), 0, stream, p);
+    return hipGetLastError();
 }
 
 }  // namespace gdn2

@@ -530,7 +530,7 @@ def delta_chunk_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_
     HV, V = v.shape[1], v.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     shapes = {"dq": ((T, H, K), q.dtype), "dk": ((T, H, K), q.dtype), "dv": ((T, HV, V), q.dtype),
-              "dg": ((T, HV), g.dtype), "dbeta": ((T, HV), q.dtype),
+              "dg": ((T, HV), torch.float32 if g is None else g.dtype), "dbeta": ((T, HV), q.dtype),
               "d_initial_state": ((N, HV, K, V), torch.float32)}
     for n, (shape, dtype) in shapes.items():
         if out.get(n) is None:

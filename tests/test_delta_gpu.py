@@ -413,3 +413,28 @@ def test_split_run(lib, lens, H, HV, K, V, io, beta_max):
     assert torch.equal(flip[0], got[0]) and torch.equal(flip[1].transpose(2, 3), got[1])
     none = dict(d, initial_state=None)
     check_fwd("no initial state", fwd(lib, none, False), forward64(none))
+
+
+@pytest.mark.parametrize("lens,H,HV,K,recurrent", [
+    ([70, 0, 65], 1, 2, 64, False), ([70, 0, 65], 1, 2, 64, True), ([129, 1], 2, 2, 128, False), ([2400], 1, 2, 64, False)])
+def test_rows_behind_the_last_sequence(lib, lens, H, HV, K, recurrent):
+    """A padded batch: what lies behind the last sequence is neither read (NaN) nor written."""
+    d = make(lens, H, HV, K, K, seed=41, beta_max=1.0)
+    T, pad = sum(lens), 100
+    big = dict(d)
+    for n in ("q", "k", "v", "g", "beta", "d_out"):
+        big[n] = torch.cat([d[n], torch.full((pad,) + d[n].shape[1:], float("nan"), dtype=d[n].dtype)])
+    out = torch.full((T + pad, HV, K), 7.0, device="cuda", dtype=d["v"].dtype)
+    got = fwd(lib, big, recurrent, out=out)
+    assert (out[T:] == 7.0).all()
+    check_fwd("padded", (out[:T], got[1]), forward64(d))
+    if recurrent or T > 1000:
+        return
+    a = on_gpu(big)
+    grads = {n: torch.full_like(a[n[1:]], 7.0) for n in ("dq", "dk", "dv", "dg", "dbeta")}
+    got = lib.delta_chunk_bwd(**a, d_out=big["d_out"].cuda(), d_final_state=d["d_final_state"].cuda(), grads=grads)
+    ref = backward64(d)
+    for n in grads:
+        assert (got[n][T:] == 7.0).all(), n
+        close("padded " + n, got[n][:T], ref[n], DG_REL if n == "dg" else F32_REL)
+    close("padded d_initial_state", got["d_initial_state"], ref["d_initial_state"], F32_REL)
