@@ -438,3 +438,23 @@ def test_rows_behind_the_last_sequence(lib, lens, H, HV, K, recurrent):
         assert (got[n][T:] == 7.0).all(), n
         close("padded " + n, got[n][:T], ref[n], DG_REL if n == "dg" else F32_REL)
     close("padded d_initial_state", got["d_initial_state"], ref["d_initial_state"], F32_REL)
+
+
+@pytest.mark.parametrize("lens,K,recurrent", [([70, 65], 128, False), ([70, 65], 64, True), ([2400], 64, False)])
+@pytest.mark.parametrize("power", [60, -60])
+def test_scales_by_powers_of_two(lib, lens, K, recurrent, power):
+    """The rule is linear in (v, S) and its gradients in (d_out, dS): times a power of two, the same bits."""
+    f = 2.0 ** power
+    d = make(lens, 1, 2, K, K, seed=43, beta_max=1.0)
+    big = dict(d, v=(d["v"].float() * f).to(BF16), initial_state=d["initial_state"] * f)
+    a, b = fwd(lib, d, recurrent), fwd(lib, big, recurrent)
+    for x, y in zip(a, b):
+        assert torch.equal((x.double() * f).to(x.dtype), y)
+    if recurrent:
+        return
+    args = on_gpu(d)
+    c = lib.delta_chunk_bwd(**args, d_out=d["d_out"].cuda(), d_final_state=d["d_final_state"].cuda())
+    e = lib.delta_chunk_bwd(**args, d_out=(d["d_out"].float() * f).to(BF16).cuda(),
+                            d_final_state=(d["d_final_state"] * f).cuda())
+    for n in c:
+        assert torch.equal((c[n].double() * f).to(c[n].dtype), e[n]), n
