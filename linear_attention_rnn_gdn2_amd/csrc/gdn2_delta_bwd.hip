@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
     const Chain chain = chain_of(p, nvb);
     const int vb = chain.part, hv = chain.hv, n = chain.n;
     const int hk = hv / (p.HV / p.H);
-    const SeqRange rng = seq_of(p, n);
+    const SeqRange rng = chain.rng;
     const int64_t nch = chunks_of(rng);
     const int64_t slot0 = chunk_slot(rng.b, n, 0);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -402,10 +402,9 @@ __global__ __launch_bounds__(4 * D, D == 64 ? 2 : 4) void delta_bwd_grad_kernel(
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int hv = (int)(blockIdx.x % (unsigned)p.HV);
     const int64_t slot = blockIdx.x / (unsigned)p.HV;
-    int n;
+    SeqRange rng;
     int64_t c;
-    if (!slot_owner(p.cu, p.cu64, p.T, p.N, slot, &n, &c)) return;
-    const SeqRange rng = seq_of(p, n);
+    if (!chunk_of(p, slot, &rng, &c)) return;
     const int64_t t0 = rng.b + c * CHUNK;
     const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
     const int hk = hv / (p.HV / p.H);

@@ -256,7 +256,13 @@ __device__ __forceinline__ float sum16(float x)
 // workgroups than compute units the short ones fill the end.
 struct Chain {
     int part, hv, n;
+    SeqRange rng;
 };
+// The range that lane i holds (T fits 32 bits).
+__device__ __forceinline__ SeqRange range_of(SeqRange r, int i)
+{
+    return SeqRange{__builtin_amdgcn_readlane((int)r.b, i), __builtin_amdgcn_readlane((int)r.e, i)};
+}
 __device__ __forceinline__ Chain chain_of(const DeltaParams &p, int per)
 {
     const unsigned b = blockIdx.x;
@@ -270,20 +276,42 @@ __device__ __forceinline__ Chain chain_of(const DeltaParams &p, int per)
         pair = (int)(b / (unsigned)same);
     }
     int n = pair / p.H;
+    SeqRange rng;
     if (p.N > 1 && p.N <= 64) {
         const int lane = threadIdx.x & 63;
         int len = -1, rank = 0;
-        if (lane < p.N) {
-            const SeqRange r = seq_of(p, lane);
-            len = (int)chunks_of(r);
-        }
+        const SeqRange r = seq_of(p, lane < p.N ? lane : 0);
+        if (lane < p.N) len = (int)chunks_of(r);
         for (int j = 0; j < p.N; ++j) {
             const int x = __builtin_amdgcn_readlane(len, j);
             rank += x > len || (x == len && j < lane);
         }
         n = __builtin_ctzll(__ballot(lane < p.N && rank == n));
+        rng = range_of(r, n);
+    } else {
+        rng = seq_of(p, n);
     }
-    return Chain{u % per, pair % p.H * rep + u / per, n};
+    return Chain{u % per, pair % p.H * rep + u / per, n, rng};
+}
+
+// The chunk of a checkpoint slot: false where the slot holds none. 64
+// sequences at a time are looked at, so that up to 64 cost one load's wait.
+__device__ __forceinline__ bool chunk_of(const DeltaParams &p, int64_t slot, SeqRange *rng, int64_t *c)
+{
+    const int lane = threadIdx.x & 63;
+    int n = 0, count = p.N, step;
+    do {
+        step = (count + 63) / 64;
+        const int i = lane * step;
+        const SeqRange r = seq_of(p, n + (i < count ? i : 0));
+        const uint64_t m = __ballot(i < count && chunk_slot(r.b, n + i, 0) <= slot);
+        const int k = m ? 63 - __builtin_clzll(m) : 0;
+        *rng = range_of(r, k);
+        n += k * step;
+        count = count - k * step < step ? count - k * step : step;
+    } while (step > 1);
+    *c = slot - chunk_slot(rng->b, n, 0);
+    return *c >= 0 && *c < chunks_of(*rng);
 }
 
 }  // namespace dev

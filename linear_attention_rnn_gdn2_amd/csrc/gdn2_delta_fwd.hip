@@ -66,15 +66,26 @@ __global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int hv = (int)(blockIdx.x % (unsigned)p.HV);
     const int64_t slot = blockIdx.x / (unsigned)p.HV;
-    int n;
+    SeqRange rng;
     int64_t c;
-    if (!slot_owner(p.cu, p.cu64, p.T, p.N, slot, &n, &c)) return;
-    const SeqRange rng = seq_of(p, n);
+    if (!chunk_of(p, slot, &rng, &c)) return;
     const int64_t t0 = rng.b + c * CHUNK;
     const int len = (int)(rng.e - t0 < CHUNK ? rng.e - t0 : CHUNK);
     const int hk = hv / (p.HV / p.H);
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63, q4 = lane >> 4, l16 = lane & 15;
 
+    // the gates first (their wait is then the tiles')
+    float g = 0.0f, bt = 0.0f;
+    if (wave == 0 && lane < len) {
+        const int64_t tok = t0 + lane;
+        if (p.g) {
+            const int64_t o = tok * p.sg + hv * p.hsg;
+            if (p.gtype == G_F32) g = static_cast<const float *>(p.g)[o];
+            else if (p.gtype == G_F16) g = io_f32<IO_F16>(static_cast<const uint16_t *>(p.g)[o]);
+            else g = io_f32<IO_BF16>(static_cast<const uint16_t *>(p.g)[o]);
+        }
+        bt = p.beta ? io_f32<IO>(p.beta[tok * p.sb + hv * p.hsb]) : 1.0f;
+    }
     // the tiles (rows past the chunk's end are zeros by the buffers' range)
     {
         const __amdgpu_buffer_rsrc_t rk = buf_rsrc(p.k + t0 * p.sk + hk * p.hsk, (int)(((len - 1) * p.sk + K) * 2));
@@ -121,21 +132,9 @@ __global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
     char *rec = p.rec + delta_item(p, slot, hv) * (int64_t)DeltaRecord::BYTES;
     float *rvec = reinterpret_cast<float *>(rec + DeltaRecord::VEC);
     double G = 0.0, GC = 0.0;
-    float bt = 0.0f;
     if (wave == 0) {
         // running sum of g in 64 bits: its differences are exponents, and a
         // strongly decayed chunk's sum is far larger than they are
-        float g = 0.0f;
-        if (lane < len) {
-            const int64_t tok = t0 + lane;
-            if (p.g) {
-                const int64_t o = tok * p.sg + hv * p.hsg;
-                if (p.gtype == G_F32) g = static_cast<const float *>(p.g)[o];
-                else if (p.gtype == G_F16) g = io_f32<IO_F16>(static_cast<const uint16_t *>(p.g)[o]);
-                else g = io_f32<IO_BF16>(static_cast<const uint16_t *>(p.g)[o]);
-            }
-            bt = p.beta ? io_f32<IO>(p.beta[tok * p.sb + hv * p.hsb]) : 1.0f;
-        }
         G = (double)g * 1.4426950408889634074;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -376,7 +375,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
     const bool transition = MODE == SEG && vb >= nvb;
     if (transition && seg == 0) return;  // (entered with the known initial state)
     const int hk = hv / (p.HV / p.H);
-    SeqRange rng = seq_of(p, n);
+    SeqRange rng = chain.rng;
     int64_t nch = chunks_of(rng);
     int64_t slot0 = chunk_slot(rng.b, n, 0);
     if constexpr (MODE == SEG || MODE == JOIN) {

@@ -458,3 +458,14 @@ def test_scales_by_powers_of_two(lib, lens, K, recurrent, power):
                             d_final_state=(d["d_final_state"] * f).cuda())
     for n in c:
         assert torch.equal((c[n].double() * f).to(c[n].dtype), e[n]), n
+
+
+def test_hundreds_of_sequences(lib):
+    """Chunks find their sequence among hundreds, empty ones and one of many chunks among them."""
+    lens = [(7 * i) % 5 for i in range(150)] + [0, 0, 300, 64, 65] + [(11 * i) % 90 for i in range(150)]
+    d = make(lens, 1, 2, 64, 64, seed=47, beta_max=1.0)
+    check_fwd("many", fwd(lib, d), forward64(d))
+    got = lib.delta_chunk_bwd(**on_gpu(d), d_out=d["d_out"].cuda(), d_final_state=d["d_final_state"].cuda())
+    ref = backward64(d)
+    for n in ref:
+        close(n, got[n], ref[n], DG_REL if n == "dg" else F32_REL)
