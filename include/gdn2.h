@@ -521,7 +521,8 @@ int gdn2_delta_recurrent_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * zero; d_initial_state NULL: not written). dq, dk (summed over the value
  * heads that read each q/k head), dv and dbeta have q's type, dg g's.
  * Workspace: per (chunk, value head) 26880 + 8 K V + 514 V bytes, plus
- * 8 T HV K with grouped heads (HV > H), each part rounded up to 256 bytes.
+ * 8 T HV K with grouped heads (HV > H), each part rounded up to 256 bytes,
+ * and at most 12 MiB for the segments where few long sequences are split.
  */
 int64_t gdn2_delta_chunk_bwd_workspace(int64_t T, int32_t N, int32_t H,
                                        int32_t HV, int32_t K, int32_t V);

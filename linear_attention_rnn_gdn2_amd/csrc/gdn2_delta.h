@@ -37,10 +37,11 @@ struct DeltaParams {
     // workspace (chunked calls): every chunk's record, DeltaRecord::BYTES per (slot, value head)
     char *rec;
     int32_t low_p;          // the record's low plane of P is used
-    // a forward split along the sequences: segments of every sequence (1: whole sequences), and per (sequence,
-    // value head, segment but the last) its end state from zero [K, V] and its transition [K, K], float32
+    // a run split along the sequences: segments of every sequence (1: whole sequences), and per (sequence, value
+    // head, segment but the last) its end state from zero [K, V] and its transition [K, K], float32; backward: per
+    // segment but the first the gradient that leaves it towards the one before [K, V]
     int32_t nseg;
-    float *seg;
+    float *seg, *rseg;
     // backward only. The checkpoints are in accumulator order: per (slot,
     // value head, 16 value columns) the float32 fragments f32x4[tile][lane]
     // of a wave: lane 16 q4 + l16 holds four rows of column l16, key rows
@@ -113,13 +114,14 @@ struct QkParams {
 // 3191 us, 128 columns 900 and 3414; all of 73 chunks: 675 and 3037, 636 and
 // 3052; 1024 chains of 16 chunks: 629 and 2713, 561 and 2638).
 int delta_columns(const DeltaParams &p, int ncu);
-// Segments of each sequence of a forward call (1: not split), and the bytes
+// Segments of each sequence of a chunked call (1: not split), and the bytes
 // of DeltaParams::seg. A split costs a second walk over every chunk and pays
 // where the compute units would be idle: as many segments as keep the first
 // walk's workgroups (64 columns of the state or of the transition) resident
 // at once, of at least 8 chunks. Measured split / whole: 16 heads of 4096
-// tokens 125 / 179 us, 4 of 32768 237 / 1127, 32 of 8192 291 / 355, 16 of
-// 2304 95 / 111.
+// tokens 125 / 179 us, 4 of 32768 229 / 1127, 32 of 8192 280 / 355, 16 of
+// 2304 89 / 111; gradients 359 / 471, 706 / 2757, 973 / 1057 and 247 / 289 (8
+// heads of 1600 tokens, three segments: 154 / 147).
 int delta_segments(int64_t T, int64_t N, int64_t HV, int64_t K, int64_t V);
 inline int64_t delta_segment_bytes(int64_t N, int64_t HV, int64_t K, int64_t V, int nseg)
 {
@@ -128,6 +130,7 @@ inline int64_t delta_segment_bytes(int64_t N, int64_t HV, int64_t K, int64_t V, 
 hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_state(const DeltaParams &p, bool ckpt, int ncu, hipStream_t stream);
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream);
+hipError_t launch_delta_join_bwd(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_bwd_grad(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_qk_fwd(const QkParams &p, hipStream_t stream);

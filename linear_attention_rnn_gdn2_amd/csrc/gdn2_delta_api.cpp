@@ -208,7 +208,8 @@ struct DeltaBwd {
 
 // Byte offsets of the backward's workspace.
 struct BwdSpace {
-    int64_t rec, s, ds, u, y, mx, dq, dk, total;
+    int64_t rec, s, ds, u, y, mx, dq, dk, seg, rseg, total;
+    int nseg;
     BwdSpace(int64_t T, int64_t N, int64_t H, int64_t HV, int64_t K, int64_t V)
     {
         const int64_t items = gdn2::slot_count(T, N) * HV;
@@ -226,6 +227,9 @@ struct BwdSpace {
         mx = take(T > 0 ? items * (V / 16) * 32 : 0);
         dq = take(H != HV ? T * HV * K * 4 : 0);
         dk = take(H != HV ? T * HV * K * 4 : 0);
+        nseg = gdn2::delta_segments(T, N, HV, K, V);
+        seg = take(gdn2::delta_segment_bytes(N, HV, K, V, nseg));
+        rseg = take(N * HV * (nseg - 1) * K * V * 4);
         total = at;
     }
 };
@@ -312,7 +316,9 @@ int validate(const DeltaBwd &a, void *ws, int64_t ws_bytes, DeltaParams *p)
     char *b = static_cast<char *>(ws);
     p->rec = b + w.rec;
     p->low_p = 1;
-    p->nseg = 1;
+    p->nseg = w.nseg;
+    p->seg = reinterpret_cast<float *>(b + w.seg);
+    p->rseg = reinterpret_cast<float *>(b + w.rseg);
     p->s_ck = reinterpret_cast<float *>(b + w.s);
     p->ds_ck = reinterpret_cast<float *>(b + w.ds);
     p->u_ck = reinterpret_cast<float *>(b + w.u);

@@ -73,7 +73,11 @@ struct BwdStateLds {
     static constexpr int SIZE = 2 * HALF;
 };
 
-template <int K, int IO, int NC>
+// A split run's segments are entered from their ends: SEG walks those but the
+// first, the last from the given gradient and the others from zero, and
+// leaves what comes out of each (rseg); the transition of the gradient over a
+// segment is the state's transposed.
+template <int K, int IO, int NC, int MODE>
 __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaParams p)
 {
     constexpr int COLS = 16 * NC;
@@ -82,12 +86,18 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
     constexpr int KT = K / 16, KS = K / 32;
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int nvb = p.V / COLS;
-    const Chain chain = chain_of(p, nvb);
-    const int vb = chain.part, hv = chain.hv, n = chain.n;
+    const int nseg = MODE == SEG ? p.nseg - 1 : MODE == JOIN ? p.nseg : 1;
+    const Chain chain = chain_of(p, nvb * nseg);
+    const int vb = chain.part % nvb, hv = chain.hv, n = chain.n;
+    const int seg = chain.part / nvb + (MODE == SEG ? 1 : 0);
+    const bool last = MODE == OUT || seg == p.nseg - 1;
     const int hk = hv / (p.HV / p.H);
-    const SeqRange rng = chain.rng;
-    const int64_t nch = chunks_of(rng);
-    const int64_t slot0 = chunk_slot(rng.b, n, 0);
+    SeqRange rng = chain.rng;
+    int64_t nch = chunks_of(rng);
+    int64_t slot0 = chunk_slot(rng.b, n, 0);
+    if constexpr (MODE != OUT) segment_of(p.nseg, seg, rng, nch, slot0);
+    // where a split run keeps what enters segment s - 1 from its end: at s - 1
+    float *rseg = MODE == OUT ? nullptr : p.rseg + ((int64_t)n * p.HV + hv) * (p.nseg - 1) * K * p.V;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 
     if (wave >= NC) {
@@ -174,12 +184,14 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         }
         __syncthreads();
         for (int64_t c = nch - 1; c >= 0; --c) {
-            if (c + 1 < nch) flush(c + 1);
+            if constexpr (MODE != SEG)
+                if (c + 1 < nch) flush(c + 1);
             if (c > 0) stage(sm + ((c - 1) & 1) * L::HALF);
             if (c > 1) fetch(c - 2);
             __syncthreads();
         }
-        if (nch > 0) flush(0);
+        if constexpr (MODE != SEG)
+            if (nch > 0) flush(0);
         return;
     }
 
@@ -190,7 +202,10 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dS[i][e] = p.dht ? p.dht[shead + (int64_t)(state_row(i, q4) + e) * p.V + col] : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            const int64_t o = (int64_t)(state_row(i, q4) + e) * p.V + col;
+            dS[i][e] = !last ? (MODE == JOIN ? rseg[(int64_t)seg * K * p.V + o] : 0.0f) : p.dht ? p.dht[shead + o] : 0.0f;
+        }
     RightOp<KS> So;
     So.set(dS);
     __syncthreads();
@@ -205,7 +220,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         };
         const f32x4 scal = lds_ld<f32x4>(half, L::G0 + DeltaRecord::SCAL - DeltaRecord::VEC);  // e^(G_C), 1 / scales of T and P
         const float gamma = scal[0];
-        {
+        if constexpr (MODE != SEG) {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.ds_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = dS[i];
@@ -265,7 +280,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) Y[mt] *= tinv;
         }
-        {
+        if constexpr (MODE != SEG) {
             const f32x4 m = {max16(smax), max16(col_max(Y)), max16(Oo.mx), 0.0f};
             if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8 + 4) = m;
         }
@@ -297,9 +312,9 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         vec(DeltaRecord::BT, x4);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = Y[mt];
+            if constexpr (MODE != SEG) reinterpret_cast<f32x4 *>(p.y_ck)[frag * 256 + 64 * mt + lane] = Y[mt];
             Y[mt] *= x4[mt];
-            st_rows16<IO>(half + L::O0 + (16 * mt + 4 * q4) * L::OS + 32 * wave, L::OS, Y[mt], l16);
+            if constexpr (MODE != SEG) st_rows16<IO>(half + L::O0 + (16 * mt + 4 * q4) * L::OS + 32 * wave, L::OS, Y[mt], l16);
         }
         vec(DeltaRecord::EG, x4);
 #pragma unroll
@@ -308,11 +323,12 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
         So.set(dS);
         __syncthreads();
     }
-    if (p.dh0)
+    float *dst = MODE == SEG ? rseg + (int64_t)(seg - 1) * K * p.V : p.dh0 && seg == 0 ? p.dh0 + shead : nullptr;
+    if (dst)
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p.dh0[shead + (int64_t)(state_row(i, q4) + e) * p.V + col] = dS[i][e];
+            for (int e = 0; e < 4; ++e) dst[(int64_t)(state_row(i, q4) + e) * p.V + col] = dS[i][e];
 }
 
 // --------------------------------------------------------- all gradients --
@@ -885,31 +901,38 @@ __global__ __launch_bounds__(256) void delta_bwd_reduce_kernel(DeltaParams p)
 
 }  // namespace
 
-template <int K, int IO>
-static void launch_bwd_state_cols(const DeltaParams &p, int cols, hipStream_t stream)
+template <int K, int IO, int NC>
+static hipError_t launch_bwd_state_nc(const DeltaParams &p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / cols)));
-    if (cols == 128) {
-        // (K = V: 128 columns only with 128 key rows)
-        if constexpr (K == 128) hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 8>), grid, dim3(64 * (8 + LW)), 0, stream, p);
-    } else if (cols == 64) {
-        hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 4>), grid, dim3(64 * (4 + LW)), 0, stream, p);
-    } else {
-        hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 2>), grid, dim3(64 * (2 + LW)), 0, stream, p);
+    const int64_t chains = (int64_t)p.N * p.HV;
+    const dim3 grid((unsigned)(chains * (p.V / (16 * NC)) * p.nseg)), block(64 * (NC + LW));
+    if constexpr (NC < 8) {
+        if (p.nseg > 1) {
+            const dim3 grid1((unsigned)(chains * (p.V / 64) * (p.nseg - 1)));
+            hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, 4, SEG>), grid1, dim3(64 * (4 + LW)), 0, stream, p);
+            if (hipError_t e = launch_delta_join_bwd(p, stream); e != hipSuccess) return e;
+            hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, NC, JOIN>), grid, block, 0, stream, p);
+            return hipGetLastError();
+        }
     }
+    hipLaunchKernelGGL((delta_bwd_state_kernel<K, IO, NC, OUT>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int K, int IO>
+static hipError_t launch_bwd_state_cols(const DeltaParams &p, int cols, hipStream_t stream)
+{
+    // (K = V: 128 columns only with 128 key rows)
+    if constexpr (K == 128)
+        if (cols == 128) return launch_bwd_state_nc<K, IO, 8>(p, stream);
+    return cols == 64 ? launch_bwd_state_nc<K, IO, 4>(p, stream) : launch_bwd_state_nc<K, IO, 2>(p, stream);
 }
 
 hipError_t launch_delta_bwd_state(const DeltaParams &p, int ncu, hipStream_t stream)
 {
     const int cols = delta_columns(p, ncu);
-    if (p.K == 128) {
-        if (p.io == IO_F16) launch_bwd_state_cols<128, IO_F16>(p, cols, stream);
-        else launch_bwd_state_cols<128, IO_BF16>(p, cols, stream);
-    } else {
-        if (p.io == IO_F16) launch_bwd_state_cols<64, IO_F16>(p, cols, stream);
-        else launch_bwd_state_cols<64, IO_BF16>(p, cols, stream);
-    }
-    return hipGetLastError();
+    if (p.K == 128) return p.io == IO_F16 ? launch_bwd_state_cols<128, IO_F16>(p, cols, stream) : launch_bwd_state_cols<128, IO_BF16>(p, cols, stream);
+    return p.io == IO_F16 ? launch_bwd_state_cols<64, IO_F16>(p, cols, stream) : launch_bwd_state_cols<64, IO_BF16>(p, cols, stream);
 }
 
 hipError_t launch_delta_bwd_grad(const DeltaParams &p, hipStream_t stream)

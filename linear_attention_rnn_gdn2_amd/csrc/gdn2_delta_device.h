@@ -248,6 +248,12 @@ __device__ __forceinline__ float sum16(float x)
     return x;
 }
 
+// What a sequential pass is for: its results (OUT); the forward's walk for
+// the gradients' checkpoints (CKPTS); a split run's segments from zero (SEG)
+// and its results, each segment entered with the joined state (JOIN, and
+// JOIN_CKPTS for checkpoints).
+enum { OUT, CKPTS, SEG, JOIN, JOIN_CKPTS };
+
 // The chain (sequence, value head) of a workgroup of the sequential passes
 // and which of the chain's `per` workgroups it is. The workgroups that read
 // the same tiles of k and q run on one XCD, whose L2 they share (consecutive
@@ -292,6 +298,16 @@ __device__ __forceinline__ Chain chain_of(const DeltaParams &p, int per)
         rng = seq_of(p, n);
     }
     return Chain{u % per, pair % p.H * rep + u / per, n, rng};
+}
+
+// Of a chain's chunks, those of segment seg of a split run.
+__device__ __forceinline__ void segment_of(int nseg, int seg, SeqRange &rng, int64_t &nch, int64_t &slot0)
+{
+    const int64_t per = (nch + nseg - 1) / nseg, c0 = seg * per < nch ? seg * per : nch;
+    nch = nch - c0 < per ? nch - c0 : per;
+    slot0 += c0;
+    rng.b += c0 * CHUNK;
+    if (rng.e > rng.b + nch * CHUNK) rng.e = rng.b + nch * CHUNK;
 }
 
 // The chunk of a checkpoint slot: false where the slot holds none. 64

@@ -351,17 +351,14 @@ struct StateLds {
     static constexpr int SIZE = 2 * HALF;
 };
 
-// MODE: outputs; the backward's checkpoints (CKPT); a split run's segments
-// from zero, their end states and transitions (SEG, the K columns of the
-// transition after the V of the state); its outputs, each segment entered
-// with the joined state (JOIN).
-enum { OUT, CKPTS, SEG, JOIN };
-
+// (SEG: end states and transitions, the K columns of the transition after the
+// V of the state)
 template <int K, int IO, int NC, int MODE>
 __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams p)
 {
     constexpr int COLS = 16 * NC;
-    constexpr bool CKPT = MODE == CKPTS || MODE == SEG;  // (no outputs)
+    constexpr bool SPLIT = MODE == SEG || MODE == JOIN || MODE == JOIN_CKPTS;
+    constexpr bool STORE = MODE == CKPTS || MODE == JOIN_CKPTS, CKPT = STORE || MODE == SEG;  // (CKPT: no outputs)
     using L = StateLds<K, IO, COLS, CKPT>;
     using TL = Tile<K>;
     constexpr int KT = K / 16, KS = K / 32;
@@ -369,7 +366,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
     __shared__ __attribute__((aligned(16))) char sm[L::SIZE];
     const int nvb = p.V / COLS;
     const int blocks = MODE == SEG ? nvb + K / COLS : nvb;
-    const int nseg = MODE == SEG ? p.nseg - 1 : MODE == JOIN ? p.nseg : 1;
+    const int nseg = !SPLIT ? 1 : MODE == SEG ? p.nseg - 1 : p.nseg;
     const Chain chain = chain_of(p, blocks * nseg);
     const int hv = chain.hv, n = chain.n, seg = chain.part / blocks, vb = chain.part % blocks;
     const bool transition = MODE == SEG && vb >= nvb;
@@ -378,16 +375,10 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
     SeqRange rng = chain.rng;
     int64_t nch = chunks_of(rng);
     int64_t slot0 = chunk_slot(rng.b, n, 0);
-    if constexpr (MODE == SEG || MODE == JOIN) {
-        const int64_t per = (nch + p.nseg - 1) / p.nseg, c0 = seg * per < nch ? seg * per : nch;
-        nch = nch - c0 < per ? nch - c0 : per;
-        slot0 += c0;
-        rng.b += c0 * CHUNK;
-        if (rng.e > rng.b + nch * CHUNK) rng.e = rng.b + nch * CHUNK;
-    }
+    if constexpr (SPLIT) segment_of(p.nseg, seg, rng, nch, slot0);
     // where a split run keeps segment s of this chain
     const int64_t seg_size = (int64_t)K * p.V + K * K;
-    float *segs = (MODE == SEG || MODE == JOIN) ? p.seg + ((int64_t)n * p.HV + hv) * (p.nseg - 1) * seg_size : nullptr;
+    float *segs = SPLIT ? p.seg + ((int64_t)n * p.HV + hv) * (p.nseg - 1) * seg_size : nullptr;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 
     if (wave >= NC) {
@@ -493,7 +484,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[i][e] = transition ? (state_row(i, q4) + e == col - p.V ? 1.0f : 0.0f)
-                      : seg > 0  ? (MODE == JOIN ? segs[(seg - 1) * seg_size + (state_row(i, q4) + e) * (int64_t)p.V + col] : 0.0f)
+                      : seg > 0  ? (MODE != SEG ? segs[(seg - 1) * seg_size + (state_row(i, q4) + e) * (int64_t)p.V + col] : 0.0f)
                       : p.h0     ? state_ld(p.h0, p.h0_bf16, shead + (state_row(i, q4) + e) * sr + col * sc) : 0.0f;
     constexpr int OP = IO == IO_BF16 ? 1 : 2;  // parts of what only the outputs need
     RightOp<KS> So;
@@ -570,7 +561,7 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
 
         // K S
         early([&] { rows(KL, 0, a0), rows(KL, 1, a1); });
-        if constexpr (MODE == CKPTS) {
+        if constexpr (STORE) {
             f32x4 *dst = reinterpret_cast<f32x4 *>(p.s_ck) + frag * (KT * 64) + lane;
 #pragma unroll
             for (int i = 0; i < KT; ++i) dst[64 * i] = S[i];
@@ -662,11 +653,11 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             f32x4 W[4];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                if constexpr (MODE == CKPTS) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
+                if constexpr (STORE) reinterpret_cast<f32x4 *>(p.u_ck)[frag * 256 + 64 * mt + lane] = U[mt];
                 W[mt] = U[mt] * ed[mt];
             }
             Wo.set(W);
-            if constexpr (MODE == CKPTS) {
+            if constexpr (STORE) {
                 const f32x4 m = {max16(smax), max16(col_max(U)), max16(col_max(v)), 0.0f};
                 if (lane == 0) *reinterpret_cast<f32x4 *>(p.mx + frag * 8) = m;
             }
@@ -724,39 +715,54 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_state_kernel(DeltaParams
             for (int e = 0; e < 4; ++e) state_st(p.ht, p.ht_bf16, shead + (state_row(i, q4) + e) * sr + col * sc, S[i][e]);
 }
 
-// A split run's segments joined: end state s <- end state s + transition s
-// times end state s - 1, one after the other, in float32 (16x16x4 MFMA).
-// Columns are independent: a workgroup takes 16 of a chain's, a wave 16 of
-// the rows; the state passes between the waves through LDS, transposed, so
-// that four rows of a column are one read. A step's wait is the transition
-// (64 KiB a chain), which is loaded a step ahead.
-template <int K>
+// A split run's segments joined, one after the other, in float32 (16x16x4
+// MFMA): end state s <- end state s + transition s times end state s - 1, or,
+// of the gradients (BACK), what enters segment s from its end <- that + the
+// transposed transition times what enters segment s + 1 (rseg[s - 1] is
+// segment s's). Columns are independent: a workgroup takes 16 of a chain's, a
+// wave 16 of the rows; the state passes between the waves through LDS,
+// transposed, so that four rows of a column are one read. A step's wait is
+// the transition (64 KiB a chain), which is loaded a step ahead.
+template <int K, bool BACK>
 __global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
 {
     constexpr int KT = K / 16, RS = K + 4;
     __shared__ __attribute__((aligned(16))) float sm[2][16 * RS];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q4 = lane >> 4, l16 = lane & 15;
     const int col = (int)(blockIdx.x % (unsigned)(p.V / 16)) * 16 + l16, row = 16 * wave + 4 * q4;
-    const int64_t size = (int64_t)K * p.V + K * K;
-    float *end = p.seg + (int64_t)(blockIdx.x / (unsigned)(p.V / 16)) * (p.nseg - 1) * size;
-    auto load = [&](const float *at) {
+    const int64_t size = (int64_t)K * p.V + K * K, chain = blockIdx.x / (unsigned)(p.V / 16);
+    const int steps = p.nseg - 2;
+    const float *tr = p.seg + chain * (p.nseg - 1) * size + (int64_t)K * p.V;  // transitions, `size` apart
+    // the states that are joined, in order: end states, or rseg from its last on
+    float *at = BACK ? p.rseg + (chain * (p.nseg - 1) + steps) * K * p.V : p.seg + chain * (p.nseg - 1) * size;
+    const int64_t next = BACK ? -(int64_t)K * p.V : size;
+    auto load = [&](int s) {
         f32x4 x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = at[(row + e) * (int64_t)p.V + col];
+        for (int e = 0; e < 4; ++e) x[e] = at[s * next + (row + e) * (int64_t)p.V + col];
         return x;
     };
-    auto fetch = [&](const float *at, f32x4 (&m)[KT]) {
-        const float *tr = at + (int64_t)K * p.V + (16 * wave + l16) * K + 4 * q4;
+    auto fetch = [&](int s, f32x4 (&m)[KT]) {  // rows 16 wave + l16 of step s's matrix
+        const float *t = tr + (BACK ? p.nseg - 1 - s : s) * size;
 #pragma unroll
-        for (int i = 0; i < KT; ++i) m[i] = *reinterpret_cast<const f32x4 *>(tr + 16 * i);
+        for (int i = 0; i < KT; ++i) {
+            if constexpr (BACK) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[i][e] = t[(16 * i + 4 * q4 + e) * K + 16 * wave + l16];
+            } else {
+                m[i] = *reinterpret_cast<const f32x4 *>(t + (16 * wave + l16) * K + 16 * i + 4 * q4);
+            }
+        }
     };
-    f32x4 x = load(end), m[KT], ahead[KT];
+    f32x4 m[KT], x = load(0), y = load(1);
+    fetch(1, m);
     *reinterpret_cast<f32x4 *>(&sm[0][l16 * RS + row]) = x;
-    if (p.nseg > 2) fetch(end + size, m);
-    for (int s = 1; s < p.nseg - 1; ++s) {
-        float *at = end + s * size;
-        x = load(at);
-        if (s + 1 < p.nseg - 1) fetch(at + size, ahead);
+    for (int s = 1; s <= steps; ++s) {
+        f32x4 ahead[KT];
+        const int s1 = s < steps ? s + 1 : s;
+        x = y;
+        y = load(s1);
+        fetch(s1, ahead);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
@@ -766,7 +772,7 @@ __global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
         }
         *reinterpret_cast<f32x4 *>(&sm[s & 1][l16 * RS + row]) = x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) at[(row + e) * (int64_t)p.V + col] = x[e];
+        for (int e = 0; e < 4; ++e) at[s * next + (row + e) * (int64_t)p.V + col] = x[e];
 #pragma unroll
         for (int i = 0; i < KT; ++i) m[i] = ahead[i];
     }
@@ -788,8 +794,10 @@ void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
         if (p.nseg > 1) {
             const dim3 grid1((unsigned)(chains * ((p.V + p.K) / 64) * (p.nseg - 1)));
             hipLaunchKernelGGL((delta_state_kernel<K, IO, 4, SEG>), grid1, dim3(64 * (4 + LW)), 0, stream, p);
-            hipLaunchKernelGGL((delta_join_kernel<K>), dim3((unsigned)(chains * (p.V / 16))), dim3(4 * K), 0, stream, p);
-            hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, JOIN>), dim3(grid.x * p.nseg), block, 0, stream, p);
+            hipLaunchKernelGGL((delta_join_kernel<K, false>), dim3((unsigned)(chains * (p.V / 16))), dim3(4 * K), 0, stream, p);
+            const dim3 grid2(grid.x * p.nseg);
+            if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, JOIN_CKPTS>), grid2, block, 0, stream, p);
+            else hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, JOIN>), grid2, block, 0, stream, p);
             return;
         }
     }
@@ -818,6 +826,14 @@ hipError_t launch_delta_wy(const DeltaParams &p, hipStream_t stream)
         if (p.io == IO_F16) launch_wy_l2<64, IO_F16>(p, grid, stream);
         else launch_wy_l2<64, IO_BF16>(p, grid, stream);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_delta_join_bwd(const DeltaParams &p, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)p.N * p.HV * (p.V / 16))), block(4 * p.K);
+    if (p.K == 128) hipLaunchKernelGGL((delta_join_kernel<128, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((delta_join_kernel<64, true>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 

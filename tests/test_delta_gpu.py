@@ -469,3 +469,20 @@ def test_hundreds_of_sequences(lib):
     ref = backward64(d)
     for n in ref:
         close(n, got[n], ref[n], DG_REL if n == "dg" else F32_REL)
+
+
+@pytest.mark.parametrize("lens,H,HV,D,io,states", [
+    ([2400], 1, 2, 64, BF16, True), ([2304], 2, 4, 128, F16, True), ([5000, 0, 37, 3000], 1, 2, 64, BF16, True),
+    ([3001], 2, 2, 128, BF16, False)])
+def test_split_backward(lib, lens, H, HV, D, io, states):
+    """The gradients' walks over few long sequences run as parallel segments, with empty ones and short neighbours."""
+    d = make(lens, H, HV, D, D, seed=53, io=io, beta_max=1.0)
+    a, kw = on_gpu(d), dict(d_final_state=d["d_final_state"].cuda())
+    if not states:
+        d["initial_state"], d["d_final_state"] = None, torch.zeros_like(d["d_final_state"])
+        a["initial_state"], kw = None, dict(need_d_initial_state=False)
+    got = lib.delta_chunk_bwd(**a, d_out=d["d_out"].cuda(), **kw)
+    ref = backward64(d)
+    for n in ref:
+        if got[n] is not None:
+            close(n, got[n], ref[n], DG_REL if n == "dg" else F32_REL)

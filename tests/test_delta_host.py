@@ -272,3 +272,11 @@ def test_split_workspace(gdn2):
         for N in (1, 2, 3, 8):
             for HV in range(1, 70):
                 assert 0 <= more(T, N, HV) <= 8 << 20
+
+    def more_bwd(T, N, HV, D):
+        return gdn2.delta_chunk_bwd_workspace(T, N, HV, HV, D, D) - (T // 64 + N) * HV * (26880 + 8 * D * D + 514 * D)
+    assert more_bwd(4096, 1, 16, 128) == 4 * 16 * (131072 + 65536) and 0 <= more_bwd(1000, 1, 1, 64) < 8 * 256
+    for T in (2304, 40000):
+        for N in (1, 3):
+            for HV in range(1, 70):
+                assert 0 <= more_bwd(T, N, HV, 64) and more_bwd(T, N, HV, 128) < (12 << 20) + 8 * 256
