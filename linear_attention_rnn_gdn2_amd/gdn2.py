@@ -373,16 +373,15 @@ def _packer(n):
 
 def _one_device(names, tensors):
     """The GPU that holds every given tensor."""
-    dev = None
+    index = dev = None
     for name, t in zip(names, tensors):
-        if t is None:
+        if t is None or t.get_device() == index:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor (there is no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if dev is not None:
             raise ValueError(f"{name} is on {t.device}, {names[0]} on {dev}")
+        index, dev = t.get_device(), t.device
     return dev
 
 
