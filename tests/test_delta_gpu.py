@@ -486,3 +486,31 @@ def test_split_backward(lib, lens, H, HV, D, io, states):
     for n in ref:
         if got[n] is not None:
             close(n, got[n], ref[n], DG_REL if n == "dg" else F32_REL)
+
+
+def test_offsets_beyond_32_bits(lib):
+    """655360 tokens of 32 heads: records and checkpoints of 5 to 9 GB each; the last sequence's results are those
+    of a call of its own (which runs split: two evaluations of one sum)."""
+    N, L, H, K = 8, 81920, 32, 64
+    gen = torch.Generator(device="cuda").manual_seed(59)
+
+    def unit():
+        x = torch.randn((N * L, H, K), generator=gen, device="cuda", dtype=F32)
+        return (x / x.norm(dim=-1, keepdim=True)).to(BF16)
+
+    a = dict(q=unit(), k=unit(), v=unit(), g=-0.1 * torch.rand((N * L, H), generator=gen, device="cuda"),
+             beta=torch.rand((N * L, H), generator=gen, device="cuda").to(BF16))
+    do = unit()
+    cu = torch.arange(0, N * L + 1, L, device="cuda", dtype=torch.int32)
+    one = {n: x[-L:] for n, x in a.items()}
+    out, fin = lib.delta_chunk_fwd(**a, cu_seqlens=cu)
+    o1, f1 = lib.delta_chunk_fwd(**one)
+    close("state", fin[-1:], f1.cpu(), 2 * F32_REL)
+    close("out", out[-L:], o1.cpu().float(), 2 * F32_REL + 2.0 ** -8)
+    del out
+    big = lib.delta_chunk_bwd(**a, d_out=do, cu_seqlens=cu)
+    small = lib.delta_chunk_bwd(**one, d_out=do[-L:])
+    for n in ("dq", "dk", "dv", "dbeta", "dg"):
+        x = big[n][-L:]
+        close(n, x, small[n].cpu().float(), (2 * DG_REL if n == "dg" else 2 * F32_REL) + (0 if n == "dg" else 2.0 ** -8))
+    close("d_initial_state", big["d_initial_state"][-1:], small["d_initial_state"].cpu(), 2 * F32_REL)

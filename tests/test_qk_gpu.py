@@ -232,3 +232,34 @@ def test_chain_with_gradients(lib, io):
         wg = x[n + "_weight"].grad
         err = float((gp[f"d{n}_weight"].cpu().double() - wg).norm())
         assert err <= 2 * half * float(gr["d" + n].double().norm()), (n, err)
+
+
+@pytest.mark.parametrize("T,H,HK,K,io,inter", [(9001, 3, 2, 64, BF16, False), (4100, 2, 7, 128, F16, True)])
+def test_more_tokens_than_waves(lib, T, H, HK, K, io, inter):
+    """Waves that walk over several tokens, odd head counts, weights' gradients over thousands of rows."""
+    d = inputs(T, H, HK, K, io, F32, 32, seed=T)
+    a = gpu(d, ARGS)
+    y = lib.qk_norm_rope(**a, norm="rms", interleaved=inter)
+    g = lib.qk_norm_rope_bwd(**a, dq_out=d["dq_out"].cuda(), dk_out=d["dk_out"].cuda(), norm="rms", interleaved=inter)
+    for i, n in enumerate(("q", "k")):
+        x, w = d[n].double().requires_grad_(), d[n + "_weight"].double().requires_grad_()
+        r = rows64(x, w, "rms", None, d["rope"], d["positions"], inter)
+        close(n, y[i], r.detach(), REL)
+        r.backward(d[f"d{n}_out"].double())
+        close("d" + n, g["d" + n], x.grad, REL)
+        close(f"d{n}_weight", g[f"d{n}_weight"], w.grad, DW_REL)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_columns_that_are_not_turned(lib, inter):
+    """Infinities and NaN in columns behind the turned ones stay where they are, in both directions."""
+    d = inputs(9, 2, 2, 64, BF16, None, 32, seed=4)
+    clean = lib.qk_norm_rope(**gpu(d, ARGS), norm="none", interleaved=inter)
+    d["q"][3, 1, 40], d["k"][5, 0, 63], d["q"][0, 0, 32] = float("inf"), float("nan"), float("-inf")
+    got = lib.qk_norm_rope(**gpu(d, ARGS), norm="none", interleaved=inter)
+    back = lib.qk_norm_rope_bwd(**gpu(d, ARGS), dq_out=d["q"].cuda(), dk_out=d["k"].cuda(), norm="none", interleaved=inter)
+    for i, n in enumerate(("q", "k")):
+        odd = ~torch.isfinite(d[n])
+        assert torch.equal(~torch.isfinite(got[i].cpu()), odd) and torch.equal(~torch.isfinite(back["d" + n].cpu()), odd)
+        assert torch.equal(got[i].cpu()[~odd], clean[i].cpu()[~odd])
+        assert torch.equal(torch.nan_to_num(got[i].cpu()[odd].float()), torch.nan_to_num(d[n][odd].float()))
