@@ -121,7 +121,9 @@ int delta_columns(const DeltaParams &p, int ncu);
 // at once, of at least 8 chunks. Measured split / whole: 16 heads of 4096
 // tokens 125 / 179 us, 4 of 32768 229 / 1127, 32 of 8192 280 / 355, 16 of
 // 2304 89 / 111; gradients 359 / 471, 706 / 2757, 973 / 1057 and 247 / 289 (8
-// heads of 1600 tokens, three segments: 154 / 147).
+// heads of 1600 tokens, three segments: 154 / 147). The shortest that are
+// split, forwards of 1536 tokens: 1 or 8 heads 62 / 68 (K = V = 64) and 78 /
+// 80 us (128), 32 heads of 128 94 / 89.
 int delta_segments(int64_t T, int64_t N, int64_t HV, int64_t K, int64_t V);
 inline int64_t delta_segment_bytes(int64_t N, int64_t HV, int64_t K, int64_t V, int nseg)
 {
