@@ -284,11 +284,13 @@ def test_empty_calls(lib):
     assert torch.equal(got["d_initial_state"].cpu(), d["d_final_state"])
 
 
-@pytest.mark.parametrize("which", ["chunk", "step", "bwd"])
-def test_graph_replays(lib, which):
-    """A captured call, replayed between eager calls on other inputs, gives the eager call's bits each time."""
-    d = make([130, 40], 1, 2, 64, 64, seed=32)
-    other = make([130, 40], 1, 2, 64, 64, seed=33)
+@pytest.mark.parametrize("which,lens", [("chunk", [130, 40]), ("step", [130, 40]), ("bwd", [130, 40]), ("chunk", [3000, 200]),
+                                        ("bwd", [3000, 200])])
+def test_graph_replays(lib, which, lens):
+    """A captured call (of a split run too), replayed between eager calls on other inputs and other lengths, gives
+    the eager call's bits each time."""
+    d = make(lens, 1, 2, 64, 64, seed=32, beta_max=1.0)
+    other = make(lens[::-1], 1, 2, 64, 64, seed=33, beta_max=1.0)
     a, o = on_gpu(d), on_gpu(other)
     do, dht = d["d_out"].cuda(), d["d_final_state"].cuda()
     do2 = other["d_out"].cuda()
