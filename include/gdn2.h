@@ -454,8 +454,8 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * their own; the state and all sums are float32. Float32 results
  * (final_state, dg, d_initial_state) are within about 1e-6 of a float64
  * evaluation, relative in the 2-norm, on unit-norm keys; 16-bit results are
- * rounded once (a forward output of bf16 takes the state in one such part, 11
- * bits next to its 8).
+ * rounded once (a forward output of bf16 takes the state and the chunk's
+ * factors in one such part, rounded to nearest: 11 bits next to its 8).
  *
  * Workspace: these entries allocate nothing and keep nothing between calls.
  * The caller passes device memory of at least the number of bytes that the

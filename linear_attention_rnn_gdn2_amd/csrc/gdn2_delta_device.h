@@ -2,13 +2,14 @@
 // operands, staged tiles and MFMA fragments. Not part of the ABI.
 //
 // Precision. The sequential passes run on fp16 MFMA with float32 accumulation
-// and take a float32 operand as two fp16 parts, x = h + l, after a power of
-// two has brought the largest value of its column (or chunk) near 2^14: 21
-// significant bits next to that value, 2^-38 of it at the bottom. Products of
-// two such operands drop l l. Rows of q and k that are fp16 values are used
-// as they are; bf16 rows are brought into fp16's range by a power of two
-// (exactly, but for values under 2^-38 of the largest). The state, the chunk's
-// WY solution and all sums are float32.
+// and take a float32 operand as two fp16 parts, x = h + l, each rounded to
+// nearest, after a power of two has brought the largest value of its column (or
+// chunk) near 2^14: 22 significant bits next to that value, 2^-38 of it at the
+// bottom. Products of two such operands drop l l. Rows of q and k that are fp16
+// values are used as they are; bf16 rows are brought into fp16's range by a
+// power of two (exactly, but for values under 2^-30 of the row's largest, which
+// lose bits under fp16's smallest step, 2^-38 of it). The state, the chunk's WY
+// solution and all sums are float32.
 //
 // Fragments (lane = 16 q4 + l16). A 16x16 accumulator tile holds rows
 // 4 q4 + e (e = 0..3) of column l16. As the right operand of the next product
@@ -102,15 +103,17 @@ __device__ __forceinline__ int scale_exp(float m)
     return e > 120 ? 120 : e;
 }
 
-// y0, y1 in fp16, packed, and what is left of them. (Rounded towards zero:
-// one instruction for the pair, and the low part takes up what is lost.)
+// y0, y1 in fp16, packed, and what is left of them. (To nearest, which
+// gfx950 does for the pair in one instruction: the bf16 outputs use high parts
+// without their low ones, and cut off they were 3.5e-4 too small, all alike.)
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack_f16(float y0, float y1)
 {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(y0, y1));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{y0, y1}), f16x2));
 }
 __device__ __forceinline__ void split2_f16(float y0, float y1, uint32_t &h, uint32_t &l)
 {
-    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
     h = pack_f16(y0, y1);
     const f16x2 f = __builtin_bit_cast(f16x2, h);
     l = pack_f16(fmaf((float)f[0], -1.0f, y0), fmaf((float)f[1], -1.0f, y1));

@@ -334,8 +334,10 @@ __global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
 // chain of products, 2.3 us at 32 columns: see the split run (delta_join_kernel).
 constexpr int LW = 4;  // staging waves
 
-// For 16-bit outputs next to bf16 rounding (2^-9) the high parts of S, P and U
-// do (2^-12); next to fp16 rounding they do not.
+// For a bf16 output, which is rounded by up to 2^-8 of itself, the high parts of
+// S, P and U do: to nearest, they are off by up to 2^-11, as likely up as down
+// (outputs are off by 1.68e-3 in the 2-norm, 1.66e-3 of it their own rounding).
+// Next to fp16 rounding they do not.
 template <int K, int IO, int COLS, bool CKPT>
 struct StateLds {
     static constexpr int TILE = Tile<K>::BYTES;
