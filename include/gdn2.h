@@ -431,7 +431,8 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * but for the gates:
  *   q, k  [T, H, K], v, out [T, HV, V]   bf16 or float16, one io type
  *   g     [T, HV]   float32, bf16 or float16; natural log of the decay, <= 0
- *                   and finite (precondition, not checked); NULL: 0
+ *                   and finite (precondition, not checked), the type's lowest
+ *                   value too: it forgets the state; NULL: 0
  *   beta  [T, HV]   io type, taken as given; NULL: 1
  *   initial_state, final_state [N, HV, K, V] float32 or bf16 (or V-major by
  *                   option), cu_seqlens [N + 1] int32 or int64

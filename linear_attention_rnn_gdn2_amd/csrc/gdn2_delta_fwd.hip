@@ -134,7 +134,11 @@ __global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
     double G = 0.0, GC = 0.0;
     if (wave == 0) {
         // running sum of g in 64 bits: its differences are exponents, and a
-        // strongly decayed chunk's sum is far larger than they are
+        // strongly decayed chunk's sum is far larger than they are. Every g is
+        // bounded from below first: e^-200 is 0 in float32 as all beneath it
+        // are, and the other tokens' decays are not lost next to a state reset
+        // written as the type's lowest value (NaN stays).
+        g = g < -200.0f ? -200.0f : g;
         G = (double)g * 1.4426950408889634074;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {

@@ -1,11 +1,13 @@
 """GPU tests of the scalar-gated delta rule at its edges: how bf16 outputs
-round (tolerances of float32 results: see tests/delta_ref.py)."""
+round, and state resets written as the lowest value (tolerances of float32
+results: see tests/delta_ref.py)."""
 
 import numpy as np
 import pytest
+import torch
 
-from tests.delta_ref import forward64, make
-from tests.test_delta_gpu import fwd, lib  # noqa: F401
+from tests.delta_ref import backward64, forward64, make
+from tests.test_delta_gpu import BF16, F16, F32, check_fwd, check_grads, fwd, grads, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,29 @@ def test_bf16_outputs_are_rounded_without_bias(lib, lens, H, HV, K, V):
     allowed = 5 * rms / ref.size ** 0.5
     print(f"rel-L2 {size:.3e} (allowed {rms:.3e}), bias {bias:.2e} (allowed {allowed:.2e})", flush=True)
     assert size <= rms and abs(bias) <= allowed
+
+
+RESETS = [(F32, -1e6), (F32, -1e10), (F32, -1e12), (F32, -1e15), (F32, torch.finfo(F32).min), (BF16, torch.finfo(BF16).min),
+          (F16, torch.finfo(F16).min)]
+
+
+def with_resets(value, gtype, D, seed):
+    """Single tokens that forget everything: inside chunks, at their ends, two in a row, at a sequence's start and end."""
+    d = make([150, 70, 40], 1, 2, D, D, seed=seed, gtype=gtype, beta_max=1.0)
+    for t, head in ((20, 0), (63, 0), (64, 0), (65, 0), (100, 0), (30, 1), (149, 1), (150, 0), (190, 1), (225, 0), (226, 0), (259, 0)):
+        d["g"][t, head] = value
+    return d
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("gtype,value", RESETS)
+def test_resets(lib, recurrent, gtype, value):
+    """Tokens after a reset see nothing before it, and each other as if it were not there."""
+    d = with_resets(value, gtype, 128, 72)
+    check_fwd(f"{value}", fwd(lib, d, recurrent), forward64(d))
+
+
+@pytest.mark.parametrize("gtype,value", RESETS)
+def test_reset_gradients(lib, gtype, value):
+    d = with_resets(value, gtype, 64, 73)
+    check_grads(f"{value}", grads(lib, d), backward64(d))
