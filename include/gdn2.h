@@ -460,7 +460,8 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  *
  * Workspace: these entries allocate nothing and keep nothing between calls.
  * The caller passes device memory of at least the number of bytes that the
- * entry's _workspace function gives (0: NULL is accepted), 256-byte aligned
+ * entry's _workspace function gives (0: NULL is accepted; it also gives 0 for
+ * sizes that the entry refuses), 256-byte aligned
  * and apart from every tensor (GDN2_ERR_WORKSPACE, GDN2_ERR_ALIAS). Its
  * contents before the call do not matter and are undefined after it; it may
  * be reused once the call's work on the stream is done. Calls that can

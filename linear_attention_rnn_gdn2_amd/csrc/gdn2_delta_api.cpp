@@ -38,6 +38,15 @@ int32_t g_type(const gdn2_tensor *g)
     return g->dtype == GDN2_DTYPE_BF16 ? gdn2::G_BF16 : gdn2::G_F16;
 }
 
+// Whether one launch holds a call's chains and chunks (T within int32, N, HV > 0).
+bool fits_grid(int64_t T, int64_t N, int64_t HV)
+{
+    return N <= kMaxItems && HV <= kMaxItems && N * HV <= kMaxItems && gdn2::slot_count(T, N) * HV <= kMaxItems;
+}
+
+// (64 rows of the value heads are addressed with 32-bit byte offsets in the backward)
+bool fits_rows(int64_t HV, int64_t V) { return HV * V * 128 <= INT32_MAX; }
+
 // Sizes shared by the rule's entries, after q's, k's and v's own checks.
 int check_sizes(const gdn2_tensor *q, const gdn2_tensor *v, const gdn2_tensor *cu, int64_t *N_out)
 {
@@ -56,7 +65,7 @@ int check_sizes(const gdn2_tensor *q, const gdn2_tensor *v, const gdn2_tensor *c
         if (N < 1) return fail(GDN2_ERR_SHAPE, "cu_seqlens needs at least 2 entries (N >= 1)");
         if (!cu->data) return fail(GDN2_ERR_NULL_ARG, "cu_seqlens: data is NULL");
     }
-    if (N > kMaxItems || HV > kMaxItems || N * HV > kMaxItems || gdn2::slot_count(T, N) * HV > kMaxItems)
+    if (!fits_grid(T, N, HV))
         return fail(GDN2_ERR_SHAPE, "N * HV or the chunk count times HV exceeds the grid limit (%lld)", (long long)kMaxItems);
     *N_out = N;
     return GDN2_OK;
@@ -254,8 +263,7 @@ int validate(const DeltaBwd &a, void *ws, int64_t ws_bytes, DeltaParams *p)
     if (K != V)
         return fail(GDN2_ERR_UNSUPPORTED, "(K, V) = (%lld, %lld) not supported by the backward; it takes (64, 64) or (128, 128)",
                     (long long)K, (long long)V);
-    // (64 rows are addressed with 32-bit byte offsets)
-    if (HV * V * 128 > INT32_MAX) return fail(GDN2_ERR_SHAPE, "HV = %lld: 64 rows of the value heads must span under 2 GiB", (long long)HV);
+    if (!fits_rows(HV, V)) return fail(GDN2_ERR_SHAPE, "HV = %lld: 64 rows of the value heads must span under 2 GiB", (long long)HV);
     const int64_t gs[2] = {T, HV}, vs[3] = {T, HV, V}, ss[4] = {N, HV, K, V};
     if ((rc = check_g(a.g, "g", gs, DENSE))) return rc;
     if ((rc = check_tensor(a.beta, "beta", io, -1, 2, gs))) return rc;
@@ -339,6 +347,9 @@ const char *kQkDy[2] = {"dq_out", "dk_out"};
 const char *kQkW[2] = {"q_weight", "k_weight"};
 const char *kQkDw[2] = {"dq_weight", "dk_weight"};
 
+// Heads of q and k together.
+bool fits_heads(int64_t heads) { return heads <= INT32_MAX / 2; }
+
 // (backward: a.dy and a.dw are used, and y are the gradients dq, dk)
 int validate(const Qk &a, bool backward, void *ws, int64_t ws_bytes, QkParams *p)
 {
@@ -372,7 +383,7 @@ int validate(const Qk &a, bool backward, void *ws, int64_t ws_bytes, QkParams *p
     if (K != 64 && K != 128) return fail(GDN2_ERR_UNSUPPORTED, "K = %lld not supported; K must be 64 or 128", (long long)K);
     if (a.x[0]->shape[1] < 1 || a.x[1]->shape[1] < 1) return fail(GDN2_ERR_HEADS, "q and k need at least one head each");
     const int64_t heads = a.x[0]->shape[1] + a.x[1]->shape[1];
-    if (T > INT32_MAX || heads > INT32_MAX / 2) return fail(GDN2_ERR_SHAPE, "T or the head count exceeds the int32 range");
+    if (T > INT32_MAX || !fits_heads(heads)) return fail(GDN2_ERR_SHAPE, "T or the head count exceeds the int32 range");
     for (int i = 0; i < 2; ++i) {
         const int64_t want[3] = {T, a.x[i]->shape[1], K};
         if ((rc = check_io(a.y[i], y_names[i], io, want, ROWS))) return rc;
@@ -464,13 +475,14 @@ extern "C" {
 
 int64_t gdn2_delta_chunk_fwd_workspace(int64_t T, int32_t N, int32_t HV)
 {
-    if (T <= 0 || N <= 0 || HV <= 0) return 0;
+    if (T <= 0 || T > INT32_MAX || N <= 0 || HV <= 0 || !fits_grid(T, N, HV)) return 0;
     return fwd_records(T, N, HV) + fwd_segments(T, N, HV);
 }
 
 int64_t gdn2_delta_chunk_bwd_workspace(int64_t T, int32_t N, int32_t H, int32_t HV, int32_t K, int32_t V)
 {
-    if (T <= 0 || N <= 0 || H <= 0 || HV <= 0 || K <= 0 || V <= 0) return 0;
+    if (T <= 0 || T > INT32_MAX || N <= 0 || H <= 0 || HV <= 0 || HV % H != 0 || (K != 64 && K != 128) || V != K) return 0;
+    if (!fits_grid(T, N, HV) || !fits_rows(HV, V)) return 0;
     return BwdSpace(T, N, H, HV, K, V).total;
 }
 
@@ -566,7 +578,7 @@ int gdn2_qk_norm_rope_fwd_check(const gdn2_tensor *q, const gdn2_tensor *k, cons
 
 int64_t gdn2_qk_norm_rope_bwd_workspace(int64_t T, int32_t H, int32_t HK, int32_t K)
 {
-    if (T <= 0 || H <= 0 || HK <= 0 || (K != 64 && K != 128)) return 0;
+    if (T <= 0 || T > INT32_MAX || H <= 0 || HK <= 0 || !fits_heads((int64_t)H + HK) || (K != 64 && K != 128)) return 0;
     return up256((int64_t)gdn2::qk_bwd_groups(T, H, HK, K) * 2 * K * 4);
 }
 

@@ -56,3 +56,18 @@ def test_resets(lib, recurrent, gtype, value):
 def test_reset_gradients(lib, gtype, value):
     d = with_resets(value, gtype, 64, 73)
     check_grads(f"{value}", grads(lib, d), backward64(d))
+
+
+@pytest.mark.parametrize("K,V", [(16, 16), (8, 64), (96, 96), (64, 128)])
+def test_unsupported_head_sizes_are_refused(lib, K, V):
+    """Head sizes that the gradients do not take, the smallest too, are refused by the library."""
+    q, v, g = torch.zeros(9, 2, K, dtype=BF16, device="cuda"), torch.zeros(9, 2, V, dtype=BF16, device="cuda"), torch.zeros(9, 2, device="cuda")
+    with pytest.raises(lib.Gdn2Error) as e:
+        lib.delta_chunk_bwd(q, q.clone(), v, g, g.to(BF16), v.clone())
+    assert e.value.status == "UNSUPPORTED"
+    if (K, V) == (64, 128):
+        return
+    for call in (lib.delta_chunk_fwd, lib.delta_recurrent_fwd):
+        with pytest.raises(lib.Gdn2Error) as e:
+            call(q, q.clone(), v)
+        assert e.value.status == "UNSUPPORTED"
