@@ -118,12 +118,14 @@ int delta_columns(const DeltaParams &p, int ncu);
 // of DeltaParams::seg. A split costs a second walk over every chunk and pays
 // where the compute units would be idle: as many segments as keep the first
 // walk's workgroups (64 columns of the state or of the transition) resident
-// at once, of at least 8 chunks. Measured split / whole: 16 heads of 4096
-// tokens 125 / 179 us, 4 of 32768 229 / 1127, 32 of 8192 280 / 355, 16 of
-// 2304 89 / 111; gradients 359 / 471, 706 / 2757, 973 / 1057 and 247 / 289 (8
-// heads of 1600 tokens, three segments: 154 / 147). The shortest that are
-// split, forwards of 1536 tokens: 1 or 8 heads 62 / 68 (K = V = 64) and 78 /
-// 80 us (128), 32 heads of 128 94 / 89.
+// at once, of at least 8 chunks; where no more than three are, the sequences
+// need 32 chunks. Measured split / whole in us: 16 heads of 4096 tokens 98 /
+// 158, 4 of 32768 215 / 1106, 32 of 8192 255 / 325, 16 of 2304 75 / 93;
+// gradients 299 / 425, 662 / 2736, 918 / 1028 and 209 / 259. The shortest that
+// are split, 1536 tokens: 8 heads of 64 46 / 52 and 112 / 120, of 128 63 / 65
+// and 156 / 167. 32 heads of 128, of which three segments are resident: 1536
+// tokens 73 / 71 and 217 / 207, 1792 82 / 81 and 253 / 244, 2048 87 / 91 and
+// 275 / 271, 2304 95 / 102 and 319 / 316.
 int delta_segments(int64_t T, int64_t N, int64_t HV, int64_t K, int64_t V);
 inline int64_t delta_segment_bytes(int64_t N, int64_t HV, int64_t K, int64_t V, int nseg)
 {

@@ -857,6 +857,7 @@ int delta_segments(int64_t T, int64_t N, int64_t HV, int64_t K, int64_t V)
     if (T <= 0 || N <= 0 || HV <= 0) return 1;
     const int64_t chunks = T / CHUNK / N;  // of a sequence of mean length
     int64_t s = 1 + 256 / (N * HV * ((V + K) / 64));
+    if (s == 3 && chunks < 32) return 1;
     if (s > 32) s = 32;
     if (s > chunks / 8) s = chunks / 8;
     return s < 3 ? 1 : (int)s;

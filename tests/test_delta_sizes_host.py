@@ -29,6 +29,23 @@ def test_no_preparation_workspace_for_refused_sizes(gdn2):
         assert gdn2.qk_norm_rope_bwd_workspace(*args) == 0
 
 
+def segments(mod, T, N, HV, D):
+    """The segments of each sequence of a call with K = V = D, from what its workspace holds for them."""
+    items = (T // 64 + N) * HV
+    more = mod.delta_chunk_bwd_workspace(T, N, HV, HV, D, D) - items * (26880 + 8 * D * D + 514 * D)
+    return 1 + more // (N * HV * 3 * D * D * 4)
+
+
+@pytest.mark.parametrize("T,N,HV,D,want", [
+    (1535, 1, 1, 64, 1), (1536, 1, 1, 64, 3), (1536, 1, 8, 128, 3), (4096, 1, 16, 128, 5), (16500, 1, 1, 64, 32),
+    # no more than three segments are resident at once
+    (1536, 1, 32, 128, 1), (2047, 1, 32, 128, 1), (2048, 1, 32, 128, 3), (8192, 1, 32, 128, 3), (4095, 2, 16, 128, 1),
+    (4096, 2, 16, 128, 3), (1 << 20, 1, 65, 128, 1)])
+def test_split_rule(gdn2, T, N, HV, D, want):
+    """Sequences are split where that was measured faster."""
+    assert segments(gdn2, T, N, HV, D) == want
+
+
 def tensor(mod, at, dtype, *shape):
     """The descriptor of a dense tensor at an address of its own (`at` times 2^44), which nothing reads."""
     d = mod.Gdn2Tensor()
