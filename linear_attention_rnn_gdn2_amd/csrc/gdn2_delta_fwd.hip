@@ -807,8 +807,12 @@ void launch_state_ck(const DeltaParams &p, bool ckpt, hipStream_t stream)
             return;
         }
     }
-    if (ckpt) hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, CKPTS>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, OUT>), grid, block, 0, stream, p);
+    if constexpr (16 * NC <= K)  // (gradients: K = V)
+        if (ckpt) {
+            hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, CKPTS>), grid, block, 0, stream, p);
+            return;
+        }
+    hipLaunchKernelGGL((delta_state_kernel<K, IO, NC, OUT>), grid, block, 0, stream, p);
 }
 
 template <int K, int IO>
