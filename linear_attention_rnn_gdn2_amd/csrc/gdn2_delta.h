@@ -110,9 +110,13 @@ struct QkParams {
 // where two rounds of them run, else 128. Few chains spread over the device,
 // many do not load a chunk's tiles more often than they must, and between
 // the two, chains of unlike lengths share the compute units better in halves
-// (256 chains of 5 to 128 chunks, forward and gradients: 64 columns 868 and
-// 3191 us, 128 columns 900 and 3414; all of 73 chunks: 675 and 3037, 636 and
-// 3052; 1024 chains of 16 chunks: 629 and 2713, 561 and 2638).
+// (K = V = 128, bf16, forward and gradients: 256 chains of 20 to 128 chunks in
+// 64 columns 681 and 2952 us, in 128 733 and 3216; all of 73 chunks 670 and
+// 2939, 609 and 2905; 1024 chains of 16 chunks 630 and 2629, 561 and 2576; 64
+// chains of 64 chunks in 32 columns 195 and 762, in 64 215 and 820. The fp16
+// forward in 128 columns holds the low parts of its outputs' operands beside
+// them and spills: 1024 chains of 16 chunks 657 in 64 columns, 683 in 128; of 64
+// chunks 1236, 1290; 19,200 of one chunk 1431, 1202).
 int delta_columns(const DeltaParams &p, int ncu);
 // Segments of each sequence of a chunked call (1: not split), and the bytes
 // of DeltaParams::seg. A split costs a second walk over every chunk and pays

@@ -36,8 +36,8 @@ using namespace dev;
 // each, 4 staging waves. T and P are used transposed, through transpose reads
 // of their planes, which are staged row-major for that (PlaneTile).
 // Bound by HBM with many chains: 190 KiB per item, of which dS and dY, 96 KiB,
-// are left for the gradients (8 sequences, 37,517 tokens, 32 heads: 785 us,
-// 4.6 TB/s; the checkpoints of the forward's pass, 140 KiB per item, 530 us).
+// are left for the gradients (8 sequences, 36,962 tokens, 32 heads: 775 us,
+// 4.6 TB/s; the checkpoints of the forward's pass, 140 KiB per item, 535 us).
 constexpr int LW = 4;  // staging waves
 
 // A record's plane, row-major: columns 0 .. 31 of all rows, then columns
@@ -341,9 +341,9 @@ __global__ __launch_bounds__(64 * (NC + LW)) void delta_bwd_state_kernel(DeltaPa
 // fp16 parts under one power of two per operand and chunk (the sequential
 // passes leave the largest magnitudes). Two workgroups share a compute unit
 // and hide each other's loads; one with the next block's loads in registers
-// was slower (1.75 against 1.35 ms on 8 sequences, 37,517 tokens, 32 heads;
-// 1.5 ms with the second fp16 parts). Bound by HBM, 290 KiB per item at
-// 3.8 TB/s, and by the loads' latency in what is left of the copy rate.
+// took three tenths longer. Bound by HBM, 310 KiB per item at 4.2 TB/s (8
+// sequences, 36,962 tokens, 32 heads: 1.40 ms), and by the loads' latency in
+// what is left of the copy rate.
 
 // 32 rows (v) of C 16-bit values, written 8 bytes at a time down 16 rows and
 // read transposed from 4 rows and the 4 rows 8 further on: pieces of 16 bytes

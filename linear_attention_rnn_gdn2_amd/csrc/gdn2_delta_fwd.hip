@@ -41,9 +41,10 @@ using namespace dev;
 // column towards the left,
 //     T_ij^T = -T_jj^T (sum_{j < m <= i} A_mj^T T_im^T)
 // on float32 MFMA (16x16x4), whose accumulators are its next right operands.
-// Bound by HBM (59 KiB read and written per item): 18,700 items of 8 packed
-// sequences (37,517 tokens, 32 heads) take 225 us, 5 TB/s; with three waves
-// per SIMD instead of four, whose registers spill nothing either, 258 us.
+// Bound by HBM (57 KiB read and written per item): 18,700 items of 8 packed
+// sequences (36,962 tokens, 32 heads) take 210 us, 5.2 TB/s; with three waves
+// per SIMD instead of four, whose registers spill nothing either, a seventh
+// longer.
 template <int K>
 struct WyLds {
     static constexpr int RS = 2 * K + 16;  // row stride of a staged tile (bytes): rows 16 bytes apart in banks
@@ -332,16 +333,18 @@ __global__ __launch_bounds__(256, 4) void delta_wy_kernel(DeltaParams p)
 // outputs of the chunk before. One barrier per chunk; the computing waves
 // touch no global memory but for the states.
 //
-// Bound, with many chains, by HBM: a chunk's tiles, record and outputs are 88
-// KiB per item (the packed batch above: 510 us, of which its longest chain
-// sets 320; equal lengths 390 us, 4.3 TB/s). With few chains by a chunk's
-// chain of products, 2.3 us at 32 columns: see the split run (delta_join_kernel).
+// Bound, with many chains, by HBM: a chunk's tiles, record and outputs are 85
+// KiB per item (the packed batch above: 480 us, of which its longest chain of
+// 128 chunks sets 270; equal lengths in 128 columns 390 us, 4.1 TB/s). With few
+// chains by a chunk's chain of products, 2.1 us at 32 columns: see the split run
+// (delta_join_kernel).
 constexpr int LW = 4;  // staging waves
 
 // For a bf16 output, which is rounded by up to 2^-8 of itself, the high parts of
 // S, P and U do: to nearest, they are off by up to 2^-11, as likely up as down
-// (outputs are off by 1.68e-3 in the 2-norm, 1.66e-3 of it their own rounding).
-// Next to fp16 rounding they do not.
+// (outputs are off by 1.68e-3 in the 2-norm, 1.66e-3 of it their own rounding;
+// with the low parts a call takes 3 to 9% longer, in 128 columns 20%). Next to
+// fp16 rounding they do not.
 template <int K, int IO, int COLS, bool CKPT>
 struct StateLds {
     static constexpr int TILE = Tile<K>::BYTES;

@@ -9,10 +9,10 @@
 // once. Lane 8 i + j owns rows i K / 8 .. of columns 4 j .. 4 j + 3; the two
 // column sums per token join the 8 row groups by three lane exchanges, and no
 // wave waits for another. Bound by HBM, the states' bytes: 128 sequences of 32
-// heads (K = V = 128, 541 MB) take 99 us, 5.5 TB/s; spans of 1 to 8 tokens of
+// heads (K = V = 128, 541 MB) take 100 us, 5.4 TB/s; spans of 1 to 8 tokens of
 // 48 sequences 29 us, 3.6 TB/s (a token's loads in flight over the token
 // before it measured slower, 31 us: the waves beside a waiting one cover it,
-// and it costs registers); one sequence of 32 heads 6.3 us, all of it latency.
+// and it costs registers); one sequence of 32 heads 6.0 us, all of it latency.
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>

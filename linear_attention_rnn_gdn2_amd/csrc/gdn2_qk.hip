@@ -17,8 +17,8 @@
 // split over several waves. Sums are lane exchanges in float32. Pairs (i, i +
 // rot / 2) lie in two lanes rot / 16 apart and are exchanged through the
 // lanes, pairs (2 i, 2 i + 1) in one. 37,517 tokens of 32 + 32 heads of 128 take
-// 225 us (5.5 TB/s; four rows in flight, two: 248), their gradients for 16,384
-// tokens of 32 + 8 heads 103 us and 7 for the weights' (4.6 TB/s).
+// 225 us (5.5 TB/s; with two rows in flight a tenth longer), their gradients for
+// 16,384 tokens of 32 + 8 heads 107 us and 7 for the weights' (4.8 TB/s).
 #include <stdint.h>
 
 #include <type_traits>
