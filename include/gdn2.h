@@ -447,7 +447,9 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * (GDN2_ERR_UNSUPPORTED); the recurrent one ignores it.
  * N * HV and (T / 64 + N) * HV may reach 5592405 (GDN2_ERR_SHAPE beyond).
  * Tokens behind the last sequence (cu_seqlens[N] < T, a padded batch) are not
- * read, and no output or gradient of theirs is written.
+ * read, and no output or gradient of theirs is written. An infinity or NaN in
+ * a token reaches no other sequence; in the chunked entries it may reach the
+ * earlier tokens of its 64-token chunk too.
  *
  * Accuracy: products run on fp16 MFMA with float32 accumulation; float32
  * operands are taken in two fp16 parts next to a power of two of their
