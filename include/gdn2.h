@@ -456,16 +456,16 @@ int gdn2_chunk_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  * column's largest value (22 significant bits), bf16 rows next to one of
  * their own; the state and all sums are float32. Float32 results
  * (final_state, dg, d_initial_state) are within about 1e-6 of a float64
- * evaluation, relative in the 2-norm, on unit-norm keys; 16-bit results are
+ * evaluation, relative in the 2-norm, on unit-norm keys (within 1e-5 where a
+ * chunk repeats one key, not decayed, at beta near 2); 16-bit results are
  * rounded once (a forward output of bf16 takes the state and the chunk's
  * factors in one such part, rounded to nearest: 11 bits next to its 8).
  *
  * Workspace: these entries allocate nothing and keep nothing between calls.
  * The caller passes device memory of at least the number of bytes that the
  * entry's _workspace function gives (0: NULL is accepted; it also gives 0 for
- * sizes that the entry refuses), 256-byte aligned
- * and apart from every tensor (GDN2_ERR_WORKSPACE, GDN2_ERR_ALIAS). Its
- * contents before the call do not matter and are undefined after it; it may
+ * sizes that the entry refuses), 256-byte aligned and apart from every tensor
+ * (GDN2_ERR_WORKSPACE, GDN2_ERR_ALIAS). Its contents before the call do not matter and are undefined after it; it may
  * be reused once the call's work on the stream is done. Calls that can
  * overlap in time need workspaces of their own. Every entry may be captured
  * into a graph; a graph's workspace belongs to that graph's replays.
