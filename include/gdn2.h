@@ -29,7 +29,7 @@
 extern "C" {
 #endif
 
-#define GDN2_ABI_VERSION 6
+#define GDN2_ABI_VERSION 7
 
 /* Element types a tensor descriptor may carry. */
 typedef enum gdn2_dtype {
@@ -642,6 +642,264 @@ int gdn2_qk_norm_rope_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
                                 const gdn2_tensor *dq_weight,
                                 const gdn2_tensor *dk_weight,
                                 const gdn2_qk_options *opts);
+
+/* --------------------------------------------- around the rule: a mixer's
+ * other per-channel operators --
+ *
+ * What stands before and after a rule in a token mixer: the short causal
+ * convolution of its inputs, the gated linear recurrence (a rule with a
+ * vector for a state), and the norm of rows with a gate. Shared by all three:
+ *   types   x and its like ("io type"): bf16, float16 or float32, one type
+ *           per call; arithmetic, sums and statistics in float32, rounded
+ *           once
+ *   layout  the last dimension contiguous, the other strides free and
+ *           non-negative (0 too, for inputs); pointers aligned to their
+ *           element (rows of an even number of elements that are aligned to
+ *           two run faster); the rows of an output may not overlap. Weights,
+ *           states and cu_seqlens dense.
+ *   sizes   T and N any number to 2^31 - 65537, D to 2^24 (the norm: 16384),
+ *           within the 2^32 - 1 threads that one launch can hold
+ *           (GDN2_ERR_SHAPE beyond)
+ *   cu_seqlens, workspaces, errors, streams, graphs: as for the
+ *           scalar-gated rule above. Tokens behind the last sequence are not
+ *           read, and nothing of theirs is written. An infinity or NaN in a
+ *           token reaches no other sequence and no other channel (norm: no
+ *           other row, but for the weights' gradients).
+ * Outputs may not overlap inputs or each other (GDN2_ERR_ALIAS).
+ */
+
+/*
+ * The gated linear recurrence: per sequence and channel
+ *
+ *     h_t = e^(g_t) h_{t-1} + m_t w_t x_t,   out_t = h_t
+ *     m   = 1,  1 - e^g  or  sqrt(1 - e^(2 g))
+ *
+ *   x, w, out [T, D]  io type; w NULL: 1
+ *   g [T, D]          float32 or the io type: natural log of the decay, <= 0
+ *                     (precondition, not checked), minus infinity or the
+ *                     type's lowest value too: they forget the state
+ *   initial_state, final_state [N, D]  float32 or bf16 (NULL: zero / not
+ *                     written)
+ *
+ * gdn2_linear_scan_fwd runs over long sequences: groups of whole sequences
+ * side by side where that fills the GPU, else tiles of 64 tokens, joined by
+ * the products of their decays (chosen from T, N and D alone; only the second
+ * needs the workspace). gdn2_linear_scan_recurrent_fwd walks token by token
+ * (decode, short spans), where final_state may be initial_state's own buffer
+ * (same pointer and type) to update the state in place.
+ *
+ * Slow decays are held by e^g - 1, so that g near 0 keeps its precision:
+ * float32 results are within about 1e-6 of a float64 evaluation, relative in
+ * the 2-norm.
+ */
+enum {
+    GDN2_SCAN_INPUT_NONE = 0,   /* m = 1 */
+    GDN2_SCAN_INPUT_CONVEX = 1, /* m = 1 - e^g */
+    GDN2_SCAN_INPUT_UNIT = 2    /* m = sqrt(1 - e^(2 g)) */
+};
+
+/* struct_size: sizeof(gdn2_scan_options). NULL options: m = 1. */
+typedef struct gdn2_scan_options {
+    int32_t struct_size;
+    int32_t input_scale; /* GDN2_SCAN_INPUT_* */
+} gdn2_scan_options;
+
+int64_t gdn2_linear_scan_fwd_workspace(int64_t T, int32_t N, int32_t D);
+int gdn2_linear_scan_fwd(const gdn2_tensor *x, const gdn2_tensor *g,
+                         const gdn2_tensor *w, const gdn2_tensor *initial_state,
+                         const gdn2_tensor *cu_seqlens, const gdn2_tensor *out,
+                         const gdn2_tensor *final_state,
+                         const gdn2_scan_options *opts, void *workspace,
+                         int64_t workspace_bytes, hipStream_t stream);
+int gdn2_linear_scan_fwd_check(const gdn2_tensor *x, const gdn2_tensor *g,
+                               const gdn2_tensor *w,
+                               const gdn2_tensor *initial_state,
+                               const gdn2_tensor *cu_seqlens,
+                               const gdn2_tensor *out,
+                               const gdn2_tensor *final_state,
+                               const gdn2_scan_options *opts);
+int gdn2_linear_scan_recurrent_fwd(const gdn2_tensor *x, const gdn2_tensor *g,
+                                   const gdn2_tensor *w,
+                                   const gdn2_tensor *initial_state,
+                                   const gdn2_tensor *cu_seqlens,
+                                   const gdn2_tensor *out,
+                                   const gdn2_tensor *final_state,
+                                   const gdn2_scan_options *opts,
+                                   hipStream_t stream);
+int gdn2_linear_scan_recurrent_fwd_check(const gdn2_tensor *x,
+                                         const gdn2_tensor *g,
+                                         const gdn2_tensor *w,
+                                         const gdn2_tensor *initial_state,
+                                         const gdn2_tensor *cu_seqlens,
+                                         const gdn2_tensor *out,
+                                         const gdn2_tensor *final_state,
+                                         const gdn2_scan_options *opts);
+
+/*
+ * Its backward: dx, dw (io type; dw with w, NULL: not written), dg (g's type),
+ * d_initial_state [N, D] float32 (NULL: not written) from the inputs, d_out
+ * (io type) and d_final_state [N, D] float32 (NULL: zero). The derivative of
+ * sqrt(1 - e^(2 g)) at g = 0, where it is infinite, is taken as 0.
+ */
+int64_t gdn2_linear_scan_bwd_workspace(int64_t T, int32_t N, int32_t D);
+int gdn2_linear_scan_bwd(const gdn2_tensor *x, const gdn2_tensor *g,
+                         const gdn2_tensor *w, const gdn2_tensor *initial_state,
+                         const gdn2_tensor *cu_seqlens,
+                         const gdn2_tensor *d_out,
+                         const gdn2_tensor *d_final_state,
+                         const gdn2_tensor *dx, const gdn2_tensor *dg,
+                         const gdn2_tensor *dw,
+                         const gdn2_tensor *d_initial_state,
+                         const gdn2_scan_options *opts, void *workspace,
+                         int64_t workspace_bytes, hipStream_t stream);
+int gdn2_linear_scan_bwd_check(const gdn2_tensor *x, const gdn2_tensor *g,
+                               const gdn2_tensor *w,
+                               const gdn2_tensor *initial_state,
+                               const gdn2_tensor *cu_seqlens,
+                               const gdn2_tensor *d_out,
+                               const gdn2_tensor *d_final_state,
+                               const gdn2_tensor *dx, const gdn2_tensor *dg,
+                               const gdn2_tensor *dw,
+                               const gdn2_tensor *d_initial_state,
+                               const gdn2_scan_options *opts);
+
+/*
+ * The short causal convolution: per sequence and channel, with K = 2, 3 or 4
+ * taps,
+ *
+ *     p_t = bias + sum_j weight[j] x_{t-(K-1)+j},   out_t = p_t or p_t sigmoid(p_t)
+ *
+ *   x, out [T, D], initial_state, final_state [N, K - 1, D]  io type: the K - 1
+ *                    inputs before a sequence's first token and its last
+ *                    K - 1, the oldest first (NULL: zeros / not written). A
+ *                    sequence of under K - 1 tokens keeps rows of its initial
+ *                    state in its final one.
+ *   weight [D, K], bias [D]  float32 or the io type, both one type; bias NULL: 0
+ *
+ * gdn2_short_conv_recurrent_fwd walks token by token (decode, short spans);
+ * there final_state may be initial_state's own buffer. No workspace.
+ */
+enum { GDN2_CONV_NONE = 0, GDN2_CONV_SILU = 1 };
+
+/* struct_size: sizeof(gdn2_conv_options). NULL options: SiLU. */
+typedef struct gdn2_conv_options {
+    int32_t struct_size;
+    int32_t activation; /* GDN2_CONV_* */
+} gdn2_conv_options;
+
+int gdn2_short_conv_fwd(const gdn2_tensor *x, const gdn2_tensor *weight,
+                        const gdn2_tensor *bias,
+                        const gdn2_tensor *initial_state,
+                        const gdn2_tensor *cu_seqlens, const gdn2_tensor *out,
+                        const gdn2_tensor *final_state,
+                        const gdn2_conv_options *opts, hipStream_t stream);
+int gdn2_short_conv_fwd_check(const gdn2_tensor *x, const gdn2_tensor *weight,
+                              const gdn2_tensor *bias,
+                              const gdn2_tensor *initial_state,
+                              const gdn2_tensor *cu_seqlens,
+                              const gdn2_tensor *out,
+                              const gdn2_tensor *final_state,
+                              const gdn2_conv_options *opts);
+int gdn2_short_conv_recurrent_fwd(const gdn2_tensor *x,
+                                  const gdn2_tensor *weight,
+                                  const gdn2_tensor *bias,
+                                  const gdn2_tensor *initial_state,
+                                  const gdn2_tensor *cu_seqlens,
+                                  const gdn2_tensor *out,
+                                  const gdn2_tensor *final_state,
+                                  const gdn2_conv_options *opts,
+                                  hipStream_t stream);
+int gdn2_short_conv_recurrent_fwd_check(const gdn2_tensor *x,
+                                        const gdn2_tensor *weight,
+                                        const gdn2_tensor *bias,
+                                        const gdn2_tensor *initial_state,
+                                        const gdn2_tensor *cu_seqlens,
+                                        const gdn2_tensor *out,
+                                        const gdn2_tensor *final_state,
+                                        const gdn2_conv_options *opts);
+
+/*
+ * Its backward: dx, d_initial_state [N, K - 1, D] (io type; NULL: not
+ * written), dweight and dbias (the weight's type; NULL: not written; dbias
+ * with bias), summed over all tokens in float32 in a fixed order, from the
+ * inputs, d_out and d_final_state (io type; NULL: zero). The sums need the
+ * workspace (0 bytes when neither is given).
+ */
+int64_t gdn2_short_conv_bwd_workspace(int64_t T, int32_t D, int32_t K);
+int gdn2_short_conv_bwd(const gdn2_tensor *x, const gdn2_tensor *weight,
+                        const gdn2_tensor *bias,
+                        const gdn2_tensor *initial_state,
+                        const gdn2_tensor *cu_seqlens,
+                        const gdn2_tensor *d_out,
+                        const gdn2_tensor *d_final_state,
+                        const gdn2_tensor *dx, const gdn2_tensor *dweight,
+                        const gdn2_tensor *dbias,
+                        const gdn2_tensor *d_initial_state,
+                        const gdn2_conv_options *opts, void *workspace,
+                        int64_t workspace_bytes, hipStream_t stream);
+int gdn2_short_conv_bwd_check(const gdn2_tensor *x, const gdn2_tensor *weight,
+                              const gdn2_tensor *bias,
+                              const gdn2_tensor *initial_state,
+                              const gdn2_tensor *cu_seqlens,
+                              const gdn2_tensor *d_out,
+                              const gdn2_tensor *d_final_state,
+                              const gdn2_tensor *dx,
+                              const gdn2_tensor *dweight,
+                              const gdn2_tensor *dbias,
+                              const gdn2_tensor *d_initial_state,
+                              const gdn2_conv_options *opts);
+
+/*
+ * The norm of rows: every (token, head) row x of D elements, 1 <= D <= 16384,
+ * becomes
+ *
+ *     n = (x - mean) / sqrt(var + eps)  (LAYER)  or  x / sqrt(mean x^2 + eps)  (RMS)
+ *     y = n weight + bias,   times gate sigmoid(gate) where a gate is given
+ *
+ *   x, gate, out [T, H, D]  io type; gate NULL: none
+ *   weight, bias [D]        float32 or the io type, each; NULL: 1, 0
+ * T * H to 2^31 - 1. The output of a rule with its gate is [T, HV, V]; a
+ * residual stream [T, D] is T rows of one head.
+ */
+enum { GDN2_NORM_LAYER = 0, GDN2_NORM_RMS = 1 };
+
+/* struct_size: sizeof(gdn2_norm_options). NULL options: LAYER, 1e-5. */
+typedef struct gdn2_norm_options {
+    int32_t struct_size;
+    int32_t norm; /* GDN2_NORM_* */
+    float eps;    /* 0: 1e-5 (LAYER) or 1e-6 (RMS) */
+} gdn2_norm_options;
+
+int gdn2_layer_norm_fwd(const gdn2_tensor *x, const gdn2_tensor *gate,
+                        const gdn2_tensor *weight, const gdn2_tensor *bias,
+                        const gdn2_tensor *out, const gdn2_norm_options *opts,
+                        hipStream_t stream);
+int gdn2_layer_norm_fwd_check(const gdn2_tensor *x, const gdn2_tensor *gate,
+                              const gdn2_tensor *weight,
+                              const gdn2_tensor *bias, const gdn2_tensor *out,
+                              const gdn2_norm_options *opts);
+
+/*
+ * Its backward: dx and (with gate) dgate, of x's shape and type, and, where
+ * given, dweight and dbias [D] in their tensors' types, summed over all rows
+ * in float32 in a fixed order, which need the workspace (0 bytes when neither
+ * is given). Nothing is kept from the forward.
+ */
+int64_t gdn2_layer_norm_bwd_workspace(int64_t T, int32_t H, int32_t D);
+int gdn2_layer_norm_bwd(const gdn2_tensor *x, const gdn2_tensor *gate,
+                        const gdn2_tensor *weight, const gdn2_tensor *bias,
+                        const gdn2_tensor *d_out, const gdn2_tensor *dx,
+                        const gdn2_tensor *dgate, const gdn2_tensor *dweight,
+                        const gdn2_tensor *dbias,
+                        const gdn2_norm_options *opts, void *workspace,
+                        int64_t workspace_bytes, hipStream_t stream);
+int gdn2_layer_norm_bwd_check(const gdn2_tensor *x, const gdn2_tensor *gate,
+                              const gdn2_tensor *weight,
+                              const gdn2_tensor *bias, const gdn2_tensor *d_out,
+                              const gdn2_tensor *dx, const gdn2_tensor *dgate,
+                              const gdn2_tensor *dweight,
+                              const gdn2_tensor *dbias,
+                              const gdn2_norm_options *opts);
 
 /* Message describing the last failure on the calling thread ("" if none).
  * The string stays valid until the next call on the same thread. */

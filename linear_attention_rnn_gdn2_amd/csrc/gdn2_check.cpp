@@ -100,7 +100,10 @@ int check_tensor(const gdn2_tensor *t, const char *name, int32_t dtype, int32_t 
                 return fail(GDN2_ERR_LAYOUT, "%s: token stride %lld is too large (64 rows must span under 2 GiB)",
                             name, (long long)t->stride[0]);
         }
-    } else if (layout == GATES) {
+    } else if (layout == GATES || layout == VECTORS) {
+        if (layout == VECTORS && t->shape[ndim - 1] > 1 && t->stride[ndim - 1] != 1)
+            return fail(GDN2_ERR_LAYOUT, "%s: the last dimension must be contiguous (stride %lld)", name,
+                        (long long)t->stride[ndim - 1]);
         for (int d = 0; d < ndim; ++d)
             if (t->shape[d] > 1 && t->stride[d] < 0)
                 return fail(GDN2_ERR_LAYOUT, "%s: dimension %d stride %lld must be non-negative", name, d,
@@ -117,7 +120,7 @@ int check_tensor(const gdn2_tensor *t, const char *name, int32_t dtype, int32_t 
     if (numel(t) > 0) {
         if (!t->data)
             return fail(GDN2_ERR_NULL_ARG, "%s: data is NULL but the tensor has elements", name);
-        const int64_t align = layout == GATES ? es : 16;
+        const int64_t align = layout == GATES || layout == VECTORS ? es : 16;
         if (reinterpret_cast<uintptr_t>(t->data) % align != 0)
             return fail(GDN2_ERR_LAYOUT, "%s: data pointer is not %lld-byte aligned", name, (long long)align);
     }
@@ -160,6 +163,31 @@ bool overlaps(const gdn2_tensor *a, const gdn2_tensor *b)
     if (na == 0 || nb == 0) return false;
     const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data), pb = reinterpret_cast<uintptr_t>(b->data);
     return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
+// A byte range as a tensor, for the overlap checks.
+static gdn2_tensor bytes_of(void *data, int64_t bytes)
+{
+    gdn2_tensor t = {};
+    t.data = data;
+    t.dtype = GDN2_DTYPE_F16;  // two bytes
+    t.ndim = 1;
+    t.shape[0] = bytes / 2;
+    t.stride[0] = 1;
+    return t;
+}
+
+int check_workspace(void *ws, int64_t have, int64_t need, const gdn2_tensor *const *ts, const char *const *names, int count)
+{
+    if (need == 0) return GDN2_OK;
+    if (!ws) return fail(GDN2_ERR_WORKSPACE, "workspace is NULL, %lld bytes are needed", (long long)need);
+    if (have < need)
+        return fail(GDN2_ERR_WORKSPACE, "workspace of %lld bytes is too small, %lld are needed", (long long)have, (long long)need);
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return fail(GDN2_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    const gdn2_tensor w = bytes_of(ws, need);
+    for (int i = 0; i < count; ++i)
+        if (overlaps(&w, ts[i])) return fail(GDN2_ERR_ALIAS, "workspace overlaps %s", names[i]);
+    return GDN2_OK;
 }
 
 int read_options(const gdn2_fwd_options *opts, Options *o)

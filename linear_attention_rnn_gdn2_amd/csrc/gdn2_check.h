@@ -24,18 +24,24 @@ enum Layout {
     ROWS,   // [tokens, heads, D]: the D elements of a row contiguous, token
             // and head strides free (non-negative, multiples of 16 bytes,
             // the token stride at least one row), rows 16-byte aligned
-    GATES   // [tokens, heads], read an element at a time: any non-negative
+    GATES,  // [tokens, heads], read an element at a time: any non-negative
             // strides, aligned to the element
+    VECTORS // [..., D]: the last dimension contiguous, the others' strides
+            // free and non-negative, aligned to the element
 };
 
 // Rank, dtype (one of two accepted: dtype2 < 0 for one), extents (-1 = any),
 // non-negative extents, layout, non-NULL data when non-empty, 16-byte
-// alignment (GATES: the element's).
+// alignment (GATES, VECTORS: the element's).
 int check_tensor(const gdn2_tensor *t, const char *name, int32_t dtype, int32_t dtype2, int ndim,
                  const int64_t *want, Layout layout = DENSE);
 // Whether the [tokens, heads, D] rows of a ROWS tensor are pairwise disjoint.
 bool rows_disjoint(const gdn2_tensor *t);
 bool overlaps(const gdn2_tensor *a, const gdn2_tensor *b);
+
+// A caller's workspace of `have` bytes: large enough, 256-byte aligned, apart
+// from every one of `count` tensors.
+int check_workspace(void *ws, int64_t have, int64_t need, const gdn2_tensor *const *ts, const char *const *names, int count);
 
 // Options: fields past struct_size keep their defaults, so that callers
 // built against an older, shorter struct keep working.

@@ -74,32 +74,6 @@ int check_sizes(const gdn2_tensor *q, const gdn2_tensor *v, const gdn2_tensor *c
 int64_t tok_stride(const gdn2_tensor *t) { return t->shape[0] > 1 ? t->stride[0] : t->ndim == 3 ? t->shape[2] : 0; }
 int64_t head_stride(const gdn2_tensor *t) { return t->shape[1] > 1 ? t->stride[1] : 0; }
 
-// A byte range as a tensor, for the overlap checks.
-gdn2_tensor bytes_of(void *data, int64_t bytes)
-{
-    gdn2_tensor t = {};
-    t.data = data;
-    t.dtype = GDN2_DTYPE_F16;  // two bytes
-    t.ndim = 1;
-    t.shape[0] = bytes / 2;
-    t.stride[0] = 1;
-    return t;
-}
-
-// The caller's workspace: large enough, 256-byte aligned, apart from every tensor.
-int check_workspace(void *ws, int64_t have, int64_t need, const gdn2_tensor *const *ts, const char *const *names, int count)
-{
-    if (need == 0) return GDN2_OK;
-    if (!ws) return fail(GDN2_ERR_WORKSPACE, "workspace is NULL, %lld bytes are needed", (long long)need);
-    if (have < need)
-        return fail(GDN2_ERR_WORKSPACE, "workspace of %lld bytes is too small, %lld are needed", (long long)have, (long long)need);
-    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return fail(GDN2_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-    const gdn2_tensor w = bytes_of(ws, need);
-    for (int i = 0; i < count; ++i)
-        if (overlaps(&w, ts[i])) return fail(GDN2_ERR_ALIAS, "workspace overlaps %s", names[i]);
-    return GDN2_OK;
-}
-
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
 // The forward's workspace: the records, then a split run's segments (the

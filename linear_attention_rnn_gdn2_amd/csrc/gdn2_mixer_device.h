@@ -1,0 +1,236 @@
+// Device helpers of the recurrence's and the convolution's kernels: elements
+// of any type one or two at a time, and where a wave is in a packed batch.
+// Not part of the ABI.
+//
+// Lanes own channels: a wave reads 64 (or 128, two per lane) neighbouring
+// channels of a token at once and walks along the tokens, so that a channel's
+// whole arithmetic stays in one lane.
+#pragma once
+
+#include <stdint.h>
+
+#include <type_traits>
+
+#include <hip/hip_runtime.h>
+
+#include "gdn2_device.h"
+#include "gdn2_index.h"
+#include "gdn2_mixer.h"
+
+namespace gdn2 {
+namespace dev {
+
+// VEC elements of type E as they lie in memory.
+template <int E, int VEC>
+using Raw = std::conditional_t<E == E_F32, std::conditional_t<VEC == 2, f32x2, float>,
+                               std::conditional_t<VEC == 2, uint32_t, uint16_t>>;
+template <int E>
+using Elem = std::conditional_t<E == E_F32, float, uint16_t>;
+
+template <int E>
+__device__ __forceinline__ float el_f32(uint16_t b)
+{
+    if constexpr (E == E_F16) return (float)__builtin_bit_cast(_Float16, b);
+    else return __uint_as_float((uint32_t)b << 16);
+}
+template <int E>
+__device__ __forceinline__ uint16_t f32_el(float x)  // rounded to nearest even
+{
+    if constexpr (E == E_F16) return __builtin_bit_cast(uint16_t, (_Float16)x);
+    else return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+template <int E, int VEC>
+__device__ __forceinline__ Raw<E, VEC> ld_raw(const void *p, int64_t row, uint32_t col)
+{
+    return *reinterpret_cast<const Raw<E, VEC> *>(static_cast<const Elem<E> *>(p) + row + col);
+}
+template <int E, int VEC>
+__device__ __forceinline__ void widen(Raw<E, VEC> r, float (&o)[VEC])
+{
+    if constexpr (E == E_F32) {
+        if constexpr (VEC == 2) {
+            o[0] = r[0];
+            o[1] = r[1];
+        } else {
+            o[0] = r;
+        }
+    } else if constexpr (VEC == 2) {
+        o[0] = el_f32<E>((uint16_t)r);
+        o[1] = el_f32<E>((uint16_t)(r >> 16));
+    } else {
+        o[0] = el_f32<E>(r);
+    }
+}
+template <int E, int VEC>
+__device__ __forceinline__ void st_el(void *p, int64_t row, uint32_t col, const float (&x)[VEC])
+{
+    Raw<E, VEC> r;
+    if constexpr (E == E_F32) {
+        if constexpr (VEC == 2) r = f32x2{x[0], x[1]};
+        else r = x[0];
+    } else if constexpr (VEC == 2) {
+        r = (uint32_t)f32_el<E>(x[0]) | (uint32_t)f32_el<E>(x[1]) << 16;
+    } else {
+        r = f32_el<E>(x[0]);
+    }
+    *reinterpret_cast<Raw<E, VEC> *>(static_cast<Elem<E> *>(p) + row + col) = r;
+}
+template <int E, int VEC>
+__device__ __forceinline__ void ld_el(const void *p, int64_t row, uint32_t col, float (&x)[VEC])
+{
+    widen<E, VEC>(ld_raw<E, VEC>(p, row, col), x);
+}
+// An element of one of two types (float32 or E).
+template <int E>
+__device__ __forceinline__ float ld_either(const void *p, bool f32, int64_t i)
+{
+    if constexpr (E == E_F32) return static_cast<const float *>(p)[i];
+    else return f32 ? static_cast<const float *>(p)[i] : el_f32<E>(static_cast<const uint16_t *>(p)[i]);
+}
+template <int E>
+__device__ __forceinline__ void st_either(void *p, bool f32, int64_t i, float x)
+{
+    if constexpr (E == E_F32) static_cast<float *>(p)[i] = x;
+    else if (f32) static_cast<float *>(p)[i] = x;
+    else static_cast<uint16_t *>(p)[i] = f32_el<E>(x);
+}
+
+// Workgroups are dealt to the eight XCDs in turn; this hands each XCD a run
+// of consecutive work items, so that neighbours in memory share an L2 (rows
+// that are not multiples of a cache line have lines in two workgroups).
+__device__ __forceinline__ uint32_t xcd_run(uint32_t id, uint32_t count)
+{
+    const uint32_t q = count / 8, r = count % 8, x = id % 8;
+    return x * q + (x < r ? x : r) + id / 8;
+}
+
+// A packed batch. Every token and sequence index that is derived from
+// cu_seqlens stays in [0, T] and [0, N), whatever the array holds.
+struct Packed {
+    const void *cu;
+    int cu64, N, T;
+    __device__ __forceinline__ int entry(int i) const  // cu[i], in [0, T]
+    {
+        const int64_t v = cu_raw(cu, cu64, i);
+        return (int)(v < 0 ? 0 : v > T ? T : v);
+    }
+    __device__ __forceinline__ int tokens() const { return cu ? entry(N) : T; }  // behind the last sequence's end: none
+    // The first sequence start at or behind token t (the last sequence's end if there is none). Wave-uniform.
+    __device__ __forceinline__ int start_from(int t) const
+    {
+        if (!cu) return t > 0 ? T : 0;
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = N;  // starts before lo lie before t, those from hi on do not
+        while (lo < hi) {
+            const int step = (hi - lo + 63) / 64, i = lo + lane * step;
+            const int c = __popcll(__ballot(i < hi && entry(i) < t));
+            if (c == 0) break;
+            const int last = lo + (c - 1) * step;
+            hi = step == 1 ? lo + c : last + step < hi ? last + step : hi;
+            lo = last + 1;
+        }
+        return entry(lo < N ? lo : N);
+    }
+};
+
+// The sequence of each token, for tokens in (mostly) rising order. A lane
+// holds the end of one of 64 sequences; all members are wave-uniform else.
+struct Cursor {
+    Packed b;
+    int base = 0, from = 0, win = 0;
+    bool held = false;
+
+    __device__ __forceinline__ explicit Cursor(const Packed &p) : b(p) {}
+    __device__ __forceinline__ void seek(int t)
+    {
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = b.N;  // sequences before lo end at or before t, those from hi on do not
+        while (hi - lo > 64) {
+            const int step = (hi - lo + 63) / 64, i = lo + lane * step;
+            const int c = __popcll(__ballot(i < hi && b.entry(i + 1) <= t));
+            if (c == 0) {
+                hi = lo;
+                break;
+            }
+            const int last = lo + (c - 1) * step;
+            hi = last + step < hi ? last + step : hi;
+            lo = last + 1;
+        }
+        base = lo;
+        from = t;
+        win = base + lane < b.N ? b.entry(base + lane + 1) : INT32_MAX;
+        held = true;
+    }
+    // The sequence that holds token t (t < tokens()).
+    __device__ __forceinline__ int at(int t)
+    {
+        if (!b.cu) return 0;
+        if (!held || t < from) seek(t);
+        int c = __popcll(__ballot(win <= t));
+        if (c == 64) {
+            seek(t);
+            c = __popcll(__ballot(win <= t));
+        }
+        return base + c < b.N ? base + c : b.N - 1;
+    }
+};
+
+// R tokens of one wave: [t0, t0 + cnt), which of them begin and end their
+// sequences (bits), and the sequence of token i in lane i.
+template <int R>
+struct Slice {
+    int t0, cnt, nn;
+    uint32_t starts, lasts;
+
+    __device__ __forceinline__ void set(Cursor &cur, int t, int hi, int tokens)
+    {
+        t0 = t;
+        cnt = hi - t < 0 ? 0 : hi - t < R ? hi - t : R;
+        starts = lasts = 0;
+        nn = 0;
+        if (cnt == 0) return;
+        if (!cur.b.cu) {
+            starts = t == 0;
+            lasts = t + cnt == tokens ? 1u << (cnt - 1) : 0;
+            return;
+        }
+        const int lane = threadIdx.x & 63;
+        int before = t > 0 ? cur.at(t - 1) : -1;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (i >= cnt) break;
+            const int n = cur.at(t + i);
+            if (n != before) {
+                starts |= 1u << i;
+                lasts |= i > 0 ? 1u << (i - 1) : 0;
+            }
+            nn = lane == i ? n : nn;
+            before = n;
+        }
+        if (t + cnt >= tokens || cur.at(t + cnt) != before) lasts |= 1u << (cnt - 1);
+    }
+    __device__ __forceinline__ int seq(int i) const { return __builtin_amdgcn_readlane(nn, i); }
+};
+
+// Calls f(n) for every empty sequence among a workgroup's share of all
+// sequences (share `part` of `parts`), each by one wave, with n wave-uniform.
+template <class F>
+__device__ __forceinline__ void for_empty(const Packed &b, uint32_t part, uint32_t parts, F f)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    if (!b.cu) {
+        if (b.T == 0 && part == 0 && wave == 0) f(0);
+        return;
+    }
+    const int n0 = (int)((int64_t)b.N * part / parts), n1 = (int)((int64_t)b.N * (part + 1) / parts);
+    for (int n = n0 + 64 * wave; n < n1; n += 64 * waves) {
+        uint64_t m = __ballot(n + lane < n1 && b.entry(n + lane) >= b.entry(n + lane + 1));
+        while (m) {
+            f(n + __builtin_ctzll(m));
+            m &= m - 1;
+        }
+    }
+}
+
+}  // namespace dev
+}  // namespace gdn2

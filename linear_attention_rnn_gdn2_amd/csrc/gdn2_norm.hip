@@ -1,0 +1,489 @@
+// Layer and RMS norm of rows with weight, bias and a SiLU gate, and their
+// gradients (CDNA4, gfx950). Per row x of D elements:
+//
+//     n = (x - mean) r, r = 1 / sqrt(var + eps)   or   n = x r, r = 1 / sqrt(mean x^2 + eps)
+//     q = n w + b,   y = q   or   q z sigmoid(z)
+//
+// and with s = z sigmoid(z), dq = dy s, m = dq w:
+//
+//     dz = dy q s'(z),   dw = sum over rows of dq n,   db = sum of dq,
+//     dx = r (m - mean m - n mean(m n))   or   r (m - n mean(m n))
+//
+// Bound by HBM: a row stays in the registers of the lanes that share it (8 to
+// 64 lanes, or a whole workgroup), is read once and written once; the
+// backward makes the row's statistics again from x, which it needs anyway.
+// A lane takes 16 bytes of each of its pieces. The variance is that of the
+// differences from the mean: waves that share a row exchange their own means
+// and squares about them (and, backward, sums of m and of m times the same
+// differences), which are joined without subtracting large sums.
+#include <stdint.h>
+
+#include <type_traits>
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/gdn2.h"
+#include "gdn2_mixer_device.h"
+
+namespace gdn2 {
+namespace {
+
+using namespace dev;
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + ex2(x * -1.44269504088896340736f)); }
+
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float x)  // over aligned groups of LANES lanes
+{
+    auto dpp = [&](auto ctrl) {
+        x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    if constexpr (LANES >= 2) dpp(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+    if constexpr (LANES >= 4) dpp(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+    if constexpr (LANES >= 8) dpp(std::integral_constant<int, 0x141>{});  // mirrored in 8
+    if constexpr (LANES >= 16) dpp(std::integral_constant<int, 0x140>{}); // mirrored in 16
+    if constexpr (LANES >= 32) x += __shfl_xor(x, 16);
+    if constexpr (LANES >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
+// A lane's piece of a row: P elements, 16 bytes, at any alignment of an
+// element. `valid` of them exist (0 past the row's end).
+template <int E>
+constexpr int PIECE = E == E_F32 ? 4 : 8;
+
+template <int E>
+struct Bits {
+    typedef uint16_t type __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Bits<E_F32> {
+    typedef float type __attribute__((ext_vector_type(4)));
+};
+
+template <int E>
+__device__ __forceinline__ typename Bits<E>::type ld_piece(const void *base, int64_t at, int valid)
+{
+    constexpr int P = PIECE<E>;
+    const Elem<E> *p = static_cast<const Elem<E> *>(base) + at;
+    typename Bits<E>::type r = {};
+    if (valid == P) {
+        __builtin_memcpy(&r, p, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < P - 1; ++i)
+            if (i < valid) r[i] = p[i];
+    }
+    return r;
+}
+template <int E>
+__device__ __forceinline__ void st_piece(void *base, int64_t at, int valid, const float (&x)[PIECE<E>])
+{
+    constexpr int P = PIECE<E>;
+    Elem<E> *p = static_cast<Elem<E> *>(base) + at;
+    typename Bits<E>::type r;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if constexpr (E == E_F32) r[i] = x[i];
+        else r[i] = f32_el<E>(x[i]);
+    }
+    if (valid == P) {
+        __builtin_memcpy(p, &r, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < P - 1; ++i)
+            if (i < valid) p[i] = r[i];
+    }
+}
+template <int E>
+__device__ __forceinline__ void widen_piece(typename Bits<E>::type r, float (&x)[PIECE<E>])
+{
+#pragma unroll
+    for (int i = 0; i < PIECE<E>; ++i) {
+        if constexpr (E == E_F32) x[i] = r[i];
+        else x[i] = el_f32<E>(r[i]);
+    }
+}
+
+// Rows as lanes see them: LPR lanes share a row, each with NV pieces LPR apart.
+template <int E, int LPR, int NV>
+struct Lanes {
+    static constexpr int P = PIECE<E>;
+    int sub, D;
+    __device__ __forceinline__ Lanes(const NormParams &p) : sub(threadIdx.x % LPR), D(p.D) {}
+    __device__ __forceinline__ int first(int k) const { return (k * LPR + sub) * P; }
+    __device__ __forceinline__ int valid(int k) const
+    {
+        const int n = D - first(k);
+        return n < 0 ? 0 : n < P ? n : P;
+    }
+};
+
+template <int E, int LPR, int NV>
+__device__ __forceinline__ void ld_vector(const Lanes<E, LPR, NV> &l, const void *v, bool f32, float absent, float (&o)[NV][PIECE<E>])
+{
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < PIECE<E>; ++i) o[k][i] = v && i < l.valid(k) ? ld_either<E>(v, f32, l.first(k) + i) : absent;
+}
+
+__device__ __forceinline__ int64_t row_at(const NormParams &p, int which, int64_t row)
+{
+    if (p.H == 1) return row * p.st[which];
+    const uint32_t r = (uint32_t)row, t = r / (uint32_t)p.H;
+    return (int64_t)t * p.st[which] + (int64_t)(r - t * (uint32_t)p.H) * p.sh[which];
+}
+
+// The statistics of a row whose lanes are W waves: count, mean and squares
+// about the mean of each wave are exchanged through LDS and joined.
+struct Stats {
+    float mean, rate;
+};
+
+// Sums over the lanes of a wave that share a row, then over the row's waves.
+template <int LPR>
+constexpr int WAVES = LPR <= 64 ? 1 : LPR / 64;
+template <int LPR>
+constexpr int WLANES = LPR < 64 ? LPR : 64;
+
+template <int E, int LPR, int NV>
+__device__ __forceinline__ void own_stats(const NormParams &p, const Lanes<E, LPR, NV> &l, const float (&x)[NV][PIECE<E>],
+                                          float &count, float &mean, float &sq)
+{
+    // of the lanes in this wave that share the row
+    float s = 0.0f, n = 0.0f;
+    mean = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) n += (float)l.valid(k);
+    if (LPR <= 64) count = (float)p.D;
+    else count = lane_sum<WLANES<LPR>>(n);
+    if (!p.rms) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < PIECE<E>; ++i) s += x[k][i];
+        s = lane_sum<WLANES<LPR>>(s);
+        mean = count > 0.0f ? s / count : 0.0f;
+    }
+    sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < PIECE<E>; ++i) {
+            const float d = i < l.valid(k) ? x[k][i] - mean : 0.0f;
+            sq = fmaf(d, d, sq);
+        }
+    sq = lane_sum<WLANES<LPR>>(sq);
+}
+
+template <int E, int LPR, int NV, int THREADS, bool GATE>
+__global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p)
+{
+    constexpr int P = PIECE<E>, RPB = THREADS / LPR, W = WAVES<LPR>;
+    __shared__ float part[2][THREADS / 64][4];
+    const Lanes<E, LPR, NV> l(p);
+    float w[NV][P], b[NV][P];
+    ld_vector(l, p.w, p.w_f32, 1.0f, w);
+    ld_vector(l, p.b, p.b_f32, 0.0f, b);
+    const int wave = threadIdx.x >> 6;
+    int buf = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB, buf ^= 1) {
+        const int64_t row = r0 + threadIdx.x / LPR;
+        const bool on = row < p.rows;
+        const int64_t rr = on ? row : p.rows - 1;
+        const int64_t xa = row_at(p, NORM_X, rr), ya = row_at(p, NORM_Y, rr), za = GATE ? row_at(p, NORM_Z, rr) : 0;
+        typename Bits<E>::type rx[NV], rz[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) rx[k] = ld_piece<E>(p.x, xa + l.first(k), l.valid(k));
+        if constexpr (GATE) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) rz[k] = ld_piece<E>(p.z, za + l.first(k), l.valid(k));
+        }
+        float x[NV][P];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) widen_piece<E>(rx[k], x[k]);
+        float count, mean, sq;
+        own_stats(p, l, x, count, mean, sq);
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                part[buf][wave][0] = count;
+                part[buf][wave][1] = mean;
+                part[buf][wave][2] = sq;
+            }
+            __syncthreads();
+            const int w0 = wave / W * W;
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) total = fmaf(part[buf][w0 + i][0], part[buf][w0 + i][1], total);
+            mean = total / (float)p.D;
+            sq = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = part[buf][w0 + i][1] - mean;
+                sq += fmaf(part[buf][w0 + i][0] * d, d, part[buf][w0 + i][2]);
+            }
+        }
+        const float rate = 1.0f / sqrtf(sq / (float)p.D + p.eps);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float y[P], z[P];
+            if constexpr (GATE) widen_piece<E>(rz[k], z);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                y[i] = fmaf((x[k][i] - mean) * rate, w[k][i], b[k][i]);
+                if constexpr (GATE) y[i] *= z[i] * sigmoid(z[i]);
+            }
+            if (on) st_piece<E>(p.y, ya + l.first(k), l.valid(k), y);
+        }
+    }
+}
+
+template <int E, int LPR, int NV, int THREADS, bool GATE>
+__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p)
+{
+    constexpr int P = PIECE<E>, RPB = THREADS / LPR, W = WAVES<LPR>;
+    __shared__ float part[2][THREADS / 64][6];
+    const Lanes<E, LPR, NV> l(p);
+    float w[NV][P], b[NV][P], dw[NV][P] = {}, db[NV][P] = {};
+    ld_vector(l, p.w, p.w_f32, 1.0f, w);
+    if constexpr (GATE) ld_vector(l, p.b, p.b_f32, 0.0f, b);
+    const int wave = threadIdx.x >> 6;
+    const float over = 1.0f / (float)p.D;
+    int buf = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB, buf ^= 1) {
+        const int64_t row = r0 + threadIdx.x / LPR;
+        const bool on = row < p.rows;
+        const int64_t rr = on ? row : p.rows - 1;
+        const int64_t xa = row_at(p, NORM_X, rr), da = row_at(p, NORM_DY, rr), za = GATE ? row_at(p, NORM_Z, rr) : 0;
+        typename Bits<E>::type rx[NV], rd[NV], rz[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            rx[k] = ld_piece<E>(p.x, xa + l.first(k), l.valid(k));
+            rd[k] = ld_piece<E>(p.dy, da + l.first(k), l.valid(k));
+        }
+        if constexpr (GATE) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) rz[k] = ld_piece<E>(p.z, za + l.first(k), l.valid(k));
+        }
+        float x[NV][P], dy[NV][P];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            widen_piece<E>(rx[k], x[k]);
+            widen_piece<E>(rd[k], dy[k]);
+        }
+        float count, mean, sq;
+        own_stats(p, l, x, count, mean, sq);
+        // sums of m and of m (x - mean), about this wave's mean
+        float sm = 0.0f, sx = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float z[P];
+            if constexpr (GATE) widen_piece<E>(rz[k], z);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float m = dy[k][i];
+                if constexpr (GATE) m *= z[i] * sigmoid(z[i]);
+                m = i < l.valid(k) ? __fmul_rn(m, w[k][i]) : 0.0f;
+                sm += m;
+                sx = fmaf(m, i < l.valid(k) ? x[k][i] - mean : 0.0f, sx);
+            }
+        }
+        sm = lane_sum<WLANES<LPR>>(sm);
+        sx = lane_sum<WLANES<LPR>>(sx);
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                part[buf][wave][0] = count;
+                part[buf][wave][1] = mean;
+                part[buf][wave][2] = sq;
+                part[buf][wave][3] = sm;
+                part[buf][wave][4] = sx;
+            }
+            __syncthreads();
+            const int w0 = wave / W * W;
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) total = fmaf(part[buf][w0 + i][0], part[buf][w0 + i][1], total);
+            mean = total / (float)p.D;
+            sq = sm = sx = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = part[buf][w0 + i][1] - mean;
+                sq += fmaf(part[buf][w0 + i][0] * d, d, part[buf][w0 + i][2]);
+                sm += part[buf][w0 + i][3];
+                sx += fmaf(d, part[buf][w0 + i][3], part[buf][w0 + i][4]);
+            }
+        }
+        const float rate = 1.0f / sqrtf(sq * over + p.eps);
+        const float m0 = p.rms ? 0.0f : sm * over, m1 = sx * rate * over;  // the means of m and of m n
+        const int64_t oa = row_at(p, NORM_Y, rr), ga = GATE ? row_at(p, NORM_DZ, rr) : 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float z[P], dx[P], dz[P];
+            if constexpr (GATE) widen_piece<E>(rz[k], z);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float n = (x[k][i] - mean) * rate;
+                float dq = dy[k][i];
+                if constexpr (GATE) {
+                    const float sg = sigmoid(z[i]);
+                    dz[i] = dq * fmaf(n, w[k][i], b[k][i]) * (sg * fmaf(z[i], 1.0f - sg, 1.0f));
+                    dq *= z[i] * sg;
+                }
+                // (m rounded as it was summed: in a row of one element m - mean m is 0)
+                const float m = __fmul_rn(dq, w[k][i]);
+                dx[i] = rate * ((m - m0) - n * m1);
+                if (on) {  // (the last row again in lanes past it)
+                    dw[k][i] = fmaf(dq, n, dw[k][i]);
+                    db[k][i] += dq;
+                }
+            }
+            if (on) {
+                st_piece<E>(p.y, oa + l.first(k), l.valid(k), dx);
+                if constexpr (GATE) st_piece<E>(p.dz, ga + l.first(k), l.valid(k), dz);
+            }
+        }
+    }
+    if (!p.part) return;
+    // the rows that the workgroup held side by side, joined in a fixed order
+    float *out = p.part + (int64_t)blockIdx.x * 2 * p.D;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (i < l.valid(k)) {
+                    out[l.first(k) + i] = dw[k][i];
+                    out[p.D + l.first(k) + i] = db[k][i];
+                }
+    } else {
+        constexpr int C = LPR * P;  // columns of one piece of all lanes
+        __shared__ float red[RPB][C + 4];
+        const int sub = threadIdx.x / LPR;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < P; ++i) red[sub][l.sub * P + i] = which ? db[k][i] : dw[k][i];
+                __syncthreads();
+                for (int c = threadIdx.x; c < C; c += THREADS) {
+                    float s = 0.0f;
+#pragma unroll 8
+                    for (int r = 0; r < RPB; ++r) s += red[r][c];
+                    if (k * C + c < p.D) out[(int64_t)which * p.D + k * C + c] = s;
+                }
+            }
+    }
+}
+
+// The workgroups' partial sums joined in a fixed order: 64 columns of dw or
+// db per workgroup, 16 waves.
+template <int E>
+__global__ __launch_bounds__(1024) void norm_dw_kernel(NormParams p)
+{
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, which = blockIdx.y;
+    const int c0 = blockIdx.x * 64 + lane, col = c0 < p.D ? c0 : p.D - 1;
+    float s = 0.0f;
+    for (int g0 = wave; g0 < p.groups; g0 += 128) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int g = g0 + 16 * i;
+            x[i] = g < p.groups ? p.part[((int64_t)g * 2 + which) * p.D + col] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[i];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c0 >= p.D) return;
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x += red[i][lane];
+    void *out = which ? p.db : p.dw;
+    if (out) st_either<E>(out, which ? p.b_f32 : p.w_f32, c0, x);
+}
+
+// f<E, LPR, NV, THREADS>() for the call's type and width.
+template <int E, class F>
+void for_width(int D, F f)
+{
+    auto go = [&](auto lpr, auto nv, auto threads) { f(std::integral_constant<int, E>{}, lpr, nv, threads); };
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 4> four{};
+    constexpr std::integral_constant<int, 256> t256{};
+    constexpr std::integral_constant<int, 512> t512{};
+    constexpr std::integral_constant<int, 1024> t1024{};
+    const int pieces = (D + PIECE<E> - 1) / PIECE<E>;
+    if (pieces <= 8) go(std::integral_constant<int, 8>{}, one, t256);
+    else if (pieces <= 16) go(std::integral_constant<int, 16>{}, one, t256);
+    else if (pieces <= 32) go(std::integral_constant<int, 32>{}, one, t256);
+    else if (pieces <= 64) go(std::integral_constant<int, 64>{}, one, t256);
+    else if (pieces <= 128) go(std::integral_constant<int, 64>{}, two, t256);
+    else if (pieces <= 512) go(t256, two, t256);
+    else if (pieces <= 1024) go(t512, two, t512);
+    else if (pieces <= 2048) go(t1024, two, t1024);
+    else go(t1024, four, t1024);
+}
+template <class F>
+hipError_t for_types(const NormParams &p, F f)
+{
+    if (p.io == E_F32) for_width<E_F32>(p.D, f);
+    else if (p.io == E_F16) for_width<E_F16>(p.D, f);
+    else for_width<E_BF16>(p.D, f);
+    return hipGetLastError();
+}
+// Rows that one workgroup holds side by side.
+int rows_per_group(int D, int io)
+{
+    int r = 1;
+    auto f = [&](auto, auto lpr, auto, auto threads) { r = threads() / lpr(); };
+    if (io == E_F32) for_width<E_F32>(D, f);
+    else for_width<E_BF16>(D, f);
+    return r;
+}
+
+constexpr int64_t FWD_GROUPS = 1 << 20, BWD_GROUPS = 1024;
+
+}  // namespace
+
+int32_t norm_bwd_groups(int64_t rows, int32_t D, int32_t io)
+{
+    const int64_t r = rows_per_group(D, io), b = (rows + r - 1) / r;
+    return (int32_t)(b < BWD_GROUPS ? b : BWD_GROUPS);
+}
+
+hipError_t launch_norm_fwd(const NormParams &p, hipStream_t stream)
+{
+    if (p.rows == 0) return hipSuccess;
+    const int64_t r = rows_per_group(p.D, p.io), b = (p.rows + r - 1) / r;
+    const dim3 grid((unsigned)(b < FWD_GROUPS ? b : FWD_GROUPS));
+    return for_types(p, [&](auto e, auto lpr, auto nv, auto threads) {
+        if (p.z) hipLaunchKernelGGL((norm_fwd_kernel<e(), lpr(), nv(), threads(), true>), grid, dim3(threads()), 0, stream, p);
+        else hipLaunchKernelGGL((norm_fwd_kernel<e(), lpr(), nv(), threads(), false>), grid, dim3(threads()), 0, stream, p);
+    });
+}
+
+hipError_t launch_norm_bwd(const NormParams &p, hipStream_t stream)
+{
+    if (p.rows > 0) {
+        const dim3 grid((unsigned)p.groups);
+        hipError_t e = for_types(p, [&](auto e, auto lpr, auto nv, auto threads) {
+            if (p.z) hipLaunchKernelGGL((norm_bwd_kernel<e(), lpr(), nv(), threads(), true>), grid, dim3(threads()), 0, stream, p);
+            else hipLaunchKernelGGL((norm_bwd_kernel<e(), lpr(), nv(), threads(), false>), grid, dim3(threads()), 0, stream, p);
+        });
+        if (e != hipSuccess) return e;
+    }
+    if (!p.dw && !p.db) return hipSuccess;
+    const dim3 grid((unsigned)((p.D + 63) / 64), 2);
+    if (p.io == E_F32) hipLaunchKernelGGL((norm_dw_kernel<E_F32>), grid, dim3(1024), 0, stream, p);
+    else if (p.io == E_F16) hipLaunchKernelGGL((norm_dw_kernel<E_F16>), grid, dim3(1024), 0, stream, p);
+    else hipLaunchKernelGGL((norm_dw_kernel<E_BF16>), grid, dim3(1024), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace gdn2

@@ -35,7 +35,15 @@ EXPORTED = ["gdn2_chunk_fwd", "gdn2_chunk_fwd_opts", "gdn2_chunk_fwd_noalloc", "
             "gdn2_delta_chunk_bwd", "gdn2_delta_chunk_bwd_check", "gdn2_delta_chunk_bwd_workspace",
             "gdn2_delta_recurrent_fwd", "gdn2_delta_recurrent_fwd_check",
             "gdn2_qk_norm_rope_fwd", "gdn2_qk_norm_rope_fwd_check",
-            "gdn2_qk_norm_rope_bwd", "gdn2_qk_norm_rope_bwd_check", "gdn2_qk_norm_rope_bwd_workspace"]
+            "gdn2_qk_norm_rope_bwd", "gdn2_qk_norm_rope_bwd_check", "gdn2_qk_norm_rope_bwd_workspace",
+            "gdn2_linear_scan_fwd", "gdn2_linear_scan_fwd_check", "gdn2_linear_scan_fwd_workspace",
+            "gdn2_linear_scan_recurrent_fwd", "gdn2_linear_scan_recurrent_fwd_check",
+            "gdn2_linear_scan_bwd", "gdn2_linear_scan_bwd_check", "gdn2_linear_scan_bwd_workspace",
+            "gdn2_short_conv_fwd", "gdn2_short_conv_fwd_check",
+            "gdn2_short_conv_recurrent_fwd", "gdn2_short_conv_recurrent_fwd_check",
+            "gdn2_short_conv_bwd", "gdn2_short_conv_bwd_check", "gdn2_short_conv_bwd_workspace",
+            "gdn2_layer_norm_fwd", "gdn2_layer_norm_fwd_check",
+            "gdn2_layer_norm_bwd", "gdn2_layer_norm_bwd_check", "gdn2_layer_norm_bwd_workspace"]
 
 
 class Gdn2Tensor(ctypes.Structure):
@@ -114,11 +122,31 @@ def load_library():
             "gdn2_qk_norm_rope_fwd_check": [A] * 8 + [A],
             "gdn2_qk_norm_rope_bwd": [A] * 12 + [A, A, I64, A],
             "gdn2_qk_norm_rope_bwd_check": [A] * 12 + [A],
+            "gdn2_linear_scan_fwd": [A] * 8 + [A, I64, A],
+            "gdn2_linear_scan_fwd_check": [A] * 8,
+            "gdn2_linear_scan_recurrent_fwd": [A] * 8 + [A],
+            "gdn2_linear_scan_recurrent_fwd_check": [A] * 8,
+            "gdn2_linear_scan_bwd": [A] * 12 + [A, I64, A],
+            "gdn2_linear_scan_bwd_check": [A] * 12,
+            "gdn2_short_conv_fwd": [A] * 8 + [A],
+            "gdn2_short_conv_fwd_check": [A] * 8,
+            "gdn2_short_conv_recurrent_fwd": [A] * 8 + [A],
+            "gdn2_short_conv_recurrent_fwd_check": [A] * 8,
+            "gdn2_short_conv_bwd": [A] * 12 + [A, I64, A],
+            "gdn2_short_conv_bwd_check": [A] * 12,
+            "gdn2_layer_norm_fwd": [A] * 6 + [A],
+            "gdn2_layer_norm_fwd_check": [A] * 6,
+            "gdn2_layer_norm_bwd": [A] * 10 + [A, I64, A],
+            "gdn2_layer_norm_bwd_check": [A] * 10,
         }.items():
             getattr(lib, name).argtypes, getattr(lib, name).restype = args, ctypes.c_int
         for name, args in {"gdn2_delta_chunk_fwd_workspace": [I64, I32, I32],
                            "gdn2_delta_chunk_bwd_workspace": [I64, I32, I32, I32, I32, I32],
-                           "gdn2_qk_norm_rope_bwd_workspace": [I64, I32, I32, I32]}.items():
+                           "gdn2_qk_norm_rope_bwd_workspace": [I64, I32, I32, I32],
+                           "gdn2_linear_scan_fwd_workspace": [I64, I32, I32],
+                           "gdn2_linear_scan_bwd_workspace": [I64, I32, I32],
+                           "gdn2_short_conv_bwd_workspace": [I64, I32, I32],
+                           "gdn2_layer_norm_bwd_workspace": [I64, I32, I32]}.items():
             getattr(lib, name).argtypes, getattr(lib, name).restype = args, I64
         lib.gdn2_last_error.argtypes = []
         lib.gdn2_last_error.restype = ctypes.c_char_p
@@ -643,3 +671,340 @@ def check_qk_norm_rope_bwd(q, k, dq_out, dk_out, norm="l2", eps=None, q_weight=N
                              g.get("dq_weight"), g.get("dk_weight")])
     opts = _qk_options(norm, eps, interleaved)
     return load_library().gdn2_qk_norm_rope_bwd_check(*d, ctypes.addressof(opts))
+
+
+# ------------------------------------- around the rule: recurrence, convolution, norm --
+
+INPUT_SCALES = {"none": 0, "convex": 1, "unit": 2}
+ACTIVATIONS = {"none": 0, "silu": 1}
+NORMS = {"layer": 0, "rms": 1}
+
+
+class Gdn2ScanOptions(ctypes.Structure):
+    """Mirror of ``gdn2_scan_options``."""
+    _fields_ = [("struct_size", ctypes.c_int32), ("input_scale", ctypes.c_int32)]
+
+
+class Gdn2ConvOptions(ctypes.Structure):
+    """Mirror of ``gdn2_conv_options``."""
+    _fields_ = [("struct_size", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class Gdn2NormOptions(ctypes.Structure):
+    """Mirror of ``gdn2_norm_options``."""
+    _fields_ = [("struct_size", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+def _choice(what, names, value):
+    if value not in names:
+        raise ValueError(f"{what} must be one of {', '.join(map(repr, names))}, not {value!r}")
+    return names[value]
+
+
+@functools.lru_cache(maxsize=None)
+def _scan_options(input_scale):
+    return Gdn2ScanOptions(ctypes.sizeof(Gdn2ScanOptions), _choice("input_scale", INPUT_SCALES, input_scale))
+
+
+@functools.lru_cache(maxsize=None)
+def _conv_options(activation):
+    return Gdn2ConvOptions(ctypes.sizeof(Gdn2ConvOptions), _choice("activation", ACTIVATIONS, activation))
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_options(norm, eps):
+    return Gdn2NormOptions(ctypes.sizeof(Gdn2NormOptions), _choice("norm", NORMS, norm), float(eps or 0.0))
+
+
+def _rank2(**tensors):
+    for name, t in tensors.items():
+        if t.dim() != 2:
+            raise ValueError(f"{name} must have 2 dimensions, not {t.dim()}")
+
+
+def _sequences(cu_seqlens):
+    return 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+
+
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+_SCAN_NAMES = ("x", "g", "w", "initial_state", "cu_seqlens", "out", "final_state")
+SCAN_GRADS = ("dx", "dg", "dw", "d_initial_state")
+
+
+def linear_scan_fwd_workspace(T, N, D):
+    """Bytes of workspace of :func:`linear_scan_fwd`."""
+    return load_library().gdn2_linear_scan_fwd_workspace(int(T), int(N), int(D))
+
+
+def linear_scan_bwd_workspace(T, N, D):
+    """Bytes of workspace of :func:`linear_scan_bwd`."""
+    return load_library().gdn2_linear_scan_bwd_workspace(int(T), int(N), int(D))
+
+
+def _scan_outputs(x, g, w, initial_state, cu_seqlens, output_final_state, out, final_state):
+    dev = _one_device(_SCAN_NAMES, (x, g, w, initial_state, cu_seqlens, out, final_state))
+    _rank2(x=x, g=g)
+    N = _sequences(cu_seqlens)
+    if out is None:
+        out = _like(x)
+    if final_state is None and output_final_state and N >= 1:
+        final_state = torch.empty((N, x.shape[1]), dtype=torch.float32, device=dev)
+    return dev, N, out, final_state
+
+
+def linear_scan_fwd(x, g, w=None, initial_state=None, cu_seqlens=None, output_final_state=True, input_scale="none",
+                    out=None, final_state=None, workspace=None):
+    """The gated linear recurrence per channel, on the current HIP stream:
+    h = e^g h + m w x, out = h, with m = 1 (``input_scale`` "none"), 1 - e^g
+    ("convex") or sqrt(1 - e^(2 g)) ("unit").
+
+    x, w, out [T, D]: bf16, float16 or float32 (x's type), rows with any
+    token stride; g [T, D]: float32 or x's type, <= 0; states [N, D]: float32
+    or bf16; cu_seqlens as in :func:`chunk_fwd`. Returns (out, final_state or
+    None). ``workspace``: a contiguous device tensor of at least
+    ``linear_scan_fwd_workspace(T, N, D)`` bytes (None: taken from torch's
+    allocator).
+    """
+    lib = load_library()
+    opts = _scan_options(input_scale)
+    dev, N, out, final_state = _scan_outputs(x, g, w, initial_state, cu_seqlens, output_final_state, out, final_state)
+    ws = _workspace(lib.gdn2_linear_scan_fwd_workspace(x.shape[0], N, x.shape[1]), workspace, dev)
+    keep, d = _describe_all([x, g, w, initial_state, cu_seqlens, out, final_state])
+    _launch(dev, lambda stream: lib.gdn2_linear_scan_fwd(*d, ctypes.addressof(opts), *_ws_args(ws), stream))
+    return out, final_state
+
+
+def linear_scan_recurrent_fwd(x, g, w=None, initial_state=None, cu_seqlens=None, output_final_state=True,
+                              input_scale="none", out=None, final_state=None):
+    """:func:`linear_scan_fwd` evaluated token by token (decode and short
+    spans). ``final_state`` may be ``initial_state`` itself to update the
+    state in place."""
+    lib = load_library()
+    opts = _scan_options(input_scale)
+    dev, _, out, final_state = _scan_outputs(x, g, w, initial_state, cu_seqlens, output_final_state, out, final_state)
+    keep, d = _describe_all([x, g, w, initial_state, cu_seqlens, out, final_state])
+    _launch(dev, lambda stream: lib.gdn2_linear_scan_recurrent_fwd(*d, ctypes.addressof(opts), stream))
+    return out, final_state
+
+
+def linear_scan_bwd(x, g, w, d_out, initial_state=None, cu_seqlens=None, d_final_state=None, need_d_initial_state=True,
+                    input_scale="none", grads=None, workspace=None):
+    """Backward of :func:`linear_scan_fwd`: a dict with dx, dw (None without
+    w) in x's type, dg in g's and d_initial_state (float32 [N, D], or None
+    when not requested). d_final_state: float32 or None (zero). Tensors given
+    in ``grads`` are written in place. ``workspace``: at least
+    ``linear_scan_bwd_workspace(T, N, D)`` bytes."""
+    lib = load_library()
+    opts = _scan_options(input_scale)
+    out = dict(grads or {})
+    ins = [x, g, w, initial_state, cu_seqlens, d_out, d_final_state]
+    dev = _one_device(_SCAN_NAMES[:5] + ("d_out", "d_final_state") + SCAN_GRADS, ins + [out.get(n) for n in SCAN_GRADS])
+    _rank2(x=x, g=g)
+    N = _sequences(cu_seqlens)
+    for n, t in (("dx", x), ("dg", g), ("dw", w)):
+        if out.get(n) is None:
+            out[n] = None if t is None else _like(t)
+    if out.get("d_initial_state") is None:
+        need = need_d_initial_state and N >= 1
+        out["d_initial_state"] = torch.empty((N, x.shape[1]), dtype=torch.float32, device=dev) if need else None
+    ws = _workspace(lib.gdn2_linear_scan_bwd_workspace(x.shape[0], N, x.shape[1]), workspace, dev)
+    keep, d = _describe_all(ins + [out[n] for n in SCAN_GRADS])
+    _launch(dev, lambda stream: lib.gdn2_linear_scan_bwd(*d, ctypes.addressof(opts), *_ws_args(ws), stream))
+    return out
+
+
+def check_linear_scan(x, g, w=None, initial_state=None, cu_seqlens=None, out=None, final_state=None, input_scale="none",
+                      recurrent=False):
+    """The library's host-side validation of a :func:`linear_scan_fwd` or
+    (``recurrent``) :func:`linear_scan_recurrent_fwd` call only (no GPU
+    needed): the status code."""
+    lib = load_library()
+    keep, d = _describe_all([x, g, w, initial_state, cu_seqlens, out, final_state])
+    fn = lib.gdn2_linear_scan_recurrent_fwd_check if recurrent else lib.gdn2_linear_scan_fwd_check
+    return fn(*d, ctypes.addressof(_scan_options(input_scale)))
+
+
+def check_linear_scan_bwd(x, g, w, d_out, initial_state=None, cu_seqlens=None, d_final_state=None, input_scale="none",
+                          grads=None):
+    """The library's host-side validation of a :func:`linear_scan_bwd` call only (no GPU needed)."""
+    gr = grads or {}
+    keep, d = _describe_all([x, g, w, initial_state, cu_seqlens, d_out, d_final_state] + [gr.get(n) for n in SCAN_GRADS])
+    return load_library().gdn2_linear_scan_bwd_check(*d, ctypes.addressof(_scan_options(input_scale)))
+
+
+_CONV_NAMES = ("x", "weight", "bias", "initial_state", "cu_seqlens", "out", "final_state")
+CONV_GRADS = ("dx", "dweight", "dbias", "d_initial_state")
+
+
+def _conv_outputs(x, weight, bias, initial_state, cu_seqlens, output_final_state, out, final_state):
+    dev = _one_device(_CONV_NAMES, (x, weight, bias, initial_state, cu_seqlens, out, final_state))
+    _rank2(x=x, weight=weight)
+    N = _sequences(cu_seqlens)
+    if out is None:
+        out = _like(x)
+    if final_state is None and output_final_state and N >= 1 and weight.shape[1] >= 1:
+        final_state = torch.empty((N, weight.shape[1] - 1, x.shape[1]), dtype=x.dtype, device=dev)
+    return dev, out, final_state
+
+
+def short_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, output_final_state=True, activation="silu",
+                   out=None, final_state=None):
+    """The short causal convolution per channel, on the current HIP stream:
+    p_t = bias + sum_j weight[:, j] x_{t - (K - 1) + j} over each sequence,
+    out = p ("none") or p sigmoid(p) (``activation`` "silu").
+
+    x, out [T, D]: bf16, float16 or float32, rows with any token stride;
+    weight [D, K] (K 2 to 4) and bias [D]: float32 or x's type; states
+    [N, K - 1, D] in x's type: the inputs before the first token, the oldest
+    first (None: zeros), and the last K - 1 inputs; cu_seqlens as in
+    :func:`chunk_fwd`. Returns (out, final_state or None).
+    """
+    lib = load_library()
+    opts = _conv_options(activation)
+    dev, out, final_state = _conv_outputs(x, weight, bias, initial_state, cu_seqlens, output_final_state, out, final_state)
+    keep, d = _describe_all([x, weight, bias, initial_state, cu_seqlens, out, final_state])
+    _launch(dev, lambda stream: lib.gdn2_short_conv_fwd(*d, ctypes.addressof(opts), stream))
+    return out, final_state
+
+
+def short_conv_recurrent_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, output_final_state=True,
+                             activation="silu", out=None, final_state=None):
+    """:func:`short_conv_fwd` evaluated token by token (decode and short
+    spans). ``final_state`` may be ``initial_state`` itself to update the
+    state in place."""
+    lib = load_library()
+    opts = _conv_options(activation)
+    dev, out, final_state = _conv_outputs(x, weight, bias, initial_state, cu_seqlens, output_final_state, out, final_state)
+    keep, d = _describe_all([x, weight, bias, initial_state, cu_seqlens, out, final_state])
+    _launch(dev, lambda stream: lib.gdn2_short_conv_recurrent_fwd(*d, ctypes.addressof(opts), stream))
+    return out, final_state
+
+
+def short_conv_bwd_workspace(T, D, K):
+    """Bytes of workspace of :func:`short_conv_bwd`."""
+    return load_library().gdn2_short_conv_bwd_workspace(int(T), int(D), int(K))
+
+
+def short_conv_bwd(x, weight, bias, d_out, initial_state=None, cu_seqlens=None, d_final_state=None,
+                   need_d_initial_state=True, activation="silu", grads=None, workspace=None):
+    """Backward of :func:`short_conv_fwd`: a dict with dx and d_initial_state
+    (x's type; the second None when not requested), dweight and dbias (the
+    weight's type, dbias None without bias). Tensors given in ``grads`` are
+    written in place. ``workspace``: at least ``short_conv_bwd_workspace(T, D,
+    K)`` bytes."""
+    lib = load_library()
+    opts = _conv_options(activation)
+    out = dict(grads or {})
+    ins = [x, weight, bias, initial_state, cu_seqlens, d_out, d_final_state]
+    dev = _one_device(_CONV_NAMES[:5] + ("d_out", "d_final_state") + CONV_GRADS, ins + [out.get(n) for n in CONV_GRADS])
+    _rank2(x=x, weight=weight)
+    N, (T, D), K = _sequences(cu_seqlens), x.shape, weight.shape[1]
+    for n, t in (("dx", x), ("dweight", weight), ("dbias", bias)):
+        if out.get(n) is None:
+            out[n] = None if t is None else _like(t)
+    if out.get("d_initial_state") is None:
+        need = need_d_initial_state and N >= 1 and K >= 1
+        out["d_initial_state"] = torch.empty((N, K - 1, D), dtype=x.dtype, device=dev) if need else None
+    ws = _workspace(lib.gdn2_short_conv_bwd_workspace(T, D, K), workspace, dev)
+    keep, d = _describe_all(ins + [out[n] for n in CONV_GRADS])
+    _launch(dev, lambda stream: lib.gdn2_short_conv_bwd(*d, ctypes.addressof(opts), *_ws_args(ws), stream))
+    return out
+
+
+def check_short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, out=None, final_state=None,
+                     activation="silu", recurrent=False):
+    """The library's host-side validation of a :func:`short_conv_fwd` or
+    (``recurrent``) :func:`short_conv_recurrent_fwd` call only (no GPU
+    needed): the status code."""
+    lib = load_library()
+    keep, d = _describe_all([x, weight, bias, initial_state, cu_seqlens, out, final_state])
+    fn = lib.gdn2_short_conv_recurrent_fwd_check if recurrent else lib.gdn2_short_conv_fwd_check
+    return fn(*d, ctypes.addressof(_conv_options(activation)))
+
+
+def check_short_conv_bwd(x, weight, bias, d_out, initial_state=None, cu_seqlens=None, d_final_state=None,
+                         activation="silu", grads=None):
+    """The library's host-side validation of a :func:`short_conv_bwd` call only (no GPU needed)."""
+    gr = grads or {}
+    keep, d = _describe_all([x, weight, bias, initial_state, cu_seqlens, d_out, d_final_state]
+                            + [gr.get(n) for n in CONV_GRADS])
+    return load_library().gdn2_short_conv_bwd_check(*d, ctypes.addressof(_conv_options(activation)))
+
+
+_NORM_NAMES = ("x", "gate", "weight", "bias", "out")
+NORM_GRADS = ("dx", "dgate", "dweight", "dbias")
+
+
+def _rows3(t):
+    """A tensor of rows [T, D] as one head's, [T, 1, D]."""
+    return t.unsqueeze(1) if t is not None and t.dim() == 2 else t
+
+
+def _norm_rank(x):
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must have 2 or 3 dimensions, not {x.dim()}")
+
+
+def layer_norm(x, weight=None, bias=None, gate=None, norm="layer", eps=None, out=None):
+    """The norm of rows, on the current HIP stream: ``norm`` "layer" ((x -
+    mean) / sqrt(var + eps), eps 1e-5) or "rms" (x / sqrt(mean x^2 + eps), eps
+    1e-6), times weight, plus bias, times gate sigmoid(gate).
+
+    x, gate, out [T, H, D] or [T, D] (D up to 16384): bf16, float16 or
+    float32, strided rows accepted; weight, bias [D]: float32 or x's type.
+    Returns out.
+    """
+    lib = load_library()
+    opts = _norm_options(norm, eps)
+    dev = _one_device(_NORM_NAMES, (x, gate, weight, bias, out))
+    _norm_rank(x)
+    if out is None:
+        out = _like(x)
+    keep, d = _describe_all([_rows3(x), _rows3(gate), weight, bias, _rows3(out)])
+    _launch(dev, lambda stream: lib.gdn2_layer_norm_fwd(*d, ctypes.addressof(opts), stream))
+    return out
+
+
+def layer_norm_bwd_workspace(T, H, D):
+    """Bytes of workspace of :func:`layer_norm_bwd` with a weight's or bias's gradient."""
+    return load_library().gdn2_layer_norm_bwd_workspace(int(T), int(H), int(D))
+
+
+def layer_norm_bwd(x, d_out, weight=None, bias=None, gate=None, norm="layer", eps=None, grads=None, workspace=None):
+    """Backward of :func:`layer_norm`: a dict with dx, dgate (x's shape and
+    type), dweight and dbias (their tensors' types), None for an argument that
+    is None. Tensors given in ``grads`` are written in place. ``workspace``:
+    at least ``layer_norm_bwd_workspace(T, H, D)`` bytes."""
+    lib = load_library()
+    opts = _norm_options(norm, eps)
+    out = dict(grads or {})
+    dev = _one_device(("x", "gate", "weight", "bias", "d_out") + NORM_GRADS,
+                      [x, gate, weight, bias, d_out] + [out.get(n) for n in NORM_GRADS])
+    _norm_rank(x)
+    for n, t in (("dx", x), ("dgate", gate), ("dweight", weight), ("dbias", bias)):
+        if out.get(n) is None:
+            out[n] = None if t is None else _like(t)
+    sums = out["dweight"] is not None or out["dbias"] is not None
+    heads = 1 if x.dim() == 2 else x.shape[1]
+    ws = _workspace(lib.gdn2_layer_norm_bwd_workspace(x.shape[0], heads, x.shape[-1]) if sums else 0, workspace, dev)
+    keep, d = _describe_all([_rows3(x), _rows3(gate), weight, bias, _rows3(d_out), _rows3(out["dx"]), _rows3(out["dgate"]),
+                             out["dweight"], out["dbias"]])
+    _launch(dev, lambda stream: lib.gdn2_layer_norm_bwd(*d, ctypes.addressof(opts), *_ws_args(ws), stream))
+    return out
+
+
+def check_layer_norm(x, weight=None, bias=None, gate=None, norm="layer", eps=None, out=None):
+    """The library's host-side validation of a :func:`layer_norm` call only (no GPU needed)."""
+    keep, d = _describe_all([_rows3(x), _rows3(gate), weight, bias, _rows3(out)])
+    return load_library().gdn2_layer_norm_fwd_check(*d, ctypes.addressof(_norm_options(norm, eps)))
+
+
+def check_layer_norm_bwd(x, d_out, weight=None, bias=None, gate=None, norm="layer", eps=None, grads=None):
+    """The library's host-side validation of a :func:`layer_norm_bwd` call only (no GPU needed)."""
+    g = grads or {}
+    keep, d = _describe_all([_rows3(x), _rows3(gate), weight, bias, _rows3(d_out), _rows3(g.get("dx")),
+                             _rows3(g.get("dgate")), g.get("dweight"), g.get("dbias")])
+    return load_library().gdn2_layer_norm_bwd_check(*d, ctypes.addressof(_norm_options(norm, eps)))
