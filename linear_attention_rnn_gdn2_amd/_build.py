@@ -18,8 +18,8 @@ SOURCES = [os.path.join(HERE, "csrc", "gdn2_api.cpp"), os.path.join(HERE, "csrc"
            os.path.join(HERE, "csrc", "gdn2_delta_api.cpp"), os.path.join(HERE, "csrc", "gdn2_delta_fwd.hip"),
            os.path.join(HERE, "csrc", "gdn2_delta_bwd.hip"), os.path.join(HERE, "csrc", "gdn2_delta_step.hip"),
            os.path.join(HERE, "csrc", "gdn2_qk.hip"), os.path.join(HERE, "csrc", "gdn2_mixer_api.cpp"),
-           os.path.join(HERE, "csrc", "gdn2_scan.hip"), os.path.join(HERE, "csrc", "gdn2_conv.hip"),
-           os.path.join(HERE, "csrc", "gdn2_norm.hip")]
+           os.path.join(HERE, "csrc", "gdn2_scan_fwd.hip"), os.path.join(HERE, "csrc", "gdn2_scan_bwd.hip"),
+           os.path.join(HERE, "csrc", "gdn2_conv.hip"), os.path.join(HERE, "csrc", "gdn2_norm.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

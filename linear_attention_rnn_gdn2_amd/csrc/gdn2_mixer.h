@@ -12,8 +12,8 @@ namespace gdn2 {
 
 enum { E_BF16 = 0, E_F16 = 1, E_F32 = 2 };  // element types of these operators
 
-// Tokens of a tile of the recurrence's split run and of its gradients: what
-// one workgroup joins (8 waves of 8 tokens).
+// Tokens of a tile of the recurrence's gradients: what one workgroup joins (8
+// waves of 8 tokens).
 constexpr int SCAN_TILE = 64;
 
 struct ScanParams {
@@ -28,14 +28,15 @@ struct ScanParams {
     int32_t io, g_f32, cu64, h0_bf16, ht_bf16;
     int32_t scale;          // GDN2_SCAN_INPUT_*
     int32_t vec2;           // rows may be read two elements at a time
-    int32_t groups;         // whole-sequence groups (0: tiles, with enter)
-    // workspace: per tile and channel the sum of its g (infinity: a sequence
-    // begins in the tile), its end state from zero, and (backward) the
-    // gradient that leaves it towards the token before it; the join replaces
-    // the last two by the state that enters the tile and the gradient that
-    // reaches it from behind
-    float *sums, *end, *back;
-    int32_t tiles;
+    int32_t groups;         // whole-sequence groups (0: two passes)
+    // workspace: per tile (a range of 8 chunks forward, SCAN_TILE tokens
+    // backward) and channel the sum of its g (infinity: a sequence begins in
+    // it), its end state from zero, and (backward) the gradient that leaves it
+    // towards the token before it; the join replaces the last two by the state
+    // that enters the tile and the gradient that reaches it from behind.
+    // Forward: the same of every chunk too, as the first pass leaves it.
+    float *sums, *end, *back, *chunk_sums, *chunk_end;
+    int32_t tiles, chunk;
     // backward
     const void *dout;       // [T, D] io
     const float *dht;       // [N, D] or nullptr
@@ -44,12 +45,20 @@ struct ScanParams {
     int64_t sdo, sdx, sdw, sdg;
 };
 
-// How a forward call runs: the number of whole-sequence groups (0: tiles).
+// How a forward call runs: the number of whole-sequence groups (0: in two
+// passes over chunks of scan_chunk() tokens, eight of them to a range).
 int32_t scan_groups(int64_t T, int64_t N, int64_t D);
+int32_t scan_chunk(int64_t T, int64_t D);
+inline int64_t scan_ranges(int64_t T, int64_t D)
+{
+    const int64_t r = 8 * scan_chunk(T, D);
+    return (T + r - 1) / r;
+}
 inline int64_t scan_tiles(int64_t T) { return (T + SCAN_TILE - 1) / SCAN_TILE; }
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t stream);
 hipError_t launch_scan_step(const ScanParams &p, hipStream_t stream);
 hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t stream);
+hipError_t launch_scan_join(const ScanParams &p, bool bwd, hipStream_t stream);
 
 struct ConvParams {
     const void *x;          // [T, D] io

@@ -115,14 +115,21 @@ enum Form { SCAN, STEP, BACK };
 
 // Byte offsets of the recurrence's workspace.
 struct ScanSpace {
-    int64_t sums, end, back, total;
+    int64_t sums, end, back, chunk_sums, chunk_end, total = 0;
     ScanSpace(int64_t T, int64_t D, bool bwd)
     {
-        const int64_t one = up256(gdn2::scan_tiles(T) * D * 4);
-        sums = 0;
-        end = one;
-        back = 2 * one;
-        total = (bwd ? 3 : 2) * one;
+        const int64_t tile = up256((bwd ? gdn2::scan_tiles(T) : gdn2::scan_ranges(T, D)) * D * 4);
+        const int64_t chunk = bwd ? 0 : up256(8 * gdn2::scan_ranges(T, D) * D * 4);
+        auto take = [&](int64_t bytes) {
+            const int64_t o = total;
+            total += bytes;
+            return o;
+        };
+        sums = take(tile);
+        end = take(tile);
+        back = take(bwd ? tile : 0);
+        chunk_sums = take(chunk);
+        chunk_end = take(chunk);
     }
 };
 
@@ -193,11 +200,14 @@ int validate(const Scan &a, Form form, void *ws, int64_t ws_bytes, ScanParams *p
     p->h0_bf16 = a.h0 && a.h0->dtype == GDN2_DTYPE_BF16;
     p->scale = scale;
     p->vec2 = D % 2 == 0 && in_pairs(a.x) && in_pairs(a.g) && in_pairs(a.w) && in_pairs(a.out);
-    p->tiles = (int32_t)gdn2::scan_tiles(T);
+    p->chunk = gdn2::scan_chunk(T, D);
+    p->tiles = (int32_t)(back ? gdn2::scan_tiles(T) : gdn2::scan_ranges(T, D));
     const ScanSpace space(T, D, back);
     char *b = static_cast<char *>(ws);
     p->sums = reinterpret_cast<float *>(b + space.sums);
     p->end = reinterpret_cast<float *>(b + space.end);
+    p->chunk_sums = reinterpret_cast<float *>(b + space.chunk_sums);
+    p->chunk_end = reinterpret_cast<float *>(b + space.chunk_end);
     if (back) {
         p->back = reinterpret_cast<float *>(b + space.back);
         p->dout = a.out->data;

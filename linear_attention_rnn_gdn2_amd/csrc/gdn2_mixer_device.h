@@ -44,6 +44,19 @@ __device__ __forceinline__ Raw<E, VEC> ld_raw(const void *p, int64_t row, uint32
 {
     return *reinterpret_cast<const Raw<E, VEC> *>(static_cast<const Elem<E> *>(p) + row + col);
 }
+// R rows from t0 on (those from hi on read row hi - 1).
+template <int E, int VEC, int R>
+__device__ __forceinline__ void ld_rows(const void *p, int64_t stride, int t0, int hi, uint32_t col, Raw<E, VEC> (&r)[R])
+{
+    if (t0 + R <= hi) {
+        int64_t row = t0 * stride;
+#pragma unroll
+        for (int i = 0; i < R; ++i, row += stride) r[i] = ld_raw<E, VEC>(p, row, col);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) r[i] = ld_raw<E, VEC>(p, (int64_t)(t0 + i < hi ? t0 + i : hi - 1) * stride, col);
+    }
+}
 template <int E, int VEC>
 __device__ __forceinline__ void widen(Raw<E, VEC> r, float (&o)[VEC])
 {
@@ -131,6 +144,20 @@ struct Packed {
         }
         return entry(lo < N ? lo : N);
     }
+    // The tokens of the sequence of a rank by length, the longest first (N <= 64).
+    __device__ __forceinline__ void by_length(int rank, int &lo, int &hi) const
+    {
+        const int lane = threadIdx.x & 63;
+        const int s = lane < N ? entry(lane) : 0, e = lane < N ? entry(lane + 1) : 0, len = e > s ? e - s : 0;
+        int before = 0;
+        for (int j = 0; j < N; ++j) {
+            const int l = __builtin_amdgcn_readlane(len, j);
+            before += l > len || (l == len && j < lane);
+        }
+        const int n = __builtin_ctzll(__ballot(lane < N && before == rank));
+        lo = __builtin_amdgcn_readlane(s, n);
+        hi = lo + __builtin_amdgcn_readlane(len, n);
+    }
 };
 
 // The sequence of each token, for tokens in (mostly) rising order. A lane
@@ -139,6 +166,7 @@ struct Cursor {
     Packed b;
     int base = 0, from = 0, win = 0;
     bool held = false;
+    int n_in = 0, b_in = 0, e_in = 0;  // tokens b_in .. e_in - 1 are known to lie in sequence n_in
 
     __device__ __forceinline__ explicit Cursor(const Packed &p) : b(p) {}
     __device__ __forceinline__ void seek(int t)
@@ -173,6 +201,13 @@ struct Cursor {
         }
         return base + c < b.N ? base + c : b.N - 1;
     }
+    // Remembers that token t lies in sequence n (n = at(t)).
+    __device__ __forceinline__ void inside(int n, int t)
+    {
+        n_in = n;
+        b_in = t;
+        e_in = n - base < 64 ? __builtin_amdgcn_readlane(win, n - base) : 0;
+    }
 };
 
 // R tokens of one wave: [t0, t0 + cnt), which of them begin and end their
@@ -194,6 +229,10 @@ struct Slice {
             lasts = t + cnt == tokens ? 1u << (cnt - 1) : 0;
             return;
         }
+        if (t > cur.b_in && t + R < cur.e_in) {  // well inside a sequence
+            nn = cur.n_in;
+            return;
+        }
         const int lane = threadIdx.x & 63;
         int before = t > 0 ? cur.at(t - 1) : -1;
 #pragma unroll
@@ -208,6 +247,7 @@ struct Slice {
             before = n;
         }
         if (t + cnt >= tokens || cur.at(t + cnt) != before) lasts |= 1u << (cnt - 1);
+        cur.inside(before, t + cnt - 1);
     }
     __device__ __forceinline__ int seq(int i) const { return __builtin_amdgcn_readlane(nn, i); }
 };

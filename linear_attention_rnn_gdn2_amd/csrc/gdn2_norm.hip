@@ -122,10 +122,23 @@ struct Lanes {
 template <int E, int LPR, int NV>
 __device__ __forceinline__ void ld_vector(const Lanes<E, LPR, NV> &l, const void *v, bool f32, float absent, float (&o)[NV][PIECE<E>])
 {
+    constexpr int P = PIECE<E>;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        if (!v) {
 #pragma unroll
-        for (int i = 0; i < PIECE<E>; ++i) o[k][i] = v && i < l.valid(k) ? ld_either<E>(v, f32, l.first(k) + i) : absent;
+            for (int i = 0; i < P; ++i) o[k][i] = absent;
+        } else if (E == E_F32 || f32) {
+#pragma unroll
+            for (int h = 0; h < P / 4; ++h) {
+                const f32x4 x = ld_piece<E_F32>(v, l.first(k) + 4 * h, min(4, max(0, l.valid(k) - 4 * h)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[k][4 * h + i] = x[i];
+            }
+        } else {
+            widen_piece<E>(ld_piece<E>(v, l.first(k), l.valid(k)), o[k]);
+        }
+    }
 }
 
 __device__ __forceinline__ int64_t row_at(const NormParams &p, int which, int64_t row)
@@ -426,8 +439,8 @@ void for_width(int D, F f)
     else if (pieces <= 128) go(std::integral_constant<int, 64>{}, two, t256);
     else if (pieces <= 512) go(t256, two, t256);
     else if (pieces <= 1024) go(t512, two, t512);
-    else if (pieces <= 2048) go(t1024, two, t1024);
-    else go(t1024, four, t1024);
+    else if (E != E_F32 || pieces <= 2048) go(t1024, two, t1024);
+    else if constexpr (E == E_F32) go(t1024, four, t1024);
 }
 template <class F>
 hipError_t for_types(const NormParams &p, F f)
@@ -447,7 +460,7 @@ int rows_per_group(int D, int io)
     return r;
 }
 
-constexpr int64_t FWD_GROUPS = 1 << 20, BWD_GROUPS = 1024;
+constexpr int64_t FWD_GROUPS = 2048, BWD_GROUPS = 1024;
 
 }  // namespace
 
