@@ -654,9 +654,8 @@ int gdn2_qk_norm_rope_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  *           once
  *   layout  the last dimension contiguous, the other strides free and
  *           non-negative (0 too, for inputs); pointers aligned to their
- *           element (rows of an even number of elements that are aligned to
- *           two run faster); the rows of an output may not overlap. Weights,
- *           states and cu_seqlens dense.
+ *           element; the rows of an output may not overlap. Weights, states
+ *           and cu_seqlens dense and 16-byte aligned.
  *   sizes   T and N any number to 2^31 - 65537, D to 2^24 (the norm: 16384),
  *           within the 2^32 - 1 threads that one launch can hold
  *           (GDN2_ERR_SHAPE beyond)

@@ -126,7 +126,7 @@ __device__ __forceinline__ void activate(const ConvParams &p, float (&y)[VEC])
 // Channels of a lane and the part along the tokens of a workgroup.
 template <int VEC>
 struct Place {
-    uint32_t parts, part, c0, col;
+    uint32_t parts, part, base, col;
     bool on;
     int lane, wave;
     __device__ __forceinline__ explicit Place(const ConvParams &p)
@@ -136,9 +136,10 @@ struct Place {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         parts = gridDim.x / cols;
         part = id / cols;
-        c0 = (id % cols * 64 + lane) * VEC;
+        base = id % cols * (64 * VEC);
+        const uint32_t c0 = base + lane * VEC, last = p.D - VEC;
         on = c0 < (uint32_t)p.D;
-        col = on ? c0 : p.D - VEC;  // lanes past the last channel read it and store nothing
+        col = c0 < last ? c0 : last;  // lanes past the last channel read it and store nothing
     }
 };
 
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p)
     if (p.st)
         for_empty(b, at.part, at.parts, [&](int n) {
             win.begin(p, n, at.col);
-            if (at.on) win.end(p, n, at.c0);
+            if (at.on) win.end(p, n, at.col);
         });
     const int lo = (at.part * 4 + at.wave) * FWD_TOKENS, hi = lo + FWD_TOKENS < tokens ? lo + FWD_TOKENS : tokens;
     if (lo >= hi) return;
@@ -175,8 +176,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p)
             win.product(taps, x, y);
             win.push(x);
             activate<VEC>(p, y);
-            if (at.on) st_el<E, VEC>(p.out, (int64_t)(t + i) * p.so, at.c0, y);
-            if (s.lasts >> i & 1 && p.st && at.on) win.end(p, s.seq(i), at.c0);
+            if (at.on) st_el<E, VEC>(p.out, (int64_t)(t + i) * p.so, at.col, y);
+            if (s.lasts >> i & 1 && p.st && at.on) win.end(p, s.seq(i), at.col);
         }
     }
 }
@@ -223,7 +224,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p)
                 float x[VEC] = {};
                 const int64_t row = ((int64_t)n * (K - 1) + r) * p.D;
                 if (p.dst) ld_el<E, VEC>(p.dst, row, at.col, x);
-                if (at.on) st_el<E, VEC>(p.ds0, row, at.c0, x);
+                if (at.on) st_el<E, VEC>(p.ds0, row, at.col, x);
             }
         });
     float dw[K + 1][VEC] = {};
@@ -240,9 +241,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p)
         // Row t - (K - 1) + r, with its sum: stored where this wave owns it.
         auto emit = [&](int row, const float (&x)[VEC]) {
             if (row >= begin) {
-                if (row >= lo && row < hi && at.on) st_el<E, VEC>(p.dx, (int64_t)row * p.sdx, at.c0, x);
+                if (row >= lo && row < hi && at.on) st_el<E, VEC>(p.dx, (int64_t)row * p.sdx, at.col, x);
             } else if (begin >= lo && begin < hi && p.ds0 && at.on) {
-                st_el<E, VEC>(p.ds0, ((int64_t)n * (K - 1) + row - begin + K - 1) * p.D, at.c0, x);
+                st_el<E, VEC>(p.ds0, ((int64_t)n * (K - 1) + row - begin + K - 1) * p.D, at.col, x);
             }
         };
         const int stop = hi + K - 1 < tokens ? hi + K - 1 : tokens;
@@ -322,11 +323,12 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p)
 #pragma unroll
     for (int j = 0; j <= K; ++j)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) red[at.wave][j][at.lane * VEC + v] = dw[j][v];
+        for (int v = 0; v < VEC; ++v)
+            if (at.on) red[at.wave][j][at.col - at.base + v] = dw[j][v];
     __syncthreads();
     for (int i = threadIdx.x; i < (K + 1) * 64 * VEC; i += 256) {
         const int j = i / (64 * VEC), c = i % (64 * VEC);
-        const uint32_t col = at.c0 - at.lane * VEC + c;
+        const uint32_t col = at.base + c;
         if (col < (uint32_t)p.D)
             p.part[((int64_t)at.part * (K + 1) + j) * p.D + col] = red[0][j][c] + red[1][j][c] + (red[2][j][c] + red[3][j][c]);
     }

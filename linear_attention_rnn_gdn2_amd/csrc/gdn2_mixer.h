@@ -27,7 +27,7 @@ struct ScanParams {
     int32_t T, N, D;
     int32_t io, g_f32, cu64, h0_bf16, ht_bf16;
     int32_t scale;          // GDN2_SCAN_INPUT_*
-    int32_t vec2;           // rows may be read two elements at a time
+    int32_t vec2;           // two channels per lane (token by token, where states may be updated in place: no channel twice)
     int32_t groups;         // whole-sequence groups (0: two passes)
     // workspace: per tile (a range of 8 chunks forward, SCAN_TILE tokens
     // backward) and channel the sum of its g (infinity: a sequence begins in
@@ -106,6 +106,8 @@ struct NormParams {
 enum { NORM_X = 0, NORM_Z = 1, NORM_Y = 2, NORM_DY = 3, NORM_DZ = 4 };
 constexpr int NORM_MAX_D = 16384;
 
+// 16-byte pieces of a row of D elements.
+inline int32_t norm_pieces(int32_t D, int32_t io) { return io == E_F32 ? (D + 3) / 4 : (D + 7) / 8; }
 // Workgroups of the norm's backward (each leaves one row of partial sums).
 int32_t norm_bwd_groups(int64_t rows, int32_t D, int32_t io);
 hipError_t launch_norm_fwd(const NormParams &p, hipStream_t stream);

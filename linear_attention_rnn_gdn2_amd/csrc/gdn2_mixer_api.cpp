@@ -54,13 +54,6 @@ int check_io(const gdn2_tensor *t, const char *name, int32_t io, int ndim, const
 
 int64_t row_stride(const gdn2_tensor *t) { return t->shape[0] > 1 ? t->stride[0] : t->shape[t->ndim - 1]; }
 
-// Whether rows of D elements may be accessed two elements at a time.
-bool in_pairs(const gdn2_tensor *t)
-{
-    return !t || numel(t) == 0 ||
-           (row_stride(t) % 2 == 0 && reinterpret_cast<uintptr_t>(t->data) % (uintptr_t)(2 * elem_size(t->dtype)) == 0);
-}
-
 // The number of sequences, after x's own check.
 int check_packed(const gdn2_tensor *x, const gdn2_tensor *cu, int64_t *N_out)
 {
@@ -199,7 +192,7 @@ int validate(const Scan &a, Form form, void *ws, int64_t ws_bytes, ScanParams *p
     p->cu64 = a.cu && a.cu->dtype == GDN2_DTYPE_I64;
     p->h0_bf16 = a.h0 && a.h0->dtype == GDN2_DTYPE_BF16;
     p->scale = scale;
-    p->vec2 = D % 2 == 0 && in_pairs(a.x) && in_pairs(a.g) && in_pairs(a.w) && in_pairs(a.out);
+    p->vec2 = form == STEP ? D % 2 == 0 : D >= 2;
     p->chunk = gdn2::scan_chunk(T, D);
     p->tiles = (int32_t)(back ? gdn2::scan_tiles(T) : gdn2::scan_ranges(T, D));
     const ScanSpace space(T, D, back);
@@ -220,7 +213,6 @@ int validate(const Scan &a, Form form, void *ws, int64_t ws_bytes, ScanParams *p
         p->sdx = row_stride(a.dx);
         p->sdg = row_stride(a.dg);
         p->sdw = a.dw ? row_stride(a.dw) : 0;
-        p->vec2 = p->vec2 && in_pairs(a.dx) && in_pairs(a.dg) && in_pairs(a.dw);
     } else {
         p->out = a.out->data;
         p->so = row_stride(a.out);
@@ -303,7 +295,7 @@ int validate(const Conv &a, Form form, void *ws, int64_t ws_bytes, ConvParams *p
     p->w_f32 = wt == GDN2_DTYPE_F32;
     p->cu64 = a.cu && a.cu->dtype == GDN2_DTYPE_I64;
     p->silu = act == GDN2_CONV_SILU;
-    p->vec2 = D % 2 == 0 && in_pairs(a.x) && in_pairs(a.out);
+    p->vec2 = form == STEP ? D % 2 == 0 : D >= 2;
     if (back) {
         p->dout = a.out->data;
         p->sdo = row_stride(a.out);
@@ -313,7 +305,6 @@ int validate(const Conv &a, Form form, void *ws, int64_t ws_bytes, ConvParams *p
         p->ds0 = out_of(a.ds0);
         p->dweight = out_of(a.dweight);
         p->dbias = out_of(a.dbias);
-        p->vec2 = p->vec2 && in_pairs(a.dx);
         p->slice_tokens = gdn2::conv_slice_tokens(T, D);
         p->slices = gdn2::conv_slices(T, D);
         p->part = sums ? static_cast<float *>(ws) : nullptr;
@@ -569,7 +560,8 @@ int64_t gdn2_layer_norm_bwd_workspace(int64_t T, int32_t H, int32_t D)
 {
     if (T <= 0 || !fits_norm(T, H, D)) return 0;
     const int64_t a = gdn2::norm_bwd_groups(T * H, D, gdn2::E_BF16), b = gdn2::norm_bwd_groups(T * H, D, gdn2::E_F32);
-    return up256((a > b ? a : b) * 2 * D * 4);
+    const int64_t most = a > b ? a : b;  // the more that either width of an element takes
+    return up256(most * 2 * D * 4);
 }
 
 int gdn2_layer_norm_bwd(const gdn2_tensor *x, const gdn2_tensor *gate, const gdn2_tensor *weight, const gdn2_tensor *bias,

@@ -119,7 +119,7 @@ __global__ __launch_bounds__(512) void scan_tiles_kernel(ScanParams p)
             const float e[3] = {a[w].hi, a[w].lo, trio[w][2][lane * VEC + v]};
             c = join(e, c);
         }
-        const int64_t o = (int64_t)at.range * p.D + at.c0 + v;
+        const int64_t o = (int64_t)at.range * p.D + at.col + v;
         p.sums[o] = cut ? CUT : g;
         p.end[o] = h;
         p.back[o] = c;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
         for_empty(b, at.range, at.parts, [&](int n) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const int64_t o = (int64_t)n * p.D + at.c0 + v;
+                const int64_t o = (int64_t)n * p.D + at.col + v;
                 if (at.on) p.dh0[o] = p.dht ? p.dht[o] : 0.0f;
             }
         });
@@ -263,14 +263,14 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
         }
         if (!at.on) return;
         const int64_t t = s.t0 + i;
-        st_el<E, VEC>(p.dx, t * p.sdx, at.c0, dx);
-        if (p.dw) st_el<E, VEC>(p.dw, t * p.sdw, at.c0, dw);
-        st_el<G, VEC>(p.dg, t * p.sdg, at.c0, dg);
+        st_el<E, VEC>(p.dx, t * p.sdx, at.col, dx);
+        if (p.dw) st_el<E, VEC>(p.dw, t * p.sdw, at.col, dw);
+        st_el<G, VEC>(p.dg, t * p.sdg, at.col, dg);
     };
     auto first = [&](int i, float (&c)[VEC]) {
         if (!p.dh0 || !at.on) return;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) p.dh0[(int64_t)s.seq(i) * p.D + at.c0 + v] = c[v];
+        for (int v = 0; v < VEC; ++v) p.dh0[(int64_t)s.seq(i) * p.D + at.col + v] = c[v];
     };
     // the states before the tokens, then the gradients from the last token on
 #pragma unroll

@@ -135,7 +135,7 @@ struct Rows {
 // Where a workgroup works: channels of a lane, and its range of tokens.
 template <int VEC>
 struct Place {
-    uint32_t parts, range, c0, col;
+    uint32_t parts, range, col;
     bool on;
     int lane, wave;
     __device__ __forceinline__ explicit Place(const ScanParams &p, bool groups = false)
@@ -155,9 +155,9 @@ struct Place {
             range = id / cols;
             cb = id % cols;
         }
-        c0 = (cb * 64 + lane) * VEC;
+        const uint32_t c0 = (cb * 64 + lane) * VEC, last = p.D - VEC;
         on = c0 < (uint32_t)p.D;
-        col = on ? c0 : p.D - VEC;  // lanes past the last channel read it and store nothing
+        col = c0 < last ? c0 : last;  // lanes past the last channel read it and store nothing
     }
     // Workgroups that share a compute unit are 256 apart: every other 256 in reverse.
     __device__ static __forceinline__ uint32_t snake(uint32_t id, uint32_t count)

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(512) void scan_groups_kernel(ScanParams p)
         for_empty(b, at.range, at.parts, [&](int n) {
             float h[VEC];
             state_in<VEC>(p, n, at.col, h);
-            if (at.on) state_out<VEC>(p, n, at.c0, h);
+            if (at.on) state_out<VEC>(p, n, at.col, h);
         });
     int lo, hi;
     float h[VEC];
@@ -71,15 +71,15 @@ __global__ __launch_bounds__(512) void scan_groups_kernel(ScanParams p)
                 h[v] = join(e, h[v]);
             }
         auto store = [&](int i, float (&o)[VEC]) {
-            if (at.on) st_el<E, VEC>(p.out, (int64_t)(s.t0 + i) * p.so, at.c0, o);
+            if (at.on) st_el<E, VEC>(p.out, (int64_t)(s.t0 + i) * p.so, at.col, o);
         };
         if (plain) {
             walk<VEC, true>(p, s, at.col, a, u, enter, store);
-            if (s.lasts >> (R - 1) && p.ht && at.on) state_out<VEC>(p, s.seq(R - 1), at.c0, enter);
+            if (s.lasts >> (R - 1) && p.ht && at.on) state_out<VEC>(p, s.seq(R - 1), at.col, enter);
         } else {
             walk<VEC, false>(p, s, at.col, a, u, enter, [&](int i, float (&o)[VEC]) {
                 store(i, o);
-                if (s.lasts >> i & 1 && p.ht && at.on) state_out<VEC>(p, s.seq(i), at.c0, o);
+                if (s.lasts >> i & 1 && p.ht && at.on) state_out<VEC>(p, s.seq(i), at.col, o);
             });
         }
     }
@@ -138,8 +138,8 @@ __global__ __launch_bounds__(512) void scan_sums_kernel(ScanParams p)
         duo[wave][0][lane * VEC + v] = g;
         duo[wave][1][lane * VEC + v] = H[v];
         if (at.on) {
-            p.chunk_sums[chunk * p.D + at.c0 + v] = g;
-            p.chunk_end[chunk * p.D + at.c0 + v] = H[v];
+            p.chunk_sums[chunk * p.D + at.col + v] = g;
+            p.chunk_end[chunk * p.D + at.col + v] = H[v];
         }
     }
     __syncthreads();
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(512) void scan_sums_kernel(ScanParams p)
             any |= gw == CUT;
             g += gw;
         }
-        const int64_t o = (int64_t)at.range * p.D + at.c0 + v;
+        const int64_t o = (int64_t)at.range * p.D + at.col + v;
         p.sums[o] = any ? CUT : g;
         p.end[o] = h;
     }
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(512) void scan_chunks_kernel(ScanParams p)
         for_empty(b, at.range, at.parts, [&](int n) {
             float h[VEC];
             state_in<VEC>(p, n, at.col, h);
-            if (at.on) state_out<VEC>(p, n, at.c0, h);
+            if (at.on) state_out<VEC>(p, n, at.col, h);
         });
     const uint32_t range = at.parts - 1 - at.range;  // (from the end: the first pass read that last)
     const int64_t first = (int64_t)range * 8, lo64 = (first + wave) * p.chunk;
@@ -198,15 +198,15 @@ __global__ __launch_bounds__(512) void scan_chunks_kernel(ScanParams p)
     walk_chunk<E, G, VEC, KIND>(p, b, lo, hi, tokens, at.col,
                                 [&](const Slice<R> &s, const Decay(&a)[R][VEC], const float(&u)[R][VEC], const float(&)[VEC]) {
                                     auto store = [&](int i, float(&o)[VEC]) {
-                                        if (at.on) st_el<E, VEC>(p.out, (int64_t)(s.t0 + i) * p.so, at.c0, o);
+                                        if (at.on) st_el<E, VEC>(p.out, (int64_t)(s.t0 + i) * p.so, at.col, o);
                                     };
                                     if (s.cnt == R && !s.starts) {
                                         walk<VEC, true>(p, s, at.col, a, u, h, store);
-                                        if (s.lasts >> (R - 1) && p.ht && at.on) state_out<VEC>(p, s.seq(R - 1), at.c0, h);
+                                        if (s.lasts >> (R - 1) && p.ht && at.on) state_out<VEC>(p, s.seq(R - 1), at.col, h);
                                     } else {
                                         walk<VEC, false>(p, s, at.col, a, u, h, [&](int i, float(&o)[VEC]) {
                                             store(i, o);
-                                            if (s.lasts >> i & 1 && p.ht && at.on) state_out<VEC>(p, s.seq(i), at.c0, o);
+                                            if (s.lasts >> i & 1 && p.ht && at.on) state_out<VEC>(p, s.seq(i), at.col, o);
                                         });
                                     }
                                 });
