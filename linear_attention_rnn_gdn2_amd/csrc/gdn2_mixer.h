@@ -77,13 +77,14 @@ struct ConvParams {
     void *dweight, *dbias;  // the weight's type, or nullptr
     int64_t sdo, sdx;
     float *part;            // [slices][taps + 1][D]
-    int32_t slices, slice_tokens;
+    int32_t slices, slice_tokens;  // both directions
 };
 
-// Tokens that one wave of the convolution's gradient walks over, and the
-// workgroups along the tokens (each leaves one row of partial sums).
-int32_t conv_slice_tokens(int64_t T, int64_t D);
-int32_t conv_slices(int64_t T, int64_t D);
+// Tokens that one wave of the convolution (or of its gradients) walks over,
+// and the workgroups of four along the tokens (backward each leaves one row of
+// partial sums).
+int32_t conv_slice_tokens(int64_t T, int64_t D, bool bwd);
+int32_t conv_slices(int64_t T, int64_t D, bool bwd);
 hipError_t launch_conv_fwd(const ConvParams &p, hipStream_t stream);
 hipError_t launch_conv_step(const ConvParams &p, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvParams &p, hipStream_t stream);

@@ -37,7 +37,7 @@ bool fits_scan(int64_t T, int64_t N, int64_t D)
     const int64_t tiles = gdn2::scan_tiles(T), groups = gdn2::scan_groups(T, N, D);
     return fits_launch(tiles > groups ? tiles : groups, D, 64, 512);
 }
-bool fits_conv(int64_t T, int64_t N, int64_t D) { return fits_sizes(T, N, D) && fits_launch(T / 64 + 1, D, 64, 256); }
+bool fits_conv(int64_t T, int64_t N, int64_t D) { return fits_sizes(T, N, D) && fits_launch(T / 32 + 1, D, 64, 256); }
 bool fits_step(int64_t T, int64_t N, int64_t D) { return fits_sizes(T, N, D) && fits_launch(N, D, 256, 256); }
 
 // An io tensor: its type from bf16, float16, float32 (io 0) or the given one.
@@ -295,6 +295,8 @@ int validate(const Conv &a, Form form, void *ws, int64_t ws_bytes, ConvParams *p
     p->w_f32 = wt == GDN2_DTYPE_F32;
     p->cu64 = a.cu && a.cu->dtype == GDN2_DTYPE_I64;
     p->silu = act == GDN2_CONV_SILU;
+    p->slice_tokens = gdn2::conv_slice_tokens(T, D, back);
+    p->slices = gdn2::conv_slices(T, D, back);
     p->vec2 = form == STEP ? D % 2 == 0 : D >= 2;
     if (back) {
         p->dout = a.out->data;
@@ -305,8 +307,6 @@ int validate(const Conv &a, Form form, void *ws, int64_t ws_bytes, ConvParams *p
         p->ds0 = out_of(a.ds0);
         p->dweight = out_of(a.dweight);
         p->dbias = out_of(a.dbias);
-        p->slice_tokens = gdn2::conv_slice_tokens(T, D);
-        p->slices = gdn2::conv_slices(T, D);
         p->part = sums ? static_cast<float *>(ws) : nullptr;
     } else {
         p->out = a.out->data;
@@ -517,7 +517,7 @@ int gdn2_short_conv_recurrent_fwd_check(const gdn2_tensor *x, const gdn2_tensor 
 int64_t gdn2_short_conv_bwd_workspace(int64_t T, int32_t D, int32_t K)
 {
     if (T <= 0 || K < 2 || K > 4 || !fits_conv(T, 1, D)) return 0;
-    return up256(gdn2::conv_slices(T, D) * (int64_t)(K + 1) * D * 4);
+    return up256(gdn2::conv_slices(T, D, true) * (int64_t)(K + 1) * D * 4);
 }
 
 int gdn2_short_conv_bwd(const gdn2_tensor *x, const gdn2_tensor *weight, const gdn2_tensor *bias, const gdn2_tensor *initial_state,

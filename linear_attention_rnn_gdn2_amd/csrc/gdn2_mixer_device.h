@@ -7,7 +7,7 @@
 // whole arithmetic stays in one lane. With an odd number of channels the last
 // pair begins at the last but one, which two lanes then have: both compute and
 // store the same values. (Rows of 2047 channels one per lane: convolution of
-// 37,000 tokens 123 us, gradients 209; in pairs ODDCONV.)
+// 37,000 tokens 123 us, gradients 209; in pairs 76 and 133.)
 #pragma once
 
 #include <stdint.h>
