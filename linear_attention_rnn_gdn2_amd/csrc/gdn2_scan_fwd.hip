@@ -241,21 +241,33 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanParams p)
 
 }  // namespace
 
+// Tokens per wave: about 8192 waves of 64 channels (65,536 tokens of 1024
+// channels in 128: 163 us, in 64 164, in 32 174; 8192 tokens 43, 53, 53).
 int32_t scan_chunk(int64_t T, int64_t D)
 {
     const int64_t c = T * ((D + 63) / 64) / 8192 / R * R;
     return (int32_t)(c < R ? R : c > 256 ? 256 : c);
 }
 
+// Whole sequences take 2.2 us per 64 tokens of the longest, all side by side,
+// or the time of their bytes; two passes read x, w and g twice and take a
+// launch or two more. Measured, two passes / whole in us: one sequence of 8192
+// tokens, 4096 channels 124 / 284, two 240 / 287, three 372 / 292, four 484 /
+// 297; 8 and 12 of 1024 channels 270 / 290 and 387 / 294; one of 256 and of
+// 1024 tokens 22 / 14 and 22 / 39; five of 700, 2048 channels 53 / 32; 300 of
+// 20 to 200 310 / 178. The lengths are not known here, and taken as equal: one
+// sequence of 30,000 tokens among seven of 500 takes 1023, in two passes 607.
+// Groups: each sequence its own where there are few, the longest first;
+// else enough for the GPU, of 64 tokens and more (1000 sequences of 20 tokens,
+// 1024 channels: 32 groups 65, 128 83).
 int32_t scan_groups(int64_t T, int64_t N, int64_t D)
 {
-    const int64_t cols = (D + 63) / 64;
-    if (T <= 512) return 1;
-    if (N * cols >= 256) {
-        const int64_t s = (2048 + cols - 1) / cols;
-        return (int32_t)(s < N ? s : N);
-    }
-    return 0;
+    const double bytes = (double)T * (double)D, walk = 0.035 * (double)T / (double)N, move = bytes * 10 / 4.6e6;
+    if (8 + (walk > move ? walk : move) > 18 + bytes * 18 / 4.9e6) return 0;
+    if (N <= 64 && T / N >= 64) return (int32_t)N;
+    const int64_t cols = (D + 63) / 64, fill = (1024 + cols - 1) / cols, most = T / 64 < N ? T / 64 : N;
+    const int64_t s = fill < most ? fill : most;
+    return (int32_t)(s < 1 ? 1 : s);
 }
 
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t stream)

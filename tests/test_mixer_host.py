@@ -209,7 +209,7 @@ def test_workspaces(gdn2):
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     assert gdn2.linear_scan_fwd_workspace(1000, 1, 70) == 2 * up(16 * 70 * 4) + 2 * up(8 * 16 * 70 * 4)
     assert gdn2.linear_scan_bwd_workspace(1000, 1, 70) == 3 * up(16 * 70 * 4)
-    assert gdn2.linear_scan_fwd_workspace(512, 1, 70) == gdn2.linear_scan_bwd_workspace(64, 1, 70) == 0
+    assert gdn2.linear_scan_fwd_workspace(256, 1, 70) == gdn2.linear_scan_bwd_workspace(64, 1, 70) == 0
     assert gdn2.short_conv_bwd_workspace(1000, 70, 4) == up(-(-1000 // 64) * 5 * 70 * 4)
     assert gdn2.layer_norm_bwd_workspace(1000, 3, 64) >= 2 * 64 * 4
     for f in (gdn2.linear_scan_fwd_workspace, gdn2.linear_scan_bwd_workspace):

@@ -51,11 +51,14 @@ def test_forward_step_and_backward(lib, lens, D, io, gtype, kind, w, init, cu):
         close(n, g[n], r[n], DG_REL if n == "dg" else SCAN_REL)
 
 
-@pytest.mark.parametrize("N,D", [(300, 64), (40, 4096)])
-def test_groups_of_sequences(lib, N, D):
-    """Batches that run as groups: one group per sequence, and several sequences (empty ones among them) per group."""
-    lens = [(11 * i + 3) % 37 for i in range(N)]
-    assert sum(lens) > 512 and N * ((D + 63) // 64) >= 256 and lib.linear_scan_fwd_workspace(sum(lens), N, D) == 0
+@pytest.mark.parametrize("lens,D", [([(11 * i + 3) % 37 for i in range(300)], 64), ([(11 * i + 3) % 37 for i in range(40)], 4096),
+                                    ([70, 300, 0, 300, 1, 129], 4096), ([65 + 2 * (i * i % 40) for i in range(64)], 96),
+                                    ([65 + 2 * (i * i % 40) for i in range(65)], 96)])
+def test_groups_of_sequences(lib, lens, D):
+    """Batches that run whole: several sequences (empty ones among them) per group, and each its own group, by length, equal and
+    empty ones too, as many as one look-up holds and one more."""
+    N = len(lens)
+    assert lib.linear_scan_fwd_workspace(sum(lens), N, D) == 0
     d = scan_inputs(lens, D, seed=N, io=F32)
     out, end = lib.linear_scan_fwd(**gpu(d, SCAN_ARGS), input_scale="unit")
     ro, re = scan64(d, "unit")
@@ -63,12 +66,13 @@ def test_groups_of_sequences(lib, N, D):
     close("final_state", end, re, SCAN_REL)
 
 
-@pytest.mark.parametrize("lens", [[19200 + 17], [7000, 1, 0, 9000, 3000]])
-def test_many_tiles(lib, lens):
-    """More tiles than one pass of the join holds per wave."""
-    d = scan_inputs(lens, 3, seed=1, io=F32, lowest=0.1)
+@pytest.mark.parametrize("lens,D", [([19200 + 17], 3), ([7000, 1, 0, 9000, 3000], 3), ([1300, 900], 2100), ([2000], 33)])
+def test_two_passes(lib, lens, D):
+    """Few long sequences: chunks of 8 and more tokens per wave, more tiles than one pass of the join holds, both widths of the
+    join (up to 2048 channels and beyond)."""
+    d = scan_inputs(lens, D, seed=1, io=F32, lowest=0.1)
     a = gpu(d, SCAN_ARGS)
-    assert lib.linear_scan_fwd_workspace(sum(lens), len(lens), 3) > 0
+    assert lib.linear_scan_fwd_workspace(sum(lens), len(lens), D) > 0
     out, end = lib.linear_scan_fwd(**a, input_scale="convex")
     g = lib.linear_scan_bwd(a["x"], a["g"], a["w"], d["d_out"].cuda(), initial_state=a["initial_state"],
                             cu_seqlens=a["cu_seqlens"], d_final_state=d["d_final_state"].cuda(), input_scale="convex")
