@@ -663,7 +663,8 @@ int gdn2_qk_norm_rope_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  *           scalar-gated rule above. Tokens behind the last sequence are not
  *           read, and nothing of theirs is written. An infinity or NaN in a
  *           token reaches no other sequence and no other channel (norm: no
- *           other row, but for the weights' gradients).
+ *           other row; the weights' gradients are sums over all). A state
+ *           that is an infinity may be NaN in the tokens after it.
  * Outputs may not overlap inputs or each other (GDN2_ERR_ALIAS).
  */
 
@@ -680,14 +681,14 @@ int gdn2_qk_norm_rope_bwd_check(const gdn2_tensor *q, const gdn2_tensor *k,
  *   initial_state, final_state [N, D]  float32 or bf16 (NULL: zero / not
  *                     written)
  *
- * gdn2_linear_scan_fwd runs over long sequences: groups of whole sequences
- * side by side where that fills the GPU, else tiles of 64 tokens, joined by
- * the products of their decays (chosen from T, N and D alone; only the second
- * needs the workspace). gdn2_linear_scan_recurrent_fwd walks token by token
+ * gdn2_linear_scan_fwd runs over long sequences: whole ones side by side, or
+ * few long ones in two passes over chunks of tokens, joined by the products of
+ * their decays (chosen from T, N and D alone; only the second needs the
+ * workspace). gdn2_linear_scan_recurrent_fwd walks token by token
  * (decode, short spans), where final_state may be initial_state's own buffer
  * (same pointer and type) to update the state in place.
  *
- * Slow decays are held by e^g - 1, so that g near 0 keeps its precision:
+ * Slow decays are held in two parts, so that g near 0 keeps its precision:
  * float32 results are within about 1e-6 of a float64 evaluation, relative in
  * the 2-norm.
  */

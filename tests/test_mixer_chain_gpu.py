@@ -106,3 +106,48 @@ def test_convolution_delta_rule_gated_norm(lib):
         whole, _ = lib.short_conv_fwd(torch.cat([x[cu[n]:ends[n]], xt[n:n + 1]]), cw, cb, initial_state=cs[n:n + 1])
         assert torch.equal(whole[-1], t1[n])
     assert torch.equal(t2[:, -1], xt)
+
+
+def test_two_threads_on_two_streams(lib):
+    """Calls of two host threads at once, each on its own stream, give the bits of the calls alone."""
+    import threading
+
+    from tests.mixer_ref import norm_inputs, scan_inputs
+
+    def make(seed):
+        s, c, n = scan_inputs([700, 0, 300], 130, seed), conv_inputs([700, 0, 300], 130, 4, seed), norm_inputs(500, 2, 130, seed)
+        return [{k: t.cuda() if torch.is_tensor(t) else t for k, t in d.items()} for d in (s, c, n)]
+
+    def calls(ins):
+        s, c, n = ins
+        kw = dict(initial_state=s["initial_state"], cu_seqlens=s["cu_seqlens"])
+        out = list(lib.linear_scan_fwd(s["x"], s["g"], s["w"], input_scale="unit", **kw))
+        g = lib.linear_scan_bwd(s["x"], s["g"], s["w"], s["d_out"], d_final_state=s["d_final_state"], input_scale="unit", **kw)
+        out += [g[k] for k in sorted(g)]
+        g = lib.short_conv_bwd(c["x"], c["weight"], c["bias"], c["d_out"], initial_state=c["initial_state"], cu_seqlens=c["cu_seqlens"])
+        out += [g[k] for k in sorted(g)]
+        g = lib.layer_norm_bwd(n["x"], n["d_out"], n["weight"], n["bias"], gate=n["gate"])
+        return out + [g[k] for k in sorted(g)]
+
+    ins = [make(5), make(6)]
+    want = [calls(i) for i in ins]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[k] = calls(ins[k])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for k in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(got[k], want[k]))
