@@ -45,12 +45,23 @@ struct Taps {
     float w[K][VEC], b[VEC];
     __device__ __forceinline__ Taps(const ConvParams &p, uint32_t col)
     {
+        // the taps of neighbouring channels lie one after the other
+        auto get = [&](auto *raw, auto wide) {
+            __builtin_memcpy(raw, static_cast<decltype(raw)>(const_cast<void *>(p.weight)) + (int64_t)col * K, VEC * K * sizeof *raw);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
+            for (int v = 0; v < VEC; ++v)
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[j][v] = ld_either<E>(p.weight, p.w_f32, (int64_t)(col + v) * K + j);
-            b[v] = p.bias ? ld_either<E>(p.bias, p.w_f32, col + v) : 0.0f;
+                for (int j = 0; j < K; ++j) w[j][v] = wide(raw[v * K + j]);
+        };
+        if (E == E_F32 || p.w_f32) {
+            float raw[VEC * K];
+            get(raw, [](float x) { return x; });
+        } else if constexpr (E != E_F32) {
+            uint16_t raw[VEC * K];
+            get(raw, [](uint16_t x) { return el_f32<E>(x); });
         }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) b[v] = p.bias ? ld_either<E>(p.bias, p.w_f32, col + v) : 0.0f;
     }
 };
 

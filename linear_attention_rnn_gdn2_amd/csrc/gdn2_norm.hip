@@ -410,31 +410,34 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p)
     }
 }
 
-// The workgroups' partial sums joined in a fixed order: 64 columns of dw or
-// db per workgroup, 16 waves.
-template <int E>
+// The workgroups' partial sums joined in a fixed order: COLS columns of dw or
+// db per workgroup, 1024 / COLS threads per column, eight loads in flight. Few
+// columns need many threads each (1024 rows of partial sums of 128 columns: 64
+// columns per workgroup 7.4 us, 16 5.4), many read whole lines.
+template <int E, int COLS>
 __global__ __launch_bounds__(1024) void norm_dw_kernel(NormParams p)
 {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, which = blockIdx.y;
-    const int c0 = blockIdx.x * 64 + lane, col = c0 < p.D ? c0 : p.D - 1;
+    constexpr int RUNS = 1024 / COLS;
+    __shared__ float red[RUNS][COLS + 1];
+    const int c = threadIdx.x % COLS, run = threadIdx.x / COLS, which = blockIdx.y;
+    const int c0 = blockIdx.x * COLS + c, col = c0 < p.D ? c0 : p.D - 1;
     float s = 0.0f;
-    for (int g0 = wave; g0 < p.groups; g0 += 128) {
+    for (int g0 = run; g0 < p.groups; g0 += 8 * RUNS) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int g = g0 + 16 * i;
+            const int g = g0 + RUNS * i;
             x[i] = g < p.groups ? p.part[((int64_t)g * 2 + which) * p.D + col] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += x[i];
     }
-    red[wave][lane] = s;
+    red[run][c] = s;
     __syncthreads();
-    if (wave != 0 || c0 >= p.D) return;
+    if (run != 0 || c0 >= p.D) return;
     float x = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x += red[i][lane];
+#pragma unroll 16
+    for (int i = 0; i < RUNS; ++i) x += red[i][c];
     void *out = which ? p.db : p.dw;
     if (out) st_either<E>(out, which ? p.b_f32 : p.w_f32, c0, x);
 }
@@ -553,10 +556,14 @@ hipError_t launch_norm_bwd(const NormParams &p, hipStream_t stream)
         if (e != hipSuccess) return e;
     }
     if (!p.dw && !p.db) return hipSuccess;
-    const dim3 grid((unsigned)((p.D + 63) / 64), 2);
-    if (p.io == E_F32) hipLaunchKernelGGL((norm_dw_kernel<E_F32>), grid, dim3(1024), 0, stream, p);
-    else if (p.io == E_F16) hipLaunchKernelGGL((norm_dw_kernel<E_F16>), grid, dim3(1024), 0, stream, p);
-    else hipLaunchKernelGGL((norm_dw_kernel<E_BF16>), grid, dim3(1024), 0, stream, p);
+    auto sums = [&](auto e) {
+        const dim3 few((unsigned)((p.D + 15) / 16), 2), many((unsigned)((p.D + 63) / 64), 2);
+        if (p.D <= 1024) hipLaunchKernelGGL((norm_dw_kernel<e(), 16>), few, dim3(1024), 0, stream, p);
+        else hipLaunchKernelGGL((norm_dw_kernel<e(), 64>), many, dim3(1024), 0, stream, p);
+    };
+    if (p.io == E_F32) sums(std::integral_constant<int, E_F32>{});
+    else if (p.io == E_F16) sums(std::integral_constant<int, E_F16>{});
+    else sums(std::integral_constant<int, E_BF16>{});
     return hipGetLastError();
 }
 
