@@ -16,18 +16,16 @@ struct OutRows {
     {
         ld_rows<E, VEC, R>(p.dout, p.sdo, t0, hi, col, d);
     }
-    __device__ __forceinline__ void wide(const ScanParams &p, const Slice<R> &s, uint32_t col, float (&o)[R][VEC]) const
+    // Token i's (widened where it is used: registers decide the workgroups per compute unit).
+    template <bool PLAIN>
+    __device__ __forceinline__ void wide(const ScanParams &p, const Slice<R> &s, uint32_t col, int i, float (&o)[VEC]) const
     {
+        widen<E, VEC>(d[i], o);
+        if (!PLAIN && p.dht && s.lasts >> i & 1) {
+            const float *q = p.dht + (int64_t)s.seq(i) * p.D + col;
 #pragma unroll
-        for (int i = 0; i < R; ++i) widen<E, VEC>(d[i], o[i]);
-        if (!s.lasts || !p.dht) return;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (s.lasts >> i & 1) {
-                const float *q = p.dht + (int64_t)s.seq(i) * p.D + col;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) o[i][v] += q[v];
-            }
+            for (int v = 0; v < VEC; ++v) o[v] += q[v];
+        }
     }
 };
 
@@ -36,17 +34,18 @@ struct OutRows {
 // state's gradient at token i, g(i, c) what leaves a sequence's first token
 // (for its initial state). PLAIN: the tokens all exist, and no sequence
 // begins or ends among them.
-template <int VEC, bool PLAIN, class F, class G>
-__device__ __forceinline__ void walk_back(const Slice<R> &s, const Decay (&a)[R][VEC], const float (&d)[R][VEC], float (&after)[VEC],
-                                          F f, G g)
+template <int E, int VEC, bool PLAIN, class F, class G>
+__device__ __forceinline__ void walk_back(const ScanParams &p, const Slice<R> &s, uint32_t col, const Decay (&a)[R][VEC],
+                                          const OutRows<E, VEC> &outs, float (&after)[VEC], F f, G g)
 {
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
         if (!PLAIN && i >= s.cnt) continue;
-        float dh[VEC];
+        float d[VEC], dh[VEC];
+        outs.template wide<PLAIN>(p, s, col, i, d);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            dh[v] = !PLAIN && s.lasts >> i & 1 ? d[i][v] : d[i][v] + after[v];
+            dh[v] = !PLAIN && s.lasts >> i & 1 ? d[v] : d[v] + after[v];
             after[v] = times(a[i][v], dh[v]);
         }
         f(i, dh);
@@ -83,10 +82,8 @@ __global__ __launch_bounds__(512) void scan_tiles_kernel(ScanParams p)
         auto none = [](int, float (&)[VEC]) {};
         if (s.cnt == R && !s.starts) walk<VEC, true>(p, s, at.col, a, u, H, none);
         else walk<VEC, false>(p, s, at.col, a, u, H, none);
-        float d[R][VEC];
-        outs.wide(p, s, at.col, d);
-        if (s.cnt == R && !s.starts && !s.lasts) walk_back<VEC, true>(s, a, d, C, none, none);
-        else walk_back<VEC, false>(s, a, d, C, none, none);
+        if (s.cnt == R && !s.starts && !s.lasts) walk_back<E, VEC, true>(p, s, at.col, a, outs, C, none, none);
+        else walk_back<E, VEC, false>(p, s, at.col, a, outs, C, none, none);
         if (s.starts) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) sum[v] = CUT;
@@ -186,6 +183,10 @@ __global__ __launch_bounds__(1024) void scan_join_kernel(ScanParams p)
 
 // The gradients of a tile, from the state that enters it and the gradient
 // that reaches it from behind.
+// Registers decide: m, x, w and dout are made again from what was loaded where
+// they are needed (108 registers, two workgroups per compute unit: 36,962
+// tokens of 4096 channels 514 us, 5.3 TB/s; held from the first walk on 162
+// registers, 640 us).
 template <int E, int G, int VEC, int KIND>
 __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
 {
@@ -219,17 +220,16 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
     Slice<R> s;
     s.set(cur, lo + wave * R, hi, tokens);
     Decay a[R][VEC];
-    float u[R][VEC], d[R][VEC], before[R][VEC], sum[VEC], H[VEC] = {}, C[VEC] = {};
+    float u[R][VEC], before[R][VEC], sum[VEC], H[VEC] = {}, C[VEC] = {};
     rows.template inputs<KIND>(p, s.cnt, a, u, sum);
-    outs.wide(p, s, at.col, d);
     const bool plain = s.cnt == R && !s.starts && !s.lasts;
     auto none = [](int, float (&)[VEC]) {};
     if (plain) {
         walk<VEC, true>(p, s, at.col, a, u, H, none);
-        walk_back<VEC, true>(s, a, d, C, none, none);
+        walk_back<E, VEC, true>(p, s, at.col, a, outs, C, none, none);
     } else {
         walk<VEC, false>(p, s, at.col, a, u, H, none);
-        walk_back<VEC, false>(s, a, d, C, none, none);
+        walk_back<E, VEC, false>(p, s, at.col, a, outs, C, none, none);
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -240,6 +240,14 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
         quad[wave][3][lane * VEC + v] = C[v];
     }
     __syncthreads();
+    if constexpr (sizeof(rows.x[0]) >= 4) {
+        // (x and w widened again where the gradients need them)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            asm("" : "+v"(rows.x[i]));
+            asm("" : "+v"(rows.w[i]));
+        }
+    }
     // the waves before this one, then those behind it from the last on
     auto from = [&](int k, int which, float (&x)[VEC]) {
 #pragma unroll
@@ -256,10 +264,12 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
         rows.wide(p, i, gf, w, x);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float m = factor<KIND>(a[i][v]), mdh = m * dh[v];
+            Decay ai = a[i][v];
+            asm("" : "+v"(ai.hi));  // (keeps m from being held since u was made)
+            const float m = factor<KIND>(ai), mdh = m * dh[v];
             dx[v] = w[v] * mdh;
             dw[v] = x[v] * mdh;
-            dg[v] = dh[v] * fmaf(factor_slope<KIND>(a[i][v], m), w[v] * x[v], a[i][v].hi * before[i][v]);
+            dg[v] = dh[v] * fmaf(factor_slope<KIND>(ai, m), w[v] * x[v], ai.hi * before[i][v]);
         }
         if (!at.on) return;
         const int64_t t = s.t0 + i;
@@ -282,8 +292,8 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p)
             h[v] = advance(a[i][v], h[v], u[i][v]);
         }
     }
-    if (plain) walk_back<VEC, true>(s, a, d, after, gradients, first);
-    else walk_back<VEC, false>(s, a, d, after, gradients, first);
+    if (plain) walk_back<E, VEC, true>(p, s, at.col, a, outs, after, gradients, first);
+    else walk_back<E, VEC, false>(p, s, at.col, a, outs, after, gradients, first);
 }
 
 }  // namespace
