@@ -1,6 +1,5 @@
 // Device helpers of the recurrence's and the convolution's kernels: elements
-// of any type one or two at a time, and where a wave is in a packed batch.
-// Not part of the ABI.
+// of any type one or two at a time. Not part of the ABI.
 //
 // Lanes own channels: a wave reads 64 (or 128, two per lane) neighbouring
 // channels of a token at once and walks along the tokens, so that a channel's
@@ -17,8 +16,8 @@
 #include <hip/hip_runtime.h>
 
 #include "gdn2_device.h"
-#include "gdn2_index.h"
 #include "gdn2_mixer.h"
+#include "gdn2_packed.h"
 
 namespace gdn2 {
 namespace dev {
@@ -121,141 +120,6 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t id, uint32_t count)
     const uint32_t q = count / 8, r = count % 8, x = id % 8;
     return x * q + (x < r ? x : r) + id / 8;
 }
-
-// A packed batch. Every token and sequence index that is derived from
-// cu_seqlens stays in [0, T] and [0, N), whatever the array holds.
-struct Packed {
-    const void *cu;
-    int cu64, N, T;
-    __device__ __forceinline__ int entry(int i) const  // cu[i], in [0, T]
-    {
-        const int64_t v = cu_raw(cu, cu64, i);
-        return (int)(v < 0 ? 0 : v > T ? T : v);
-    }
-    __device__ __forceinline__ int tokens() const { return cu ? entry(N) : T; }  // behind the last sequence's end: none
-    // The first sequence start at or behind token t (the last sequence's end if there is none). Wave-uniform.
-    __device__ __forceinline__ int start_from(int t) const
-    {
-        if (!cu) return t > 0 ? T : 0;
-        const int lane = threadIdx.x & 63;
-        int lo = 0, hi = N;  // starts before lo lie before t, those from hi on do not
-        while (lo < hi) {
-            const int step = (hi - lo + 63) / 64, i = lo + lane * step;
-            const int c = __popcll(__ballot(i < hi && entry(i) < t));
-            if (c == 0) break;
-            const int last = lo + (c - 1) * step;
-            hi = step == 1 ? lo + c : last + step < hi ? last + step : hi;
-            lo = last + 1;
-        }
-        return entry(lo < N ? lo : N);
-    }
-    // The tokens of the sequence of a rank by length, the longest first (N <= 64).
-    __device__ __forceinline__ void by_length(int rank, int &lo, int &hi) const
-    {
-        const int lane = threadIdx.x & 63;
-        const int s = lane < N ? entry(lane) : 0, e = lane < N ? entry(lane + 1) : 0, len = e > s ? e - s : 0;
-        int before = 0;
-        for (int j = 0; j < N; ++j) {
-            const int l = __builtin_amdgcn_readlane(len, j);
-            before += l > len || (l == len && j < lane);
-        }
-        const int n = __builtin_ctzll(__ballot(lane < N && before == rank));
-        lo = __builtin_amdgcn_readlane(s, n);
-        hi = lo + __builtin_amdgcn_readlane(len, n);
-    }
-};
-
-// The sequence of each token, for tokens in (mostly) rising order. A lane
-// holds the end of one of 64 sequences; all members are wave-uniform else.
-struct Cursor {
-    Packed b;
-    int base = 0, from = 0, win = 0;
-    bool held = false;
-    int n_in = 0, b_in = 0, e_in = 0;  // tokens b_in .. e_in - 1 are known to lie in sequence n_in
-
-    __device__ __forceinline__ explicit Cursor(const Packed &p) : b(p) {}
-    __device__ __forceinline__ void seek(int t)
-    {
-        const int lane = threadIdx.x & 63;
-        int lo = 0, hi = b.N;  // sequences before lo end at or before t, those from hi on do not
-        while (hi - lo > 64) {
-            const int step = (hi - lo + 63) / 64, i = lo + lane * step;
-            const int c = __popcll(__ballot(i < hi && b.entry(i + 1) <= t));
-            if (c == 0) {
-                hi = lo;
-                break;
-            }
-            const int last = lo + (c - 1) * step;
-            hi = last + step < hi ? last + step : hi;
-            lo = last + 1;
-        }
-        base = lo;
-        from = t;
-        win = base + lane < b.N ? b.entry(base + lane + 1) : INT32_MAX;
-        held = true;
-    }
-    // The sequence that holds token t (t < tokens()).
-    __device__ __forceinline__ int at(int t)
-    {
-        if (!b.cu) return 0;
-        if (!held || t < from) seek(t);
-        int c = __popcll(__ballot(win <= t));
-        if (c == 64) {
-            seek(t);
-            c = __popcll(__ballot(win <= t));
-        }
-        return base + c < b.N ? base + c : b.N - 1;
-    }
-    // Remembers that token t lies in sequence n (n = at(t)).
-    __device__ __forceinline__ void inside(int n, int t)
-    {
-        n_in = n;
-        b_in = t;
-        e_in = n - base < 64 ? __builtin_amdgcn_readlane(win, n - base) : 0;
-    }
-};
-
-// R tokens of one wave: [t0, t0 + cnt), which of them begin and end their
-// sequences (bits), and the sequence of token i in lane i.
-template <int R>
-struct Slice {
-    int t0, cnt, nn;
-    uint32_t starts, lasts;
-
-    __device__ __forceinline__ void set(Cursor &cur, int t, int hi, int tokens)
-    {
-        t0 = t;
-        cnt = hi - t < 0 ? 0 : hi - t < R ? hi - t : R;
-        starts = lasts = 0;
-        nn = 0;
-        if (cnt == 0) return;
-        if (!cur.b.cu) {
-            starts = t == 0;
-            lasts = t + cnt == tokens ? 1u << (cnt - 1) : 0;
-            return;
-        }
-        if (t > cur.b_in && t + R < cur.e_in) {  // well inside a sequence
-            nn = cur.n_in;
-            return;
-        }
-        const int lane = threadIdx.x & 63;
-        int before = t > 0 ? cur.at(t - 1) : -1;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (i >= cnt) break;
-            const int n = cur.at(t + i);
-            if (n != before) {
-                starts |= 1u << i;
-                lasts |= i > 0 ? 1u << (i - 1) : 0;
-            }
-            nn = lane == i ? n : nn;
-            before = n;
-        }
-        if (t + cnt >= tokens || cur.at(t + cnt) != before) lasts |= 1u << (cnt - 1);
-        cur.inside(before, t + cnt - 1);
-    }
-    __device__ __forceinline__ int seq(int i) const { return __builtin_amdgcn_readlane(nn, i); }
-};
 
 // Calls f(n) for every empty sequence among a workgroup's share of all
 // sequences (share `part` of `parts`), each by one wave, with n wave-uniform.
