@@ -307,7 +307,7 @@ int validate(const Conv &a, Form form, void *ws, int64_t ws_bytes, ConvParams *p
         p->ds0 = out_of(a.ds0);
         p->dweight = out_of(a.dweight);
         p->dbias = out_of(a.dbias);
-        p->part = sums ? static_cast<float *>(ws) : nullptr;
+        p->part = sums && T > 0 ? static_cast<float *>(ws) : nullptr;  // (without tokens there is nothing to sum, and no room is asked for)
     } else {
         p->out = a.out->data;
         p->so = row_stride(a.out);
