@@ -134,22 +134,18 @@ __device__ __forceinline__ void activate(const ConvParams &p, float (&y)[VEC])
 }
 
 // Channels of a lane and the part along the tokens of a workgroup.
+__device__ __forceinline__ uint32_t work_id() { return xcd_run(blockIdx.x, gridDim.x); }
 template <int VEC>
-struct Place {
-    uint32_t parts, part, base, col;
-    bool on;
-    int lane, wave;
-    __device__ __forceinline__ explicit Place(const ConvParams &p)
+struct Place : Channels<VEC> {
+    uint32_t parts, part;
+    int wave;
+    __device__ __forceinline__ explicit Place(const ConvParams &p) : Place(p, (p.D + 64 * VEC - 1) / (64 * VEC)) {}
+
+private:
+    __device__ __forceinline__ Place(const ConvParams &p, uint32_t cols)
+        : Channels<VEC>(work_id() % cols, threadIdx.x & 63, p.D), parts(gridDim.x / cols), part(work_id() / cols),
+          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))
     {
-        const uint32_t cols = (p.D + 64 * VEC - 1) / (64 * VEC), id = xcd_run(blockIdx.x, gridDim.x);
-        lane = threadIdx.x & 63;
-        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        parts = gridDim.x / cols;
-        part = id / cols;
-        base = id % cols * (64 * VEC);
-        const uint32_t c0 = base + lane * VEC, last = p.D - VEC;
-        on = c0 < (uint32_t)p.D;
-        col = c0 < last ? c0 : last;  // lanes past the last channel read it and store nothing
     }
 };
 
@@ -368,10 +364,12 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p)
     }
     if (!p.part) return;
 #pragma unroll
-    for (int j = 0; j <= K; ++j)
+    for (int v = 0; v < VEC; ++v) {
+        const int c = at.place(v);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
-            if (at.on) red[at.wave][j][at.col - at.base + v] = dw[j][v];
+        for (int j = 0; j <= K; ++j)
+            if (c >= 0) red[at.wave][j][c] = dw[j][v];
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < (K + 1) * 64 * VEC; i += 256) {
         const int j = i / (64 * VEC), c = i % (64 * VEC);

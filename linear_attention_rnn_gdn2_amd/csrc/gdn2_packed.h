@@ -55,6 +55,24 @@ uint64_t vote(F f)
 }
 #endif
 
+// The channels of a lane: VEC neighbouring ones from `col` on, of the 64 VEC that
+// a wave takes from `base` on. With VEC = 2 and an odd D the last pair begins at
+// the last channel but one, which may lie in front of `base` (D = 64 VEC k + 1).
+template <int VEC>
+struct Channels {
+    uint32_t base, col;
+    bool on;  // (lanes past the last channel read the last pair and store nothing)
+    GDN2_WAVE Channels(uint32_t block, int lane, int D)
+    {
+        base = block * (64 * VEC);
+        const uint32_t c0 = base + lane * VEC, last = (uint32_t)D - VEC;
+        on = c0 < (uint32_t)D;
+        col = c0 < last ? c0 : last;
+    }
+    // The place of channel col + v among the wave's own 64 VEC, or -1: another workgroup's, or no lane's to store.
+    GDN2_WAVE int place(int v) const { return on && col + v >= base ? (int)(col + v - base) : -1; }
+};
+
 // A packed batch. Every token and sequence index that is derived from
 // cu_seqlens stays in [0, T] and [0, N), whatever the array holds.
 struct Packed {

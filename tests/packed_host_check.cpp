@@ -3,7 +3,7 @@
 // 8 tokens reports, for waves that walk as the kernels' do - consecutive tokens
 // (the convolution's slices, its gradients' with the rows behind, the
 // recurrence's chunks) and 8 of every 64 (the recurrence's groups) - and the
-// starts and ranks that divide a batch into groups.
+// starts and ranks that divide a batch into groups; and the channels of lanes.
 // Built with g++ by tests/test_packed_host.py; prints "ok" and exits 0.
 #include <stdint.h>
 #include <stdio.h>
@@ -108,8 +108,35 @@ static void check(const std::string &name, const std::vector<int> &lens, std::ve
     }
 }
 
+// Every channel has a place among its own workgroup's 64 VEC, and no lane one outside.
+template <int VEC>
+static void check_channels(int D)
+{
+    const int width = 64 * VEC, blocks = (D + width - 1) / width;
+    for (int b = 0; b < blocks; ++b) {
+        std::vector<char> seen(width, 0);
+        for (int lane = 0; lane < 64; ++lane) {
+            const Channels<VEC> at(b, lane, D);
+            bool ok = (int)at.col + VEC <= D && at.on == (b * width + lane * VEC < D);
+            for (int v = 0; v < VEC; ++v) {
+                const int c = at.place(v);
+                ok = ok && c < width && (c >= 0 ? at.on && b * width + c == (int)at.col + v : !at.on || (int)at.col + v < b * width);
+                if (c >= 0 && c < width) seen[c] = 1;
+            }
+            if (!ok && failures++ < 20) fprintf(stderr, "D = %d, block %d, lane %d of %d channels\n", D, b, lane, VEC);
+        }
+        for (int c = 0; c < width; ++c)
+            if (seen[c] != (b * width + c < D) && failures++ < 20) fprintf(stderr, "D = %d, block %d: channel %d\n", D, b, c);
+    }
+}
+
 int main()
 {
+    for (int D = 1; D <= 1100; ++D) {
+        check_channels<1>(D);
+        if (D >= 2) check_channels<2>(D);
+    }
+    for (int D : {2049, 4097, 8193, (1 << 20) + 1}) check_channels<2>(D);
     check("1000 of 64", std::vector<int>(1000, 64), {16});
     check("65 of 1 and one of 300", [] { std::vector<int> l(65, 1); l.push_back(300); return l; }());
     {

@@ -1,10 +1,12 @@
 """GPU tests of the convolution's, the recurrence's and the norm's calls at
-their edges: workspaces of calls that need none."""
+their edges: workspaces of calls that need none, widths whose last workgroup
+holds a single channel."""
 
 import pytest
 import torch
 
-from tests.mixer_ref import BF16, CONV_ARGS, F32, NORM_ARGS, SCAN_ARGS, conv_inputs, gpu, norm_inputs, scan_inputs
+from tests.mixer_ref import (BF16, CONV_ARGS, CONV_REL, F32, NORM_ARGS, SCAN_ARGS, SUM_REL, close, conv64, conv64_grads,
+                             conv_inputs, gpu, norm_inputs, scan_inputs)
 from tests.test_delta_gpu import lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +36,16 @@ def test_a_workspace_that_is_not_needed_stays(lib, size):
                             workspace=ws)
     torch.cuda.synchronize()
     assert (room == 7).all()
+
+
+@pytest.mark.parametrize("D", [127, 129, 385, 2049])
+@pytest.mark.parametrize("K", [2, 4])
+def test_weight_sums_of_a_last_single_channel(lib, D, K):
+    d = conv_inputs([70, 0, 3, 200], D, K, seed=D, io=F32)
+    a = gpu(d, CONV_ARGS)
+    out, _ = lib.short_conv_fwd(**a)
+    g = lib.short_conv_bwd(a["x"], a["weight"], a["bias"], d["d_out"].cuda(), initial_state=a["initial_state"],
+                           cu_seqlens=a["cu_seqlens"], d_final_state=d["d_final_state"].cuda())
+    close("out", out, conv64(d, "silu")[0], CONV_REL)
+    for n, r in conv64_grads(d, "silu").items():
+        close(n, g[n], r, SUM_REL if n in ("dweight", "dbias") else CONV_REL)

@@ -4,7 +4,8 @@ Compiles ``tests/packed_host_check.cpp`` against the library's
 ``gdn2_packed.h`` with g++ and runs it: sequence starts, ends and indices of
 every 8 tokens, as the recurrence's and the convolution's kernels look them
 up, against a plain list of boundaries, with more sequences than the 64 that a
-wave holds at once, empty ones among them (no GPU).
+wave holds at once, empty ones among them; and each lane's channels at every
+width (no GPU).
 """
 
 import os
