@@ -39,8 +39,10 @@ using namespace dev;
 constexpr int R = 8;  // tokens per wave and tile
 
 // e^g in two parts. For |g| < 1/4 the second is what the first leaves of 1 +
-// (e^g - 1), the bracket a polynomial (relative error 1e-7); a faster decay
-// forgets a state within four steps, and the first part's 2^-24 is enough.
+// (e^g - 1), the bracket g times a polynomial fitted to (e^g - 1) / g on [-1/4,
+// 0] (at most 4.7e-9 off there, relative; 1e-7 as float32 evaluates it); a
+// faster decay forgets a state within four steps, and the first part's 2^-24
+// is enough.
 struct Decay {
     float hi, lo;
 };

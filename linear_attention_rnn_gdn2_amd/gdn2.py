@@ -951,7 +951,8 @@ def _norm_rank(x):
 def layer_norm(x, weight=None, bias=None, gate=None, norm="layer", eps=None, out=None):
     """The norm of rows, on the current HIP stream: ``norm`` "layer" ((x -
     mean) / sqrt(var + eps), eps 1e-5) or "rms" (x / sqrt(mean x^2 + eps), eps
-    1e-6), times weight, plus bias, times gate sigmoid(gate).
+    1e-6), times weight, plus bias, times gate sigmoid(gate). ``eps`` None or
+    0: these values.
 
     x, gate, out [T, H, D] or [T, D] (D up to 16384): bf16, float16 or
     float32, strided rows accepted; weight, bias [D]: float32 or x's type.

@@ -88,3 +88,16 @@ def test_most_tokens_and_sequences(gdn2):
     for T, H, want in ((2 ** 31 - 1, 1, "OK"), (2 ** 31, 1, "SHAPE"), (2 ** 30, 1, "OK"), (2 ** 30, 2, "SHAPE")):
         rc = lib.gdn2_layer_norm_fwd_check(t(T, H, 1), None, None, None, t(T, H, 1, out=1), None)
         assert verdict(gdn2, rc) == want, gdn2.last_error()
+
+
+def test_interleaved_outputs_are_refused(gdn2):
+    """Overlaps go by whole spans: gradients that are views of one joint buffer, although no element is shared."""
+    both = torch.zeros(7, 3, 20, dtype=BF16)
+    x, gate, d_out = (torch.zeros(7, 3, 10, dtype=BF16) for _ in range(3))
+    for dx, dgate, want in ((both[..., :10], both[..., 10:], "ALIAS"), (both[..., :10], torch.zeros(7, 3, 10, dtype=BF16), "OK")):
+        rc = gdn2.check_layer_norm_bwd(x, d_out, gate=gate, grads={"dx": dx, "dgate": dgate})
+        assert verdict(gdn2, rc) == want
+
+
+def test_no_eps_is_the_default(gdn2):
+    assert gdn2._norm_options("rms", None).eps == gdn2._norm_options("rms", 0.0).eps == 0.0
